@@ -313,6 +313,157 @@ kda_status kda_tril_inv_packed_noalloc(const void *A, kda_dtype a_dtype, void *X
                                        const int32_t *chunk_indices, int64_t num_chunks,
                                        hipStream_t stream);
 
+/*
+ * The KDA layer around the solver and the decode step: a prompt's chunk map,
+ * its causal convolution, the gated delta rule over whole prompts (in chunks)
+ * and over a few tokens (recurrent), and the gated RMSNorm. They take the
+ * tensors of kda_decode_step with a token dimension in front and the same
+ * state pools, so a prompt run through them leaves the state and the
+ * convolution windows on which kda_decode_step continues.
+ *
+ * Requests: packed, rows of all requests concatenated along T with
+ * cu_seqlens (int32 [num_seqs + 1], device; as above: not validated, clamped
+ * to [0, total_tokens]; rows outside every request are neither read nor
+ * written), or dense, [B, T, ...], every batch row one request.
+ *
+ * Pools: `state` / `conv_state` may be NULL: every request then starts from
+ * zeros and nothing is kept (slot, init and num_slots are ignored). Else
+ *   slot  [num_seqs] int32 (device) or NULL: the pool slot of each request
+ *         (NULL: request n uses slot n, num_slots >= num_seqs). A slot < 0 or
+ *         >= num_slots marks a padding entry: its output rows are 0 and no
+ *         state is touched. Other entries must be distinct (entries sharing a
+ *         slot race).
+ *   init  [num_seqs] int32 (device) or NULL: 0 starts the request from zeros
+ *         (the slot is not read), anything else from its slot. NULL: every
+ *         request continues from its slot.
+ * The slot holds the request's new state after the call, also for a request
+ * of no tokens (its old state, or zeros where init is 0).
+ *
+ * Types: token tensors of in_dtype (out of out_dtype), decays, write
+ * strengths, taps, norm weights and pools FP32. All pointers 16-byte aligned
+ * but int32 arrays, beta and norm_w (4 bytes). Outputs must not overlap
+ * inputs or pools. As above, nothing is allocated, copied or synchronised.
+ */
+
+/*
+ * cu_seqlens and the chunk map of kda_tril_inv_packed, kda_kkt_packed and
+ * their chunk-size forms, from request lengths, in one launch (so a captured
+ * graph can rebuild them when the lengths change).
+ *   seq_lens      [num_seqs] int32; a negative length counts as 0, and the
+ *                 running sum stops at total_tokens (the rows of the tensors
+ *                 the map is for).
+ *   chunk_size    16, 32 or 64.
+ *   cu_seqlens    [num_seqs + 1] int32, written.
+ *   chunk_indices [max_chunks][2] int32, written in full: the (request, chunk)
+ *                 pairs in packed order, then (-1, -1), which the solvers skip
+ *                 (floor(total_tokens / chunk_size) + num_seqs entries always
+ *                 suffice; further chunks are dropped). NULL with
+ *                 max_chunks = 0 writes cu_seqlens alone.
+ *   num_chunks    [1] int32 (device) or NULL: the number of chunks, whether or
+ *                 not they fit.
+ */
+kda_status kda_chunk_map(const int32_t *seq_lens, int64_t num_seqs, int64_t total_tokens,
+                         int32_t chunk_size, int32_t *cu_seqlens, int32_t *chunk_indices,
+                         int64_t max_chunks, int32_t *num_chunks, hipStream_t stream);
+
+/*
+ * Causal convolution of a prompt, the first stage of kda_decode_step for many
+ * tokens: for p in (q, k, v), y_p[t] = silu(sum_{w<W} conv_w[p][w] x_p[t - W + 1 + w])
+ * with x before a request's first token taken from its window in conv_state;
+ *   q = y_q / sqrt(|y_q|^2 + eps_l2),  k = y_k / sqrt(|y_k|^2 + eps_l2),  v = y_v
+ * (the decode step's 1/sqrt(d) of q is the `scale` of the delta rule below),
+ * and the window is left holding the request's last W - 1 inputs.
+ *   qkv        [T, 3, H, d] of dtype ([B, T, 3, H, d] dense); q, k, v [T, H, d]
+ *              of dtype.
+ *   conv_w     [3, W, H, d];  conv_state [num_slots, 3, H, W - 1, d].
+ * head_dim 64 or 128, 2 <= conv_width <= 4, else KDA_ERR_UNSUPPORTED.
+ */
+kda_status kda_conv_prefill_packed(const void *qkv, kda_dtype dtype, const float *conv_w, void *q,
+                                   void *k, void *v, const int32_t *cu_seqlens, int64_t num_seqs,
+                                   int64_t total_tokens, int32_t H, int32_t head_dim,
+                                   int32_t conv_width, float *conv_state, const int32_t *slot,
+                                   const int32_t *init, int64_t num_slots, float eps_l2,
+                                   hipStream_t stream);
+
+kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float *conv_w, void *q,
+                                  void *k, void *v, int64_t B, int64_t T, int32_t H,
+                                  int32_t head_dim, int32_t conv_width, float *conv_state,
+                                  const int32_t *slot, const int32_t *init, int64_t num_slots,
+                                  float eps_l2, hipStream_t stream);
+
+/*
+ * The gated delta rule, the recurrence of kda_decode_step over a request's
+ * tokens, S the K x V FP32 state of a request and head:
+ *   S = diag(exp(g_t)) S;  u = beta_t (v_t - S^T k_t);  S = S + k_t u^T;
+ *   out_t = scale * S^T q_t
+ * kda_prefill_* runs it in chunks of tokens on the matrix cores (prompts),
+ * kda_recurrent_* token by token (decoding, drafted tokens, short
+ * extensions). Same arguments and, to rounding, the same results. (With
+ * L_ij = beta_i k_i . k_j e^{G_i - G_j} below the diagonal, a chunk's u solve
+ * (I + L) u = ...: the inverse that kda_kkt_tril_inv_* builds when it is given
+ * -beta.)
+ *   q, k   [T, Hk, K], v [T, H, V] of in_dtype; H a multiple of Hk: head h
+ *          reads query and key head h / (H / Hk). k is expected to be of about
+ *          unit length (kda_conv_prefill), as beta k k^T would else grow the
+ *          state.
+ *   g      [T, H, K] (gate_dim = K: one decay per key channel, as in KDA) or
+ *          [T, H] (gate_dim = 1: one per head), the log-decay of each token
+ *          (<= 0; not summed; -inf resets the channel).
+ *   beta   [T, H].
+ *   out    [T, H, V] of out_dtype.
+ *   state  [num_slots, H, K, V].
+ * K 64 or 128, V a multiple of 32 up to 256, num_seqs x H < 2^23, else
+ * KDA_ERR_UNSUPPORTED. Arithmetic is FP32 with FP32 state and sums; the
+ * chunked form's products take each FP32 factor as two bfloat16 parts (about
+ * 2^-17 of each term).
+ *
+ * workspace: kda_prefill_* uses the workspace, when one of at least
+ * kda_prefill_workspace_size bytes is given, to cut long requests into
+ * segments that run side by side; without it (NULL, 0) each request runs in
+ * one piece. 16-byte aligned; concurrent calls need different workspaces.
+ */
+kda_status kda_prefill_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t K,
+                                      int32_t V, size_t *bytes);
+
+kda_status kda_prefill_packed(const void *q, const void *k, const void *v, kda_dtype in_dtype,
+                              const float *g, const float *beta, void *out, kda_dtype out_dtype,
+                              const int32_t *cu_seqlens, int64_t num_seqs, int64_t total_tokens,
+                              int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t gate_dim,
+                              float *state, const int32_t *slot, const int32_t *init,
+                              int64_t num_slots, float scale, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+kda_status kda_prefill_dense(const void *q, const void *k, const void *v, kda_dtype in_dtype,
+                             const float *g, const float *beta, void *out, kda_dtype out_dtype,
+                             int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+                             int32_t gate_dim, float *state, const int32_t *slot,
+                             const int32_t *init, int64_t num_slots, float scale, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+kda_status kda_recurrent_packed(const void *q, const void *k, const void *v, kda_dtype in_dtype,
+                                const float *g, const float *beta, void *out, kda_dtype out_dtype,
+                                const int32_t *cu_seqlens, int64_t num_seqs, int64_t total_tokens,
+                                int32_t H, int32_t Hk, int32_t K, int32_t V, int32_t gate_dim,
+                                float *state, const int32_t *slot, const int32_t *init,
+                                int64_t num_slots, float scale, hipStream_t stream);
+
+kda_status kda_recurrent_dense(const void *q, const void *k, const void *v, kda_dtype in_dtype,
+                               const float *g, const float *beta, void *out, kda_dtype out_dtype,
+                               int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+                               int32_t gate_dim, float *state, const int32_t *slot,
+                               const int32_t *init, int64_t num_slots, float scale,
+                               hipStream_t stream);
+
+/*
+ * Gated RMSNorm of `rows` x H vectors, the decode step's last stage:
+ *   out = o / sqrt(mean(o^2) + eps_norm) * norm_w * sigmoid(z)
+ * o, z [rows, H, d] of in_dtype, out of out_dtype, norm_w [d]. head_dim 64 or
+ * 128, else KDA_ERR_UNSUPPORTED. out may be o itself when the types are equal.
+ */
+kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, const float *norm_w,
+                          void *out, kda_dtype out_dtype, int64_t rows, int32_t H,
+                          int32_t head_dim, float eps_norm, hipStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status s);
 

@@ -406,3 +406,13 @@ def prepare_decode(qkv, z, g, beta, norm_w, conv_w, slot, state, conv_state, out
                      _decode_args(qkv, z, g, beta, norm_w, conv_w, slot, state, conv_state, out,
                                   eps_l2, eps_norm, stream))
 
+
+
+# ---- the layer's calls around the solver and the decode step ----------------
+
+from . import layer as _layer  # noqa: E402  (it uses the definitions above)
+from .layer import (chunk_map, conv_prefill, gated_norm, kda_chunk_map,  # noqa: E402,F401
+                    kda_conv_prefill, kda_gated_norm, kda_prefill, kda_prefill_workspace_size,
+                    kda_recurrent, prefill, prepare_prefill, prepare_recurrent, recurrent)
+
+EXPORTED += _layer.EXPORTED

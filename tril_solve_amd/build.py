@@ -19,7 +19,8 @@ PROBE_LIB = os.path.join(HERE, "libkda_bench_probe.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cpp", "plan.cpp", "launch_common.cpp", "tril_fused.hip", "tril_split.hip",
-           "tril_small.hip", "tril_kkt.hip", "kda_decode.hip"]
+           "tril_small.hip", "tril_kkt.hip", "kda_decode.hip", "layer_api.cpp", "kda_map.hip",
+           "kda_conv.hip", "kda_prefill.hip", "kda_recurrent.hip", "kda_norm.hip"]
 PROBE_SOURCES = ["bench_probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -62,7 +63,7 @@ def build(verbose: bool = False) -> str:
     copy probe. Returns the solver library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = SOURCES + PROBE_SOURCES
-    with ThreadPoolExecutor(min(5, len(srcs))) as ex:
+    with ThreadPoolExecutor(min(8, len(srcs))) as ex:
         objs = dict(zip(srcs, ex.map(_compile, srcs)))
     _link([objs[s] for s in SOURCES], LIB)
     _link([objs[s] for s in PROBE_SOURCES], PROBE_LIB)

@@ -1,0 +1,118 @@
+// Chunk maps from request lengths, on the GPU: cu_seqlens (the running sum of
+// the lengths) and the (request, chunk-within-request) pair of every chunk in
+// packed order, so a serving loop can rebuild both inside a captured graph.
+//
+// Bound by latency: a few kilobytes each way. One launch; every workgroup
+// scans all lengths itself (4 per thread and tile, in L2 after the first) and
+// writes its own range of map entries, each found by a binary search in the
+// tile's running chunk counts in LDS, so a request of thousands of chunks is
+// as balanced as many short ones and no second pass over a global scan is
+// needed.
+#include <hip/hip_runtime.h>
+
+#include "layer_device.h"
+
+namespace kda {
+
+constexpr int kMapThreads = 1024;
+constexpr int kMapPer = 4;                          // requests per thread and tile
+constexpr int kMapTile = kMapThreads * kMapPer;     // requests per tile
+constexpr int kMapSlots = 2048;                     // map entries a workgroup aims at
+
+// Running sum over the workgroup of one value per thread with additions that
+// saturate at `cap` (both operands are at most 2^31 - 1, so a sum never
+// wraps). Returns the sum of the threads before this one; *all: of all.
+__device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t cap, uint32_t *wsum,
+                                                    uint32_t *all) {
+    const int l = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+    uint32_t x = v;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t y = __shfl_up(x, d);
+        if (l >= d) x = min(x + y, cap);
+    }
+    __syncthreads();  // the previous scan's reads of wsum are done
+    if (l == kWave - 1) wsum[w] = x;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kMapThreads / kWave; ++i) {
+        if (i == w) before = total;
+        total = min(total + wsum[i], cap);
+    }
+    *all = total;
+    uint32_t up = __shfl_up(x, 1);
+    if (l == 0) up = 0;
+    return min(before + up, cap);
+}
+
+__global__ __launch_bounds__(kMapThreads) void kda_chunk_map_kernel(MapProblem p) {
+    __shared__ uint32_t wsum[kMapThreads / kWave];
+    __shared__ uint32_t ends[kMapTile];  // running chunk count after each request of the tile
+    const int tid = threadIdx.x;
+    const uint32_t cap = (uint32_t)p.total_tokens, none = 0x7FFFFFFFu;
+    // this workgroup's map entries
+    const long per = ((long)p.max_chunks + gridDim.x - 1) / gridDim.x;
+    const long lo = per * blockIdx.x, hi = min(lo + per, (long)p.max_chunks);
+    uint32_t tokens = 0, chunks = 0;  // before the tile
+    for (long base = 0; base < p.num_seqs; base += kMapTile) {
+        uint32_t len[kMapPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kMapPer; ++i) {
+            const long r = base + tid * kMapPer + i;
+            const int v = r < p.num_seqs ? p.seq_lens[r] : 0;
+            len[i] = min((uint32_t)max(v, 0), cap);
+            sum = min(sum + len[i], cap);
+        }
+        uint32_t all;
+        uint32_t at = min(tokens + block_excl_scan(sum, cap, wsum, &all), cap);
+        tokens = min(tokens + all, cap);
+        uint32_t cnt[kMapPer], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kMapPer; ++i) {
+            const uint32_t end = min(at + len[i], cap);
+            cnt[i] = (end - at + p.chunk - 1) / p.chunk;
+            mine += cnt[i];
+            at = end;
+            const long r = base + tid * kMapPer + i;
+            if (blockIdx.x == 0 && r < p.num_seqs) p.cu[r + 1] = (int32_t)end;
+        }
+        uint32_t tile;
+        uint32_t run = block_excl_scan(mine, none, wsum, &tile);
+#pragma unroll
+        for (int i = 0; i < kMapPer; ++i) ends[tid * kMapPer + i] = run += cnt[i];
+        __syncthreads();
+        // map entries of this workgroup that fall into the tile
+        const long first = max(lo, (long)chunks), last = min(hi, (long)chunks + tile);
+        for (long s = first + tid; s < last; s += kMapThreads) {
+            const uint32_t want = (uint32_t)(s - chunks);
+            int a = 0, b = kMapTile - 1;  // the first request whose running count passes `want`
+            while (a < b) {
+                const int m = (a + b) / 2;
+                if (ends[m] > want)
+                    b = m;
+                else
+                    a = m + 1;
+            }
+            const uint32_t start = a ? ends[a - 1] : 0;
+            reinterpret_cast<int2 *>(p.map)[s] = make_int2((int)(base + a), (int)(want - start));
+        }
+        chunks += tile;
+        __syncthreads();  // `ends` is rewritten by the next tile
+    }
+    for (long s = max(lo, (long)chunks) + tid; s < hi; s += kMapThreads)
+        reinterpret_cast<int2 *>(p.map)[s] = make_int2(-1, -1);  // past the last chunk
+    if (blockIdx.x == 0 && tid == 0) {
+        p.cu[0] = 0;
+        if (p.count) *p.count = (int32_t)chunks;
+    }
+}
+
+hipError_t launch_map(const MapProblem &p, hipStream_t stream) {
+    long grid = ((long)p.max_chunks + kMapSlots - 1) / kMapSlots;
+    grid = grid < 1 ? 1 : grid > 256 ? 256 : grid;
+    hipLaunchKernelGGL(kda_chunk_map_kernel, dim3((unsigned)grid), dim3(kMapThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace kda
