@@ -1,13 +1,12 @@
-// Gated delta rule over whole prompts for gfx950.
-#include <hip/hip_runtime.h>
-
-#include "kda_layer.h"
+// Launch of the gated delta rule over whole prompts.
+#include "kda_prefill.h"
 
 namespace kda {
 
-// Token by token, as the recurrent form does.
 hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) {
-    return launch_recurrent(p, in_dt, stream);
+    return in_dt == 0   ? launch_prefill_f32(p, stream)
+           : in_dt == 1 ? launch_prefill_bf16(p, stream)
+                        : launch_prefill_f16(p, stream);
 }
 
 }  // namespace kda

@@ -1,0 +1,11 @@
+// The prefill kernels for bf16 inputs (a file per input type: they compile side
+// by side).
+#include "kda_prefill.h"
+
+namespace kda {
+
+hipError_t launch_prefill_bf16(const DeltaProblem &p, hipStream_t stream) {
+    return launch_prefill_of<BF16>(p, stream);
+}
+
+}  // namespace kda
