@@ -25,19 +25,25 @@
 // is 6 or 3 of 16 cycles. Sums, the state and the decays stay FP32.
 //
 //   * Each wavefront owns 32 value columns of the state in registers
-//     (accumulator layout). With the reduction index of a 16 x 16 x 32
-//     product permuted as 8 g + 4 b + s <-> 16 b + 4 g + s, two accumulator
-//     tiles are the B operand of the next product as they stand, so the chain
-//     k S -> U -> O, S stays inside the wavefront's registers.
+//     (accumulator layout). Two accumulator tiles b = 0, 1 are the B operand of
+//     the next product as they stand when its reduction index 8 g + 4 b + s
+//     means row 4 g + s of tile b: tokens 16 b + 4 g + s of U, and, for the
+//     state, tile 2 i + b holding channels 32 i + 8 g + 4 b + s, so that keys
+//     and queries keep their order. The chain k S -> U -> O, S thus stays
+//     inside the wavefront's registers.
 //   * The A operands (decayed keys and queries, the inverse of I + L, P) are
 //     the same for all columns: the wavefronts prepare them together in LDS,
 //     8 tokens each.
-//   * Decays enter as factors relative to the middle of each 16-token block,
-//     e^{G_i - G_j} = e^{G_i - m} e^{m - G_j}, so that no factor leaves FP32's
-//     range while the decay of 8 adjacent tokens stays within e^{+-64}. A
-//     chunk that has a steeper channel (or a gate that is not finite) forms
-//     its L and P from running products of the decays instead, every factor
-//     of which is the decay between two tokens.
+//   * Decays enter as factors relative to the chunk's middle, G_16 =: m:
+//     e^{G_i - G_j} = e^{G_i - m} e^{m - G_j}, and with S' = e^m S
+//       (k e^G) S = (k e^{G - m}) S',  (q e^G) S likewise,
+//       e^{G_32} S + (k e^{G_32 - G})^T U = e^{G_32 - m} (S' + (k e^{m - G})^T U),
+//     so three operands serve all six products, and the last one is the keys
+//     of L and P read transposed from LDS. No factor leaves FP32's range while
+//     the decay of 16 adjacent tokens stays within e^{-64}. A chunk that has a
+//     steeper channel (or a gate that is not finite) forms its L and P from
+//     running products of the decays instead, every factor of which is the
+//     decay between two tokens, and takes the left-hand forms above.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,7 +61,7 @@ constexpr float kSteep = 64.0f * kLog2E;  // in powers of two
 
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
-// Position of index x (0..31) of a 32-long reduction in operand order.
+// Position of token x (0..31) in an operand reduced over tokens.
 __device__ __forceinline__ constexpr int operand_pos(int x) {
     return 8 * ((x & 15) >> 2) + 4 * (x >> 4) + (x & 3);
 }
@@ -127,9 +133,47 @@ __device__ __forceinline__ f4 mul(const Operand<NA> &a, const Operand<NB> &b, f4
     return mfma(a.p[0], b.p[0], c);
 }
 
-// A lane's CPL adjacent channels of one token as loaded (no conversion).
+// Shapes the schedule of the code around it: N times one matrix instruction
+// followed by up to V vector instructions, which run in its shadow.
+template <int N, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+        __builtin_amdgcn_sched_group_barrier(0x002, V, 0);  // vector
+    }
+}
+
+// Two registers of 16-bit values, transposed among 16 lanes (see its use).
+__device__ __forceinline__ w2 read_transposed(const char *p) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4 *Lds;
+    return __builtin_bit_cast(w2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                      (Lds)(__attribute__((address_space(3))) char *)p));
+}
+
+// N adjacent elements of one row as loaded (no conversion).
 template <class E, int N>
 struct RawC;
+template <class E>
+struct RawC<E, 4> {
+    w2 w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
+        w = __builtin_bit_cast(w2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    }
+    __device__ __forceinline__ f4 all() const {
+        return f4{Elem<E>::widen(w[0] & 0xFFFFu), Elem<E>::widen(w[0] >> 16),
+                  Elem<E>::widen(w[1] & 0xFFFFu), Elem<E>::widen(w[1] >> 16)};
+    }
+};
+template <>
+struct RawC<F32, 4> {
+    f4 w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
+        w = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    }
+    __device__ __forceinline__ f4 all() const { return w; }
+};
 template <class E>
 struct RawC<E, 2> {
     uint32_t w;
@@ -140,35 +184,44 @@ struct RawC<E, 2> {
         return Elem<E>::widen(i ? w >> 16 : w & 0xFFFFu);
     }
 };
-template <class E>
-struct RawC<E, 1> {
-    uint32_t w;
-    __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
-        w = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
-    }
-    __device__ __forceinline__ float at(int) const { return Elem<E>::widen(w); }
-};
 template <>
 struct RawC<F32, 2> {
     f2 w;
     __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
         w = __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
     }
-    __device__ __forceinline__ void load_same(Rsrc r, uint32_t off) {
-        const float x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-        w = f2{x, x};
-    }
     __device__ __forceinline__ float at(int i) const { return w[i]; }
 };
-template <>
-struct RawC<F32, 1> {
-    float w;
-    __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
-        w = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+
+__device__ __forceinline__ f4 exp2(f4 x) {
+    return f4{__builtin_amdgcn_exp2f(x[0]), __builtin_amdgcn_exp2f(x[1]),
+              __builtin_amdgcn_exp2f(x[2]), __builtin_amdgcn_exp2f(x[3])};
+}
+__device__ __forceinline__ f4 rcp(f4 x) {
+    return f4{__builtin_amdgcn_rcpf(x[0]), __builtin_amdgcn_rcpf(x[1]),
+              __builtin_amdgcn_rcpf(x[2]), __builtin_amdgcn_rcpf(x[3])};
+}
+// out[g] = x of the lane at the same place in group g, G groups of 64 / G lanes.
+template <int G>
+__device__ __forceinline__ void gather_groups(f4 x, f4 (&out)[G]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a = x[e], b = x[e];
+        lane_swap32(a, b);
+        if constexpr (G == 2) {
+            out[0][e] = a;
+            out[1][e] = b;
+        } else {
+            float a1 = a, b1 = b;
+            lane_swap16(a, a1);
+            lane_swap16(b, b1);
+            out[0][e] = a;
+            out[1][e] = a1;
+            out[2][e] = b;
+            out[3][e] = b1;
+        }
     }
-    __device__ __forceinline__ void load_same(Rsrc r, uint32_t off) { load(r, off); }
-    __device__ __forceinline__ float at(int) const { return w; }
-};
+}
 
 // LDS layout (bytes). Operands lie in rows of 2 K bytes (reduced over
 // channels) or 64 bytes (over tokens); the 16-byte pieces of a row are
@@ -178,29 +231,27 @@ struct RawC<F32, 1> {
 template <int K, int OUT>
 struct PreLds {
     static constexpr int RS = 2 * K, TS = 2 * kPreC;
-    static constexpr int R32 = kPreC * RS, R16 = R32 / 2, T32 = kPreC * TS, KTP = K * TS;
-    static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of P's factors, P and q e^G
-    // first half of a chunk: keys, queries (relative to their block's middle)
-    // against keys; block 0's keys relative to block 1's middle
-    static constexpr int KR = 0, QR = KR + 2 * R32, KL = QR + NQ * R32, KO = KL + NQ * R32;
-    static constexpr int kFirst = KO + NQ * R16;
-    // the steep form: keys, queries, decays FP32, then L / beta and P
+    static constexpr int kPatch = 20;  // floats between rows of a block of L
+    static constexpr int R32 = kPreC * RS, T32 = kPreC * TS;
+    static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of queries, P and S'
+    // keys and queries times e^{G - m} (steep: e^G), keys times e^{m - G}
+    // (steep: e^{G_32 - G})
+    static constexpr int KR = 0, QR = KR + 2 * R32, KL = QR + NQ * R32;
+    static constexpr int kOperands = KL + 3 * R32;
+    // a steep chunk's first half: keys, queries, decays FP32, then L / beta and P
     static constexpr int SK = 0, SQ = SK + kPreC * K * 4, SA = SQ + kPreC * K * 4;
     static constexpr int SM = SA + kPreC * K * 4, SP = SM + kPreC * kPreC * 4;
     static constexpr int kSteepBytes = SP + kPreC * kPreC * 4;
-    // second half: k e^G, q e^G, (k e^{G_32 - G})^T
-    static constexpr int KS = 0, QS = KS + 2 * R32, KT = QS + NQ * R32;
-    static constexpr int kSecond = KT + 3 * KTP;
-    static constexpr int kMax1 = kFirst > kSteepBytes ? kFirst : kSteepBytes;
-    static constexpr int kShared = kMax1 > kSecond ? kMax1 : kSecond;
-    // kept apart: diagonal blocks of the inverse and -L_10; P
-    static constexpr int TM = kShared, PM = TM + 3 * T32;
+    // diagonal blocks of the inverse and -L_10; P
+    static constexpr int TM = kOperands > kSteepBytes ? kOperands : kSteepBytes;
+    static constexpr int PM = TM + 3 * T32;
     static constexpr int PATCH = PM + NQ * T32;
-    static constexpr int TOT = PATCH + 2 * 16 * 17 * 4;
-    static constexpr int DEC = TOT + kPreWaves * K * 4;
-    static constexpr int BETA = DEC + K * 4;
-    static constexpr int FLAG = BETA + 2 * kPreC * 4;
-    static constexpr int kBytes = FLAG + kPreWaves * 4;
+    static constexpr int TOT = PATCH + 2 * 16 * kPatch * 4;
+    // per channel: what S' is of S and the new S of S' + ... (steep: 1), and
+    // for a steep chunk e^{G_32}
+    static constexpr int EM = TOT + kPreWaves * K * 4, EG = EM + K * 4, EF = EG + K * 4;
+    static constexpr int BETA = EF + K * 4;
+    static constexpr int kBytes = BETA + 2 * kPreC * 4;
     // exchange of 16-byte pieces
     static __device__ __forceinline__ int swz_row(int row) {
         return (K == 128 ? row & 15 : (row >> 1) & 7) << 4;
@@ -208,19 +259,131 @@ struct PreLds {
     static __device__ __forceinline__ int swz_tok(int row) { return ((row >> 2) & 3) << 4; }
 };
 
-template <int I, int N>
-__device__ __forceinline__ void substitute(const float (&arow)[16], float (&x)[16], int c) {
-    if constexpr (I < N) {
-        subst_row<I>(arow, x, c);
-        substitute<I + 1, N>(arow, x, c);
-    }
+// x = (I + L)^-1, one lane per column of a 16 x 16 block in every 16-lane row:
+// lane i of the row holds row i of -L in a (0 on and above the diagonal), x
+// starts as the identity's column, and once x_j is final every x_i below takes
+// a_ij x_j, with a_ij read from lane i by a DPP broadcast inside the
+// multiply-add (the compiler spends a move on each). The updates of one j do
+// not depend on each other. The DPP source must not have been written by the
+// two instructions before: s_nop 1.
+#define KDA_FMAC(i, o, a, x) \
+    "v_fmac_f32_dpp %" #o ", %" #a ", %" #x " row_newbcast:" #i " row_mask:0xf bank_mask:0xf\n\t"
+__device__ __forceinline__ void substitute(const float (&a)[16], float (&x)[16]) {
+    asm("s_nop 1\n\t"
+        KDA_FMAC(1, 0, 15, 16) KDA_FMAC(2, 1, 15, 16) KDA_FMAC(3, 2, 15, 16)
+        KDA_FMAC(4, 3, 15, 16) KDA_FMAC(5, 4, 15, 16) KDA_FMAC(6, 5, 15, 16)
+        KDA_FMAC(7, 6, 15, 16) KDA_FMAC(8, 7, 15, 16) KDA_FMAC(9, 8, 15, 16)
+        KDA_FMAC(10, 9, 15, 16) KDA_FMAC(11, 10, 15, 16) KDA_FMAC(12, 11, 15, 16)
+        KDA_FMAC(13, 12, 15, 16) KDA_FMAC(14, 13, 15, 16) KDA_FMAC(15, 14, 15, 16)
+        : "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(x[4]), "+v"(x[5]),
+          "+v"(x[6]), "+v"(x[7]), "+v"(x[8]), "+v"(x[9]), "+v"(x[10]),
+          "+v"(x[11]), "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[0]), "v"(x[0]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(2, 0, 14, 15) KDA_FMAC(3, 1, 14, 15) KDA_FMAC(4, 2, 14, 15)
+        KDA_FMAC(5, 3, 14, 15) KDA_FMAC(6, 4, 14, 15) KDA_FMAC(7, 5, 14, 15)
+        KDA_FMAC(8, 6, 14, 15) KDA_FMAC(9, 7, 14, 15) KDA_FMAC(10, 8, 14, 15)
+        KDA_FMAC(11, 9, 14, 15) KDA_FMAC(12, 10, 14, 15) KDA_FMAC(13, 11, 14, 15)
+        KDA_FMAC(14, 12, 14, 15) KDA_FMAC(15, 13, 14, 15)
+        : "+v"(x[2]), "+v"(x[3]), "+v"(x[4]), "+v"(x[5]), "+v"(x[6]),
+          "+v"(x[7]), "+v"(x[8]), "+v"(x[9]), "+v"(x[10]), "+v"(x[11]),
+          "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[1]), "v"(x[1]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(3, 0, 13, 14) KDA_FMAC(4, 1, 13, 14) KDA_FMAC(5, 2, 13, 14)
+        KDA_FMAC(6, 3, 13, 14) KDA_FMAC(7, 4, 13, 14) KDA_FMAC(8, 5, 13, 14)
+        KDA_FMAC(9, 6, 13, 14) KDA_FMAC(10, 7, 13, 14) KDA_FMAC(11, 8, 13, 14)
+        KDA_FMAC(12, 9, 13, 14) KDA_FMAC(13, 10, 13, 14) KDA_FMAC(14, 11, 13, 14)
+        KDA_FMAC(15, 12, 13, 14)
+        : "+v"(x[3]), "+v"(x[4]), "+v"(x[5]), "+v"(x[6]), "+v"(x[7]),
+          "+v"(x[8]), "+v"(x[9]), "+v"(x[10]), "+v"(x[11]), "+v"(x[12]),
+          "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[2]), "v"(x[2]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(4, 0, 12, 13) KDA_FMAC(5, 1, 12, 13) KDA_FMAC(6, 2, 12, 13)
+        KDA_FMAC(7, 3, 12, 13) KDA_FMAC(8, 4, 12, 13) KDA_FMAC(9, 5, 12, 13)
+        KDA_FMAC(10, 6, 12, 13) KDA_FMAC(11, 7, 12, 13) KDA_FMAC(12, 8, 12, 13)
+        KDA_FMAC(13, 9, 12, 13) KDA_FMAC(14, 10, 12, 13) KDA_FMAC(15, 11, 12, 13)
+        : "+v"(x[4]), "+v"(x[5]), "+v"(x[6]), "+v"(x[7]), "+v"(x[8]),
+          "+v"(x[9]), "+v"(x[10]), "+v"(x[11]), "+v"(x[12]), "+v"(x[13]),
+          "+v"(x[14]), "+v"(x[15])
+        : "v"(a[3]), "v"(x[3]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(5, 0, 11, 12) KDA_FMAC(6, 1, 11, 12) KDA_FMAC(7, 2, 11, 12)
+        KDA_FMAC(8, 3, 11, 12) KDA_FMAC(9, 4, 11, 12) KDA_FMAC(10, 5, 11, 12)
+        KDA_FMAC(11, 6, 11, 12) KDA_FMAC(12, 7, 11, 12) KDA_FMAC(13, 8, 11, 12)
+        KDA_FMAC(14, 9, 11, 12) KDA_FMAC(15, 10, 11, 12)
+        : "+v"(x[5]), "+v"(x[6]), "+v"(x[7]), "+v"(x[8]), "+v"(x[9]),
+          "+v"(x[10]), "+v"(x[11]), "+v"(x[12]), "+v"(x[13]), "+v"(x[14]),
+          "+v"(x[15])
+        : "v"(a[4]), "v"(x[4]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(6, 0, 10, 11) KDA_FMAC(7, 1, 10, 11) KDA_FMAC(8, 2, 10, 11)
+        KDA_FMAC(9, 3, 10, 11) KDA_FMAC(10, 4, 10, 11) KDA_FMAC(11, 5, 10, 11)
+        KDA_FMAC(12, 6, 10, 11) KDA_FMAC(13, 7, 10, 11) KDA_FMAC(14, 8, 10, 11)
+        KDA_FMAC(15, 9, 10, 11)
+        : "+v"(x[6]), "+v"(x[7]), "+v"(x[8]), "+v"(x[9]), "+v"(x[10]),
+          "+v"(x[11]), "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[5]), "v"(x[5]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(7, 0, 9, 10) KDA_FMAC(8, 1, 9, 10) KDA_FMAC(9, 2, 9, 10)
+        KDA_FMAC(10, 3, 9, 10) KDA_FMAC(11, 4, 9, 10) KDA_FMAC(12, 5, 9, 10)
+        KDA_FMAC(13, 6, 9, 10) KDA_FMAC(14, 7, 9, 10) KDA_FMAC(15, 8, 9, 10)
+        : "+v"(x[7]), "+v"(x[8]), "+v"(x[9]), "+v"(x[10]), "+v"(x[11]),
+          "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[6]), "v"(x[6]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(8, 0, 8, 9) KDA_FMAC(9, 1, 8, 9) KDA_FMAC(10, 2, 8, 9)
+        KDA_FMAC(11, 3, 8, 9) KDA_FMAC(12, 4, 8, 9) KDA_FMAC(13, 5, 8, 9)
+        KDA_FMAC(14, 6, 8, 9) KDA_FMAC(15, 7, 8, 9)
+        : "+v"(x[8]), "+v"(x[9]), "+v"(x[10]), "+v"(x[11]), "+v"(x[12]),
+          "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[7]), "v"(x[7]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(9, 0, 7, 8) KDA_FMAC(10, 1, 7, 8) KDA_FMAC(11, 2, 7, 8)
+        KDA_FMAC(12, 3, 7, 8) KDA_FMAC(13, 4, 7, 8) KDA_FMAC(14, 5, 7, 8)
+        KDA_FMAC(15, 6, 7, 8)
+        : "+v"(x[9]), "+v"(x[10]), "+v"(x[11]), "+v"(x[12]), "+v"(x[13]),
+          "+v"(x[14]), "+v"(x[15])
+        : "v"(a[8]), "v"(x[8]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(10, 0, 6, 7) KDA_FMAC(11, 1, 6, 7) KDA_FMAC(12, 2, 6, 7)
+        KDA_FMAC(13, 3, 6, 7) KDA_FMAC(14, 4, 6, 7) KDA_FMAC(15, 5, 6, 7)
+        : "+v"(x[10]), "+v"(x[11]), "+v"(x[12]), "+v"(x[13]), "+v"(x[14]),
+          "+v"(x[15])
+        : "v"(a[9]), "v"(x[9]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(11, 0, 5, 6) KDA_FMAC(12, 1, 5, 6) KDA_FMAC(13, 2, 5, 6)
+        KDA_FMAC(14, 3, 5, 6) KDA_FMAC(15, 4, 5, 6)
+        : "+v"(x[11]), "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[10]), "v"(x[10]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(12, 0, 4, 5) KDA_FMAC(13, 1, 4, 5) KDA_FMAC(14, 2, 4, 5)
+        KDA_FMAC(15, 3, 4, 5)
+        : "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[11]), "v"(x[11]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(13, 0, 3, 4) KDA_FMAC(14, 1, 3, 4) KDA_FMAC(15, 2, 3, 4)
+        : "+v"(x[13]), "+v"(x[14]), "+v"(x[15])
+        : "v"(a[12]), "v"(x[12]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(14, 0, 2, 3) KDA_FMAC(15, 1, 2, 3)
+        : "+v"(x[14]), "+v"(x[15])
+        : "v"(a[13]), "v"(x[13]));
+    asm("s_nop 1\n\t"
+        KDA_FMAC(15, 0, 1, 2)
+        : "+v"(x[15])
+        : "v"(a[14]), "v"(x[14]));
 }
+#undef KDA_FMAC
 
 template <class EI, int K, int OUT>
 __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProblem p) {
     typedef PreLds<K, OUT> L;
-    constexpr int CPL = K / kWave;  // channels per lane
-    constexpr int NT = K / 16;      // state row tiles
+    constexpr int NT = K / 16;  // state row tiles
+    // A wavefront prepares 8 tokens: K / 4 lanes of 4 channels to a token, in
+    // GRP groups of lanes with TPL tokens each.
+    constexpr int GRP = 4 * kWave / K, TPL = 8 / GRP;
     constexpr int NQ = L::NQ;
     constexpr int MQ = OUT == 0 ? 6 : 3;  // products for P, P U and (q e^G) S
     constexpr int OE = OUT == 0 ? 4 : 2;  // bytes of an output element
@@ -277,16 +440,18 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         return;
     }
 
-    // the state
+    // the state: lane group g4's rows of tile rt are channels
+    // 32 (rt / 2) + 8 g4 + 4 (rt % 2) + s
+    auto state_row = [](int rt, int s) { return 32 * (rt >> 1) + 4 * (rt & 1) + s; };
     f4 S[NT][2];
-    float *pool = p.pool.base + (((long)slot * p.H + h) * K + 4 * (lane0 >> 4)) * p.V + col;
+    float *pool = p.pool.base + (((long)slot * p.H + h) * K + 8 * (lane0 >> 4)) * p.V + col;
     if (cols && request_continues(p.pool, n)) {
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const f2 v = __builtin_nontemporal_load(
-                    reinterpret_cast<const f2 *>(pool + (long)(16 * rt + s) * p.V));
+                    reinterpret_cast<const f2 *>(pool + (long)state_row(rt, s) * p.V));
                 S[rt][0][s] = v[0];
                 S[rt][1][s] = v[1];
             }
@@ -300,28 +465,35 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
     for (int i = threadIdx.x; i < (3 + NQ) * L::T32 / 4; i += kPreThreads)
         reinterpret_cast<uint32_t *>(lds + L::TM)[i] = 0;
 
-    // this wavefront's 8 tokens of the next chunk, as loaded
-    RawC<EI, CPL> kraw[8], qraw[8];
-    RawC<F32, CPL> graw[8];
+    // this wavefront's tokens of the next chunk, as loaded, and (wavefront 3)
+    // the chunk's write strengths
+    RawC<EI, 4> kraw[TPL], qraw[TPL];
+    f4 graw[TPL];
+    float braw = 0.0f;
     auto load_rows = [&](int t0) {
         const int len = min(kPreC, len_all - t0);
         const Rsrc rk = rows_of(kb + (long)t0 * ks, ks, K * EI::kBytes, len);
         const Rsrc rq = rows_of(qb + (long)t0 * ks, ks, K * EI::kBytes, len);
         const Rsrc rg = rows_of(gb + (long)t0 * gs, gs, gd * 4, len);
         const int lane = opaque_lane(lane0);
-        const uint32_t ok = 8 * wv * ks + CPL * lane * EI::kBytes;
+        const uint32_t first = 8 * wv + lane / (K / 4) * TPL, c4 = lane % (K / 4) * 4;
         if (gd == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) graw[i].load_same(rg, (8 * wv + i) * gs);
+            for (int i = 0; i < TPL; ++i) {
+                const float x = load1<F32>(rg, (first + i) * gs);
+                graw[i] = f4{x, x, x, x};
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) graw[i].load(rg, 8 * wv * gs + CPL * lane * 4 + i * gs);
+            for (int i = 0; i < TPL; ++i) graw[i] = load4<F32>(rg, (first + i) * gs + c4 * 4);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            kraw[i].load(rk, ok + i * ks);
-            qraw[i].load(rq, ok + i * ks);
+        for (int i = 0; i < TPL; ++i) {
+            kraw[i].load(rk, (first + i) * ks + c4 * EI::kBytes);
+            qraw[i].load(rq, (first + i) * ks + c4 * EI::kBytes);
         }
+        if (wv == 3)
+            braw = lane < len ? p.beta[(row_first + t0 + lane) * p.H + h] : 0.0f;
     };
     if (len_all > 0) load_rows(0);
 
@@ -331,157 +503,137 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         // where they are used instead of being kept (and spilled) across chunks
         const int lane = opaque_lane(lane0);
         const int g4 = lane >> 4, n16 = lane & 15;
-        const int ch = CPL * lane;
-        // byte of this lane's channels in a row reduced over channels, and of its
-        // operand piece
-        const int cpos = 2 * (32 * (ch >> 5) + operand_pos(ch & 31));
+        // this lane's group, channels and first token of the wavefront's 8
+        const int grp = lane / (K / 4), ch = lane % (K / 4) * 4, tok = 8 * wv + TPL * grp;
         const int rpos = n16 * L::RS + ((g4 << 4) ^ L::swz_row(n16));
         const int tpos = n16 * L::TS + ((g4 << 4) ^ L::swz_tok(n16));
 
-        auto put_row = [&]<int N>(int at, int row, int size, const float (&x)[CPL]) {
-            char *d = lds + at + row * L::RS + (cpos ^ L::swz_row(row));
-            uint32_t part[N];
-            split2<N>(x[0], x[CPL - 1], part);
+        auto put_row = [&]<int N>(int at, int row, f4 x) {
+            char *d = lds + at + row * L::RS + ((2 * ch) ^ L::swz_row(row));
+            const Half<N> hx = split4<N>(x);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if constexpr (CPL == 2)
-                    *reinterpret_cast<uint32_t *>(d + i * size) = part[i];
-                else
-                    *reinterpret_cast<uint16_t *>(d + i * size) = (uint16_t)part[i];
+            for (int i = 0; i < N; ++i) *reinterpret_cast<w2 *>(d + i * L::R32) = hx.p[i];
         };
-        // rows 16 I + n16 of an operand
-        auto row_operand = [&]<int N>(int at, int kk, int size) -> Operand<N> {
+        // 16 rows of an operand reduced over channels, k-step kk
+        auto row_operand = [&]<int N>(int at, int kk) -> Operand<N> {
             Operand<N> o;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                o.p[i] = *reinterpret_cast<const w4 *>(lds + at + i * size + (rpos ^ (64 * kk)));
+                o.p[i] = *reinterpret_cast<const w4 *>(lds + at + i * L::R32 + (rpos ^ (64 * kk)));
             return o;
         };
-        auto tok_operand = [&]<int N>(int at, int size) -> Operand<N> {
+        auto tok_operand = [&]<int N>(int at) -> Operand<N> {
             Operand<N> o;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                o.p[i] = *reinterpret_cast<const w4 *>(lds + at + i * size + tpos);
+                o.p[i] = *reinterpret_cast<const w4 *>(lds + at + i * L::T32 + tpos);
             return o;
         };
-        // one entry of an operand reduced over tokens
-        auto put_entry = [&]<int N>(int at, int row, int c, float x) {
+        // entries (row, c) and (row + 1, c), row even, of an operand reduced
+        // over tokens
+        auto put_pair = [&]<int N>(int at, int row, int c, float x, float y) {
             char *d = lds + at + row * L::TS + ((2 * operand_pos(c)) ^ L::swz_tok(row));
             uint32_t part[N];
-            split2<N>(x, 0.0f, part);
+            split2<N>(x, y, part);
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
                 *reinterpret_cast<uint16_t *>(d + i * L::T32) = (uint16_t)part[i];
+                *reinterpret_cast<uint16_t *>(d + i * L::T32 + L::TS) = (uint16_t)(part[i] >> 16);
+            }
         };
 
-        // ---- 1. decays of this wavefront's 8 tokens
-        float tot[CPL];
-        float steep = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            float x = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x += graw[i].at(c) * kLog2E;
-                steep = !(__builtin_fabsf(x) <= kSteep) ? 1.0f : steep;
-            }
-            tot[c] = x;
-        }
+        // ---- 1. decays of this lane's tokens, summed from its wavefront's
+        // first token on
+        f4 er[TPL], sums[GRP];
         float *tots = reinterpret_cast<float *>(lds + L::TOT);
+        {
+            f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) tots[wv * K + ch + c] = tot[c];
-        int *flag = reinterpret_cast<int *>(lds + L::FLAG);
-        const bool any = __ballot(steep != 0.0f) != 0;
-        if (lane == 0) flag[wv] = any;
+            for (int i = 0; i < TPL; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(graw[i][e], kLog2E, x[e]);
+                er[i] = x;
+            }
+            gather_groups<GRP>(x, sums);
+            f4 all = sums[0];
+#pragma unroll
+            for (int g = 1; g < GRP; ++g) all += sums[g];
+            if (grp == 0) *reinterpret_cast<f4 *>(tots + wv * K + ch) = all;
+        }
         float *beta = reinterpret_cast<float *>(lds + L::BETA) + buf * kPreC;
-        if (wv == 3 && lane < kPreC)
-            beta[lane] =
-                lane < len ? p.beta[(row_first + t0 + lane) * p.H + h] : 0.0f;
+        if (wv == 3 && lane < kPreC) beta[lane] = braw;
         __syncthreads();  // totals; every read of the previous chunk's operands is done
 
-        const bool far = (flag[0] | flag[1] | flag[2] | flag[3]) != 0;
-        float wt[kPreWaves][CPL];
+        f4 wt[kPreWaves];  // every wavefront's 8 tokens
 #pragma unroll
         for (int w = 0; w < kPreWaves; ++w)
+            wt[w] = *reinterpret_cast<const f4 *>(tots + w * K + ch);
+        const f4 first = wt[0] + wt[1], second = wt[2] + wt[3];  // m, G_32 - m
+        bool steep = false;  // (NaN or infinite where any gate is)
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) wt[w][c] = tots[w * K + ch + c];
-        if (wv == 0) {
-#pragma unroll
-            for (int c = 0; c < CPL; ++c)
-                reinterpret_cast<float *>(lds + L::DEC)[ch + c] =
-                    __builtin_amdgcn_exp2f(wt[0][c] + wt[1][c] + wt[2][c] + wt[3][c]);
+        for (int e = 0; e < 4; ++e)
+            steep |= !(__builtin_fabsf(first[e]) <= kSteep) |
+                     !(__builtin_fabsf(second[e]) <= kSteep);
+        const bool far = __ballot(steep) != 0;  // the same in every wavefront
+        if (wv == 0 && grp == 0) {
+            const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
+            *reinterpret_cast<f4 *>(lds + L::EM + 4 * ch) = far ? one : exp2(first);
+            *reinterpret_cast<f4 *>(lds + L::EG + 4 * ch) = far ? one : exp2(second);
+            *reinterpret_cast<f4 *>(lds + L::EF + 4 * ch) = exp2(first + second);
         }
-        // e^{G - middle of the block} of every token (or, of a steep chunk, e^G
-        // from step 3 on)
-        float er[8][CPL];
         if (!far) {
-            float ko[CPL];
+            // from the chunk's middle to this lane's first token
+            f4 mid = wv == 0 ? -wt[1] : wv == 3 ? wt[2] : f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                float x = wv & 1 ? 0.0f : -tot[c];
-                ko[c] = __builtin_amdgcn_exp2f(wt[1][c] + wt[2][c]);
+            for (int g = 0; g < GRP; ++g)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x += graw[i].at(c) * kLog2E;
-                    er[i][c] = __builtin_amdgcn_exp2f(x);
-                }
-            }
+                for (int e = 0; e < 4; ++e)
+                    mid[e] += wv >= 2 ? (g < grp ? sums[g][e] : 0.0f)
+                                      : (g >= grp ? -sums[g][e] : 0.0f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 8 * wv + i;
-                float a[CPL], b[CPL], d[CPL];
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    a[c] = kraw[i].at(c) * er[i][c];
-                    b[c] = qraw[i].at(c) * (er[i][c] * p.scale);
-                    d[c] = kraw[i].at(c) * __builtin_amdgcn_rcpf(er[i][c]);
-                }
-                put_row.template operator()<2>(L::KR, r, L::R32, a);
-                put_row.template operator()<NQ>(L::QR, r, L::R32, b);
-                put_row.template operator()<NQ>(L::KL, r, L::R32, d);
-            }
-            if (wv < 2) {  // block 0's keys relative to block 1's middle
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float d[CPL];
-#pragma unroll
-                    for (int c = 0; c < CPL; ++c)
-                        d[c] = kraw[i].at(c) * (__builtin_amdgcn_rcpf(er[i][c]) * ko[c]);
-                    put_row.template operator()<NQ>(L::KO, 8 * wv + i, L::R16, d);
-                }
+            for (int i = 0; i < TPL; ++i) {
+                const f4 e = exp2(er[i] + mid), k = kraw[i].all();
+                put_row.template operator()<2>(L::KR, tok + i, k * e);
+                put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
+                put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    const int at = (8 * wv + i) * K + ch + c;
-                    reinterpret_cast<float *>(lds + L::SK)[at] = kraw[i].at(c);
-                    reinterpret_cast<float *>(lds + L::SQ)[at] = qraw[i].at(c) * p.scale;
-                    reinterpret_cast<float *>(lds + L::SA)[at] =
-                        __builtin_amdgcn_exp2f(graw[i].at(c) * kLog2E);
-                }
+            for (int i = 0; i < TPL; ++i) {
+                const int at = 4 * ((tok + i) * K + ch);
+                *reinterpret_cast<f4 *>(lds + L::SK + at) = kraw[i].all();
+                *reinterpret_cast<f4 *>(lds + L::SQ + at) = qraw[i].all() * p.scale;
+                *reinterpret_cast<f4 *>(lds + L::SA + at) = exp2(graw[i] * kLog2E);
+            }
         }
         __syncthreads();
 
-        // ---- 2. L / beta and P, one 16 x 16 block per wavefront: (0, 0),
-        // (1, 1), (1, 0)
-        const int bi = wv == 0 ? 0 : 1, bj = wv == 1 ? 1 : 0;
-        f4 m = {0.0f, 0.0f, 0.0f, 0.0f}, pp = m;
+        // ---- 2. 16 x 16 blocks of L / beta and P: wavefronts 0 and 1 a
+        // diagonal block of L each (and its inverse), 2 those of P, 3 the two
+        // blocks below
+        f4 m[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
         if (!far) {
-            if (wv < 3) {
-                const int kl = wv == 2 ? L::KO : L::KL + 16 * bj * L::RS;
-                const int size = wv == 2 ? L::R16 : L::R32;
+            // rows 16 bi .. of `left` against rows 16 bj .. of the keys
+            auto block = [&]<int M, int N>(int left, int bi, int bj) -> f4 {
+                Operand<N> l[K / 32], r[K / 32];
 #pragma unroll
                 for (int kk = 0; kk < K / 32; ++kk) {
-                    const auto d = row_operand.template operator()<NQ>(kl, kk, size);
-                    m = mul<3>(row_operand.template operator()<2>(L::KR + 16 * bi * L::RS, kk,
-                                                                  L::R32),
-                               d, m);
-                    pp = mul<MQ>(row_operand.template operator()<NQ>(L::QR + 16 * bi * L::RS, kk,
-                                                                     L::R32),
-                                 d, pp);
+                    l[kk] = row_operand.template operator()<N>(left + 16 * bi * L::RS, kk);
+                    r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
                 }
+                f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int kk = 0; kk < K / 32; ++kk) c = mul<M>(l[kk], r[kk], c);
+                return c;
+            };
+            if (wv < 2) {
+                m[0] = block.template operator()<3, 2>(L::KR, wv, wv);
+            } else if (wv == 2) {
+                m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
+                m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 1);
+            } else {
+                m[0] = block.template operator()<3, 2>(L::KR, 1, 0);
+                m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
             }
         } else {
             // running products of the decays from token j on
@@ -492,17 +644,19 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             float *sp = reinterpret_cast<float *>(lds + L::SP);
 #pragma unroll 1
             for (int j = wv; j < kPreC; j += kPreWaves) {
+                constexpr int CPL = K / kWave;  // channels per lane, 64 apart
                 float f[CPL];
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) f[c] = sk[j * K + ch + c];
+                for (int c = 0; c < CPL; ++c) f[c] = sk[j * K + lane + 64 * c];
 #pragma unroll 1
                 for (int i = j; i < kPreC; ++i) {
                     float a = 0.0f, b = 0.0f;
 #pragma unroll
                     for (int c = 0; c < CPL; ++c) {
-                        if (i > j) f[c] *= sa[i * K + ch + c];
-                        a = __builtin_fmaf(f[c], sk[i * K + ch + c], a);
-                        b = __builtin_fmaf(f[c], sq[i * K + ch + c], b);
+                        const int at = i * K + lane + 64 * c;
+                        if (i > j) f[c] *= sa[at];
+                        a = __builtin_fmaf(f[c], sk[at], a);
+                        b = __builtin_fmaf(f[c], sq[at], b);
                     }
                     a = sum64(a);
                     b = sum64(b);
@@ -515,114 +669,114 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             __syncthreads();
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int at = (16 * bi + 4 * g4 + s) * kPreC + 16 * bj + n16;
-                m[s] = sm[at];
-                pp[s] = sp[at];
+                const int top = (4 * g4 + s) * kPreC + n16, low = top + 16 * kPreC;
+                if (wv < 2) m[0][s] = sm[wv == 0 ? top : low + 16];
+                if (wv == 2) {
+                    m[0][s] = sp[top];
+                    m[1][s] = sp[low + 16];
+                }
+                if (wv == 3) {
+                    m[0][s] = sm[low];
+                    m[1][s] = sp[low];
+                }
             }
         }
         // the inverse's diagonal blocks and -L_10, and P, as A operands
-        if (wv < 3) {
-            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 * bi + 4 * g4);
-            if (wv == 2) {
+        if (wv < 2) {
+            float *patch = reinterpret_cast<float *>(lds + L::PATCH) + wv * 16 * L::kPatch;
+            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 * wv + 4 * g4);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    put_entry.template operator()<2>(L::TM, 16 + 4 * g4 + s, n16, -b4[s] * m[s]);
-                    put_entry.template operator()<NQ>(L::PM, 16 + 4 * g4 + s, n16, pp[s]);
-                }
-            } else {
-                float *patch = reinterpret_cast<float *>(lds + L::PATCH) + wv * 16 * 17;
+            for (int s = 0; s < 4; ++s) {
+                const int r = 4 * g4 + s;
+                patch[r * L::kPatch + n16] = n16 < r ? -b4[s] * m[0][s] : 0.0f;
+            }
+            float arow[16], x[16];  // every 16-lane row the same
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
+            for (int j = 0; j < 16; ++j) x[j] = j == n16 ? 1.0f : 0.0f;
+            wave_sync();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f4 v = *reinterpret_cast<const f4 *>(&patch[n16 * L::kPatch + 4 * j]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) arow[4 * j + s] = v[s];
+            }
+            substitute(arow, x);
+            f4 y;  // rows 4 g4 .. + 3 (two opaque bits: selects, not a switch on g4)
+            const bool odd = opaque_lane(g4 & 1), high = opaque_lane(g4 >> 1);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float a = odd ? x[4 + s] : x[s], b = odd ? x[12 + s] : x[8 + s];
+                y[s] = high ? b : a;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; s += 2)
+                put_pair.template operator()<3>(L::TM, 16 * wv + 4 * g4 + s, 16 * wv + n16, y[s],
+                                                y[s + 1]);
+        } else if (wv == 2) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int s = 0; s < 4; s += 2) {
                     const int r = 4 * g4 + s;
-                    patch[r * 17 + n16] = n16 < r ? b4[s] * m[s] : 0.0f;
-                    put_entry.template operator()<NQ>(L::PM, 16 * wv + r, 16 * wv + n16,
-                                                      n16 <= r ? pp[s] : 0.0f);
+                    put_pair.template operator()<NQ>(L::PM, 16 * b + r, 16 * b + n16,
+                                                     n16 <= r ? m[b][s] : 0.0f,
+                                                     n16 <= r + 1 ? m[b][s + 1] : 0.0f);
                 }
-                wave_sync();
-                // forward substitution, one lane per column (every 16-lane row
-                // of the wavefront the same)
-                float arow[16], x[16];
+        } else {
+            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 + 4 * g4);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    arow[j] = patch[n16 * 17 + j];
-                    x[j] = j == n16 ? 1.0f : 0.0f;
-                }
-                substitute<1, 16>(arow, x, n16);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const float y = g4 == 0 ? x[s] : g4 == 1 ? x[4 + s]
-                                                : g4 == 2   ? x[8 + s]
-                                                            : x[12 + s];
-                    put_entry.template operator()<3>(L::TM, 16 * wv + 4 * g4 + s, 16 * wv + n16,
-                                                     y);
-                }
+            for (int s = 0; s < 4; s += 2) {
+                put_pair.template operator()<2>(L::TM, 16 + 4 * g4 + s, n16, -b4[s] * m[0][s],
+                                                -b4[s + 1] * m[0][s + 1]);
+                put_pair.template operator()<NQ>(L::PM, 16 + 4 * g4 + s, n16, m[1][s], m[1][s + 1]);
             }
         }
-        __syncthreads();
-
-        // ---- 3. k e^G, q e^G and (k e^{G_32 - G})^T
-        {
-            // k e^{G_32 - G} first, while er is relative to the block's middle
-            float kh[8][CPL];
-            if (!far) {
+        if (far) {
+            // k e^G, q e^G and k e^{G_32 - G} over the FP32 copies; sums from
+            // the chunk's ends, so that no difference of large sums is taken
+            // (formed anew from the loaded gates, through copies that the
+            // compiler cannot tell from new values, so that nothing is held in
+            // registers for this branch)
+            f4 before = {0.0f, 0.0f, 0.0f, 0.0f}, after = before, g2[TPL], ends[GRP], x = before;
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    const float before = wv < 2 ? wt[0][c] : wt[0][c] + wt[1][c] + wt[2][c];
-                    const float after = wv < 2 ? wt[1][c] + wt[2][c] + wt[3][c] : wt[3][c];
-                    const float eb = __builtin_amdgcn_exp2f(before);
-                    const float ea = __builtin_amdgcn_exp2f(after);
+            for (int i = 0; i < TPL; ++i) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        kh[i][c] = kraw[i].at(c) * (__builtin_amdgcn_rcpf(er[i][c]) * ea);
-                        er[i][c] *= eb;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    float g = graw[i][e];
+                    asm("" : "+v"(g));
+                    g2[i][e] = g * kLog2E;
                 }
-            } else {
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    float x = 0.0f, y = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kPreWaves; ++w) {
-                        x += w < wv ? wt[w][c] : 0.0f;
-                        y += w > wv ? wt[w][c] : 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 7; i >= 0; --i) {
-                        kh[i][c] = kraw[i].at(c) * __builtin_amdgcn_exp2f(y);
-                        y += graw[i].at(c) * kLog2E;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x += graw[i].at(c) * kLog2E;
-                        er[i][c] = __builtin_amdgcn_exp2f(x);
-                    }
-                }
+                x += g2[i];
+            }
+            gather_groups<GRP>(x, ends);
+#pragma unroll 1
+            for (int w = 0; w < kPreWaves; ++w) {
+                const f4 y = *reinterpret_cast<const f4 *>(tots + w * K + ch);
+                if (w < wv) before += y;
+                if (w > wv) after += y;
             }
 #pragma unroll
-            for (int c = 0; c < CPL; ++c)
+            for (int g = 0; g < GRP; ++g)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const Half<3> hx = split4<3>(
-                        f4{kh[4 * j][c], kh[4 * j + 1][c], kh[4 * j + 2][c], kh[4 * j + 3][c]});
-                    char *d = lds + L::KT + (ch + c) * L::TS +
-                              ((2 * operand_pos(8 * wv + 4 * j)) ^ L::swz_tok(ch + c));
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) *reinterpret_cast<w2 *>(d + i * L::KTP) = hx.p[i];
+                for (int e = 0; e < 4; ++e) {
+                    before[e] += g < grp ? ends[g][e] : 0.0f;
+                    after[e] += g > grp ? ends[g][e] : 0.0f;
                 }
+            __syncthreads();  // the copies (and L and P) have been read
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a[CPL], b[CPL];
+            for (int i = 0; i < TPL; ++i) {
+                before += g2[i];
+                const f4 e = exp2(before);
+                put_row.template operator()<2>(L::KR, tok + i, kraw[i].all() * e);
+                put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
+            }
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    a[c] = kraw[i].at(c) * er[i][c];
-                    b[c] = qraw[i].at(c) * (er[i][c] * p.scale);
-                }
-                put_row.template operator()<2>(L::KS, 8 * wv + i, L::R32, a);
-                put_row.template operator()<NQ>(L::QS, 8 * wv + i, L::R32, b);
+            for (int i = TPL - 1; i >= 0; --i) {
+                put_row.template operator()<3>(L::KL, tok + i, kraw[i].all() * exp2(after));
+                after += g2[i];
             }
         }
-        // the next chunk's rows, and the values of this wavefront's columns
-        __syncthreads();
+        // the values of this wavefront's columns
         RawC<EI, 2> vraw[2][4];
         {
             const Rsrc rv = rows_of(vb + (long)t0 * vs, vs, p.V * EI::kBytes, len);
@@ -632,29 +786,54 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 #pragma unroll
                 for (int s = 0; s < 4; ++s) vraw[I][s].load(rv, at + (16 * I + s) * vs);
         }
-        if (t0 + kPreC < len_all) load_rows(t0 + kPreC);
+        __syncthreads();
 
-        // ---- 4. this wavefront's columns
+        // ---- 3. this wavefront's columns
+        if (t0 + kPreC < len_all) load_rows(t0 + kPreC);
         if (!cols) continue;
+        // The operands of each group of products are read from LDS one group
+        // ahead, and the state's next rows are scaled and split in the
+        // products' shadow.
         const f4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-        f4 ks[2][2] = {{z, z}, {z, z}}, o[2][2] = {{z, z}, {z, z}};
+        f4 kS[2][2] = {{z, z}, {z, z}}, o[2][2] = {{z, z}, {z, z}};
+        Operand<2> ka_op[2];
+        Operand<NQ> qa_op[2], b[2][2];
+        f4 em[2];
+        auto read_rows = [&](int j) {  // k-step j / 2, row tile j % 2
+            const int at = 16 * (j & 1) * L::RS;
+            ka_op[j & 1] = row_operand.template operator()<2>(L::KR + at, j >> 1);
+            qa_op[j & 1] = row_operand.template operator()<NQ>(L::QR + at, j >> 1);
+        };
+        auto read_em = [&](int kk) {
 #pragma unroll
-        for (int kk = 0; kk < K / 32; ++kk) {
-            Operand<NQ> b[2];
+            for (int t = 0; t < 2; ++t)
+                em[t] = *reinterpret_cast<const f4 *>(lds + L::EM +
+                                                      4 * (8 * g4 + state_row(2 * kk + t, 0)));
+        };
+        auto split_state = [&](int kk, int ct) {  // S' (also of a steep chunk, where it is S)
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct)
-                b[ct] = join(split4<NQ>(S[2 * kk][ct]), split4<NQ>(S[2 * kk + 1][ct]));
+            for (int t = 0; t < 2; ++t) S[2 * kk + t][ct] *= em[t];
+            b[kk & 1][ct] = join(split4<NQ>(S[2 * kk][ct]), split4<NQ>(S[2 * kk + 1][ct]));
+        };
+        read_em(0);
+        read_rows(0);
+        split_state(0, 0);
+        split_state(0, 1);
+        read_em(1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int I = 0; I < 2; ++I) {
-                const auto a =
-                    row_operand.template operator()<2>(L::KS + 16 * I * L::RS, kk, L::R32);
+        for (int j = 0; j < K / 16; ++j) {
+            const int kk = j >> 1, I = j & 1;
+            if (j + 1 < K / 16) read_rows(j + 1);
+            if (kk + 1 < K / 32) split_state(kk + 1, I);
+            if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) ks[I][ct] = mul<3>(a, b[ct], ks[I][ct]);
-                const auto q =
-                    row_operand.template operator()<NQ>(L::QS + 16 * I * L::RS, kk, L::R32);
+            for (int ct = 0; ct < 2; ++ct) kS[I][ct] = mul<3>(ka_op[I], b[kk & 1][ct], kS[I][ct]);
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) o[I][ct] = mul<MQ>(q, b[ct], o[I][ct]);
-            }
+            for (int ct = 0; ct < 2; ++ct) o[I][ct] = mul<MQ>(qa_op[I], b[kk & 1][ct], o[I][ct]);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 + NQ, 0);  // LDS reads
+            interleave<6 + 2 * MQ, 3>();
+            __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time: U_0 = X_00 R_0, U_1 = X_11 (R_1 - L_10 U_0)
         f4 R[2][2];
@@ -665,24 +844,32 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct)
-                    R[I][ct][s] = b4[s] * (vraw[I][s].at(ct) - ks[I][ct][s]);
+                    R[I][ct][s] = b4[s] * (vraw[I][s].at(ct) - kS[I][ct][s]);
         }
         Operand<3> u[2];
         {
-            const auto x0 = tok_operand.template operator()<3>(L::TM, L::T32);
-            const auto x1 = tok_operand.template operator()<3>(L::TM + 16 * L::TS, L::T32);
-            const auto p0 = tok_operand.template operator()<NQ>(L::PM, L::T32);
-            const auto p1 = tok_operand.template operator()<NQ>(L::PM + 16 * L::TS, L::T32);
+            const auto x0 = tok_operand.template operator()<3>(L::TM);
+            const auto x1 = tok_operand.template operator()<3>(L::TM + 16 * L::TS);
+            const auto p0 = tok_operand.template operator()<NQ>(L::PM);
+            const auto p1 = tok_operand.template operator()<NQ>(L::PM + 16 * L::TS);
             const Half<3> none = zero_half<3>();
+            Half<3> h0[2];
+            f4 x[2];
+            // both column tiles step by step, so that one's products cover
+            // the other's splits
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(x0, join(split4<3>(R[0][ct]), none), z);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
-                const f4 u0 = mul<6>(x0, join(split4<3>(R[0][ct]), none), z);
-                const Half<3> h0 = split4<3>(u0);
-                const Operand<3> first = join(h0, none);
-                const f4 r1 = mul<3>(x1, first, R[1][ct]);
-                const f4 u1 = mul<6>(x1, join(none, split4<3>(r1)), z);
-                u[ct] = join(h0, split4<3>(u1));
-                o[0][ct] = mul<MQ>(p0, first, o[0][ct]);
+                h0[ct] = split4<3>(x[ct]);
+                x[ct] = mul<3>(x1, join(h0[ct], none), R[1][ct]);
+                o[0][ct] = mul<MQ>(p0, join(h0[ct], none), o[0][ct]);
+            }
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(x1, join(none, split4<3>(x[ct])), z);
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                u[ct] = join(h0[ct], split4<3>(x[ct]));
                 o[1][ct] = mul<MQ>(p1, u[ct], o[1][ct]);
             }
         }
@@ -695,13 +882,46 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 for (int s = 0; s < 4; ++s)
                     put_out(ro, at + (16 * I + s) * os, o[I][0][s], o[I][1][s]);
         }
-        // the state
+        // the state: S = e^{G_32 - m} (S' + (k e^{m - G})^T U); of a steep
+        // chunk e^{G_32} S + (k e^{G_32 - G})^T U
+        f4 eg[2];
+        Operand<3> kt[2];
+        // rows of tile rt are channels, reduced over tokens: 4 x 16 blocks of
+        // the keys' rows, transposed by the read (lane 4 r + c of 16 gives the
+        // address of 4 channels of token r, lane j gets channel j's 4 tokens)
+        const int trow = 4 * g4 + (n16 >> 2);
+        auto read_state = [&](int rt) {
+            eg[rt & 1] =
+                *reinterpret_cast<const f4 *>(lds + L::EG + 4 * (8 * g4 + state_row(rt, 0)));
+            const int at = 2 * (8 * (n16 & 3) + state_row(rt, 0));
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb) {
+                    const int row = trow + 16 * hb;
+                    const w2 x = read_transposed(lds + L::KL + i * L::R32 + row * L::RS +
+                                                 (at ^ L::swz_row(row)));
+                    kt[rt & 1].p[i][2 * hb] = x[0];
+                    kt[rt & 1].p[i][2 * hb + 1] = x[1];
+                }
+        };
+        if (far) {
+#pragma unroll
+            for (int rt = 0; rt < NT; ++rt) {
+                const f4 e =
+                    *reinterpret_cast<const f4 *>(lds + L::EF + 4 * (8 * g4 + state_row(rt, 0)));
+                S[rt][0] *= e;
+                S[rt][1] *= e;
+            }
+        }
+        read_state(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
-            const f4 d = *reinterpret_cast<const f4 *>(lds + L::DEC + (16 * rt + 4 * g4) * 4);
-            const auto a = tok_operand.template operator()<3>(L::KT + 16 * rt * L::TS, L::KTP);
+            if (rt + 1 < NT) read_state(rt + 1);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) S[rt][ct] = mul<6>(a, u[ct], S[rt][ct] * d);
+            for (int ct = 0; ct < 2; ++ct)
+                S[rt][ct] = mul<6>(kt[rt & 1], u[ct], S[rt][ct]) * eg[rt & 1];
         }
     }
     if (keep && cols) {
@@ -711,7 +931,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int s = 0; s < 4; ++s)
                 __builtin_nontemporal_store(
                     f2{S[rt][0][s], S[rt][1][s]},
-                    reinterpret_cast<f2 *>(pool + (long)(16 * rt + s) * p.V));
+                    reinterpret_cast<f2 *>(pool + (long)state_row(rt, s) * p.V));
     }
 }
 
