@@ -225,8 +225,9 @@ __device__ __forceinline__ void gather_groups(f4 x, f4 (&out)[G]) {
 
 // LDS layout (bytes). Operands lie in rows of 2 K bytes (reduced over
 // channels) or 64 bytes (over tokens); the 16-byte pieces of a row are
-// exchanged by an exclusive or with the row number so that the 16 rows that an
-// operand read touches fall in different banks without padding.
+// exchanged by an exclusive or with the row number so that the 16 rows of one
+// operand read, and the 4 rows of 4 adjacent pieces of a transposed one, fall
+// in different banks without padding.
 // OUT: kda_dtype of the output.
 template <int K, int OUT>
 struct PreLds {
@@ -254,7 +255,11 @@ struct PreLds {
     static constexpr int kBytes = BETA + 2 * kPreC * 4;
     // exchange of 16-byte pieces
     static __device__ __forceinline__ int swz_row(int row) {
-        return (K == 128 ? row & 15 : (row >> 1) & 7) << 4;
+        // bits 1, 0 of the row move it by 4 pieces, bits 2, 3 within them; (K =
+        // 64: two rows to a line, bit 0 picks the half)
+        const int low = ((row >> 2 ^ row >> 3) & 1) * 2 + (row >> 3 & 1);
+        const int high = K == 128 ? (row >> 1 & 1) * 2 + (row & 1) : row >> 1 & 1;
+        return (high * 4 + low) << 4;
     }
     static __device__ __forceinline__ int swz_tok(int row) { return ((row >> 2) & 3) << 4; }
 };
@@ -922,6 +927,9 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct)
                 S[rt][ct] = mul<6>(kt[rt & 1], u[ct], S[rt][ct]) * eg[rt & 1];
+            __builtin_amdgcn_sched_group_barrier(0x100, 7, 0);
+            interleave<12, 2>();
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (keep && cols) {
