@@ -24,6 +24,7 @@
 namespace kda {
 
 constexpr int kConvThreads = 256;
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr int kConvWaves = kConvThreads / kWave;
 
 // Number of requests that start before row t (wave-uniform t and result):
@@ -103,18 +104,22 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(ConvProb
         past_window(n, slot);
         if (slot < 0 || !live) return;
         float left[W - 1][8];
+        if (rows.y >= W - 1) {
 #pragma unroll
-        for (int w = 0; w < W - 1; ++w) {
-            const int at = rows.y - (W - 1) + w;  // place in the request, < 0: in the old window
-            if (at >= 0) {
-                row_in(rows.x + at, left[w]);
-            } else {
+            for (int w = 0; w < W - 1; ++w) row_in(rows.x + rows.y - (W - 1) + w, left[w]);
+        } else {  // the old window, shifted by the few rows there are
+#pragma unroll
+            for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) left[w][e] = win[w][e];
+            for (int i = 0; i < rows.y; ++i) {
+                float v[8];
+                row_in(rows.x + i, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float o = win[0][e];
 #pragma unroll
-                    for (int j = 1; j < W - 1; ++j) o = w + rows.y == j ? win[j][e] : o;
-                    left[w][e] = o;
+                    for (int w = 0; w + 1 < W - 1; ++w) left[w][e] = left[w + 1][e];
+                    left[W - 2][e] = v[e];
                 }
             }
         }
@@ -133,40 +138,75 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(ConvProb
         const int2 rows = request_rows(p.req, n);
         return rows.x + rows.y;
     };
-    auto token = [&](int t) {
-        float v[8], y[8];
-        row_in(t, v);
+    // Rows a .. b - 1 of the current request, U at a time, the next U loaded
+    // before the present ones are used.
+    constexpr int U = 4;
+    Raw8<E> blk[U];
+    int ready = t0;  // the first row in blk
+    auto load_rows = [&](Raw8<E>(&r)[U], int t, int last) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float a = 0.0f;
+        for (int i = 0; i < U; ++i) r[i].load(x + (long)min(t + i, last) * xrow);
+    };
+    auto run = [&](int a, int b) {
+        if (ready != a) load_rows(blk, a, b - 1);
+        for (int t = a; t < b; t += U) {
+            float v[U][8];
 #pragma unroll
-            for (int w = 0; w < W - 1; ++w) a = __builtin_fmaf(tap[w][e], win[w][e], a);
-            a = __builtin_fmaf(tap[W - 1][e], v[e], a);
-            y[e] = a / (1.0f + __expf(-a));
+            for (int i = 0; i < U; ++i) blk[i].widen(v[i]);
+            if (t + U < b) load_rows(blk, t + U, b - 1);
 #pragma unroll
-            for (int w = 0; w + 1 < W - 1; ++w) win[w][e] = win[w + 1][e];
-            win[W - 2][e] = v[e];
+            for (int i = 0; i < U; ++i) {
+                if (t + i >= b) break;
+                // inputs i - (W - 1) .. i: from the window while negative
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float s = tap[W - 1][e] * v[i][e];
+#pragma unroll
+                    for (int w = 0; w < W - 1; ++w) {
+                        const int at = i - (W - 1) + w;
+                        s = __builtin_fmaf(tap[w][e], at < 0 ? win[W - 1 + at][e] : v[at][e], s);
+                    }
+                    // silu (rcp, exp2 and rsq below are within 1 ulp)
+                    y[e] = s * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * -kLog2E));
+                }
+                if (proj < 2) {
+                    float ss = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(y[e], y[e], ss);
+                    ss = D == 128 ? sum16(ss) : sum8(ss);
+                    const float r = __builtin_amdgcn_rsqf(ss + p.eps_l2);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] *= r;
+                }
+                if (pad) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+                }
+                if (live) Raw8<E>::store(out + (long)(t + i) * width, y);
+            }
+            // the window behind a whole block (after a part of one the run ends:
+            // another run begins with another request, or there is none)
+#pragma unroll
+            for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) win[w][e] = v[U - (W - 1) + w][e];
         }
-        if (proj < 2) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(y[e], y[e], ss);
-            ss = D == 128 ? sum16(ss) : sum8(ss);
-            const float r = 1.0f / __builtin_sqrtf(ss + p.eps_l2);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= r;
-        }
-        if (pad) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-        }
-        if (live) Raw8<E>::store(out + (long)t * width, y);
+        ready = -1;
     };
 
+    // the first rows, of whatever request, while their request is looked up
+    Raw8<E> halo[W - 1];
+    const bool any_row = T_all > 0;
+    if (any_row) {
+        load_rows(blk, t0, T_all - 1);
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w) halo[w].load(x + (long)max(t0 - (W - 1) + w, 0) * xrow);
+    }
     // the request that row t0 lies in, and the next one to start
     int t = t0, cur_bos = 0, cur_end = 0;  // rows [cur_bos, cur_end) of the current request
     int next = p.req.cu ? requests_before(p.req.cu, N, t0, lane)
-                        : (t0 + p.req.seq_len - 1) / p.req.seq_len;
+                        : (t0 + p.req.seq_len - 1) / max(p.req.seq_len, 1);
     next = __builtin_amdgcn_readfirstlane(next);
     if (next > 0 && end_of(next - 1) > t0) {  // inside request next - 1
         cur_bos = start_of(next - 1);
@@ -175,23 +215,32 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(ConvProb
         // its first W - 1 rows need the window of the pool: they belong to
         // the wavefront that begins the request (below)
         t = max(t0, min(cur_bos + W - 1, cur_end));
-        if (t < cur_end) {
+        if (t == t0) {
+#pragma unroll
+            for (int w = 0; w < W - 1; ++w) halo[w].widen(win[w]);
+        } else if (t < cur_end) {
 #pragma unroll
             for (int w = 0; w < W - 1; ++w) row_in(t - (W - 1) + w, win[w]);
         }
         cur_bos = INT32_MIN / 2;  // not begun here
     }
-    for (; t < t1; ++t) {
+    while (t < t1) {
         while (next < N && start_of(next) <= t) {
             begin(next);
             cur_bos = start_of(next);
             cur_end = end_of(next);
             ++next;
         }
-        if (t < cur_end) token(t);  // else no request's row
+        if (t < cur_end) {
+            // to the segment's end, or through the first W - 1 rows of a
+            // request that begins here
+            const int stop = min(cur_end, max(t1, cur_bos + W - 1));
+            run(t, stop);
+            t = stop;
+        } else {
+            t = next < N ? min(t1, start_of(next)) : t1;  // no request's rows
+        }
     }
-    // the rest of the first W - 1 rows of a request begun here
-    for (const int stop = min(cur_bos + W - 1, cur_end); t < stop; ++t) token(t);
     if (t1 == T_all)  // requests of no tokens behind the last row
         while (next < N) begin(next++);
 }
@@ -199,8 +248,12 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(ConvProb
 hipError_t launch_conv(const ConvProblem &p0, int in_dt, hipStream_t stream) {
     ConvProblem p = p0;
     const long groups = ((long)p.H * p.d + 8 * kWave - 1) / (8 * kWave);
-    p.seg = 16;
     const long tokens = p.req.total_tokens > 0 ? p.req.total_tokens : 1;
+    // Tokens per wavefront: 32 (W - 1 rows read twice in 32), fewer while the
+    // launch would leave the compute units short of wavefronts.
+    const long want = 8 * device_cus();
+    p.seg = 32;
+    while (p.seg > 4 && (tokens + p.seg - 1) / p.seg * groups * 3 < want) p.seg /= 2;
     const long waves = (tokens + p.seg - 1) / p.seg * groups * 3;
     const long blocks = (waves + kConvWaves - 1) / kConvWaves;
     if (blocks > (long)(UINT32_MAX / kConvThreads)) return hipErrorInvalidConfiguration;
