@@ -10,8 +10,7 @@ import ctypes
 
 import torch
 
-from . import (CHUNK_SIZES, _alloc_stream, _check, _i32, _i64, _lib, _p, _prepared,
-               _require, _sz)
+from . import (CHUNK_SIZES, _alloc_stream, _check, _i32, _i64, _lib, _p, _prepared, _sz)
 
 _int, _f = ctypes.c_int, ctypes.c_float
 _DELTA = [_p, _p, _p, _int, _p, _p, _p, _int]            # q k v dtype g beta out dtype
@@ -45,20 +44,34 @@ def _code(t) -> int:
     return c
 
 
-def _place(first, stream, *tensors):
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _bad(what: str):
+    raise ValueError(what)
+
+
+# The checks below run on every call, ahead of a launch of a few microseconds:
+# conditions are tested in place and messages built only for a refusal.
+
+def _place(stream, tensors):
     """Stream handle of a call. Every tensor has to be a contiguous cuda
     tensor of the current device: the launch goes to a stream of that device."""
-    dev = first.device
-    _require(dev.type == "cuda", f"expected cuda tensors, got one on {dev}")
-    _require(dev.index == torch.cuda.current_device(),
-             f"tensors are on {dev}, which is not the current device")
-    for t in (first, *tensors):
+    dev = tensors[0].get_device()
+    for t in tensors:
         if t is not None:
-            _require(t.device == dev, f"tensors on {dev} and {t.device}")
-            _require(t.is_contiguous(), "inputs must be contiguous")
+            if t.get_device() != dev or dev < 0:
+                _bad(f"expected cuda tensors of one device, got "
+                     f"{[str(x.device) for x in tensors if x is not None]}")
+            if not t.is_contiguous():
+                _bad("inputs must be contiguous")
+    if dev != _current_device():
+        _bad(f"tensors are on cuda:{dev}, which is not the current device")
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    _require(stream.device == dev, f"tensors on {dev}, stream on {stream.device}")
+        return _current_stream(dev)
+    if stream.device.index != dev:
+        _bad(f"tensors on cuda:{dev}, stream on {stream.device}")
     return stream.cuda_stream
 
 
@@ -66,30 +79,29 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _int32(n, **tensors):
-    """int32 vectors of n entries (None: not given)."""
-    for name, t in tensors.items():
-        if t is not None:
-            _require(t.dtype == torch.int32 and t.dim() == 1 and t.numel() == n,
-                     f"{name} must be int32 [{n}]")
+def _int32(n, name, t):
+    """An int32 vector of n entries (or None)."""
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n):
+        _bad(f"{name} must be int32 [{n}]")
 
 
-def _float32(**tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            _require(t.dtype == torch.float32, f"{name} must be float32")
+def _float32(name, t):
+    if t is not None and t.dtype != torch.float32:
+        _bad(f"{name} must be float32")
 
 
 def _requests(x, lead, cu_seqlens):
     """(number of requests, their C arguments) of a token tensor whose token
     dimension is followed by `lead` - 1 others."""
     if cu_seqlens is None:
-        _require(x.dim() == lead + 1, "dense inputs are [B, T, ...]")
+        if x.dim() != lead + 1:
+            _bad("dense inputs are [B, T, ...]")
         return x.shape[0], (x.shape[0], x.shape[1])
-    _require(x.dim() == lead, "packed inputs are [T, ...]")
-    _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and
-             cu_seqlens.numel() >= 1, "cu_seqlens must be int32 [requests + 1]")
-    n = cu_seqlens.numel() - 1
+    if x.dim() != lead:
+        _bad("packed inputs are [T, ...]")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        _bad("cu_seqlens must be int32 [requests + 1]")
+    n = cu_seqlens.shape[0] - 1
     return n, (cu_seqlens.data_ptr(), n, x.shape[0])
 
 
@@ -99,15 +111,16 @@ def kda_chunk_map(seq_lens, total_tokens, chunk_size, cu_seqlens, chunk_indices=
                   num_chunks=None, stream=None) -> None:
     """cu_seqlens [N + 1] and chunk_indices [M, 2] (rows past the last chunk
     are -1) from int32 request lengths [N]; num_chunks [1] is optional."""
-    s = _place(seq_lens, stream, cu_seqlens, chunk_indices, num_chunks)
+    s = _place(stream, (seq_lens, cu_seqlens, chunk_indices, num_chunks))
     n = seq_lens.numel()
-    _int32(n, seq_lens=seq_lens)
-    _int32(n + 1, cu_seqlens=cu_seqlens)
-    _int32(1, num_chunks=num_chunks)
+    _int32(n, "seq_lens", seq_lens)
+    _int32(n + 1, "cu_seqlens", cu_seqlens)
+    _int32(1, "num_chunks", num_chunks)
     most = 0
     if chunk_indices is not None:
-        _require(chunk_indices.dtype == torch.int32 and chunk_indices.dim() == 2 and
-                 chunk_indices.shape[1] == 2, "chunk_indices must be int32 [M, 2]")
+        if chunk_indices.dtype != torch.int32 or chunk_indices.dim() != 2 or \
+                chunk_indices.shape[1] != 2:
+            _bad("chunk_indices must be int32 [M, 2]")
         most = chunk_indices.shape[0]
     _check(_lib.kda_chunk_map(seq_lens.data_ptr(), n, total_tokens, chunk_size,
                               cu_seqlens.data_ptr(), _addr(chunk_indices) if most else None, most,
@@ -119,7 +132,8 @@ def chunk_map(seq_lens, total_tokens: int, chunk_size: int = 64, stream=None):
     of requests with int32 lengths ``seq_lens`` [N] (on the GPU) that together
     take ``total_tokens`` rows. Entries past the last chunk are (-1, -1), which
     every call that takes ``chunk_indices`` skips."""
-    _require(chunk_size in CHUNK_SIZES, f"chunk size {chunk_size} (16, 32 or 64)")
+    if chunk_size not in CHUNK_SIZES:
+        _bad(f"chunk size {chunk_size} (16, 32 or 64)")
     n = seq_lens.numel()
     with _alloc_stream(stream):
         cu = torch.empty(n + 1, dtype=torch.int32, device=seq_lens.device)
@@ -137,23 +151,26 @@ def kda_conv_prefill(qkv, conv_w, q, k, v, cu_seqlens=None, conv_state=None, slo
     """Causal convolution, silu and L2 norms of packed [T, 3, H, d] (with
     ``cu_seqlens``) or dense [B, T, 3, H, d] inputs into q, k, v [.., H, d];
     ``conv_state`` [slots, 3, H, W - 1, d] is updated in place."""
-    s = _place(qkv, stream, conv_w, q, k, v, cu_seqlens, conv_state, slot, init)
+    s = _place(stream, (qkv, conv_w, q, k, v, cu_seqlens, conv_state, slot, init))
     n, req = _requests(qkv, 4, cu_seqlens)
-    H, d = qkv.shape[-2:]
-    W = conv_w.shape[1] if conv_w.dim() == 4 else 0
-    _require(qkv.shape[-3] == 3 and conv_w.shape == (3, W, H, d),
-             "shapes: qkv [.., 3, H, d], conv_w [3, W, H, d]")
-    rows = qkv.shape[:-3] + (H, d)
-    _require(q.shape == rows and k.shape == rows and v.shape == rows, "q, k, v must be [.., H, d]")
-    _require(q.dtype == qkv.dtype and k.dtype == qkv.dtype and v.dtype == qkv.dtype,
-             "q, k, v must have qkv's dtype")
-    _float32(conv_w=conv_w, conv_state=conv_state)
-    _int32(n, slot=slot, init=init)
+    shape, W = qkv.shape, conv_w.shape[1] if conv_w.dim() == 4 else 0
+    H, d = shape[-2:]
+    if shape[-3] != 3 or conv_w.shape != (3, W, H, d):
+        _bad("shapes: qkv [.., 3, H, d], conv_w [3, W, H, d]")
+    rows = shape[:-3] + (H, d)
+    if q.shape != rows or k.shape != rows or v.shape != rows:
+        _bad("q, k, v must be [.., H, d]")
+    if not q.dtype == k.dtype == v.dtype == qkv.dtype:
+        _bad("q, k, v must have qkv's dtype")
+    _float32("conv_w", conv_w)
+    _float32("conv_state", conv_state)
+    _int32(n, "slot", slot)
+    _int32(n, "init", init)
     slots = 0
     if conv_state is not None:
+        if conv_state.shape[1:] != (3, H, W - 1, d):
+            _bad("conv_state must be [slots, 3, H, W - 1, d]")
         slots = conv_state.shape[0]
-        _require(conv_state.shape == (slots, 3, H, W - 1, d),
-                 "conv_state must be [slots, 3, H, W - 1, d]")
     fn = _lib.kda_conv_prefill_dense if cu_seqlens is None else _lib.kda_conv_prefill_packed
     _check(fn(qkv.data_ptr(), _code(qkv), conv_w.data_ptr(), q.data_ptr(), k.data_ptr(),
               v.data_ptr(), *req, H, d, W, _addr(conv_state), _addr(slot), _addr(init), slots,
@@ -165,7 +182,7 @@ def conv_prefill(qkv, conv_w, cu_seqlens=None, conv_state=None, slot=None, init=
     """Convenience form of kda_conv_prefill: returns (q, k, v)."""
     shape = qkv.shape[:-3] + qkv.shape[-2:]
     with _alloc_stream(stream):
-        q = torch.empty(shape, dtype=qkv.dtype, device=qkv.device)
+        q = qkv.new_empty(shape)
         k, v = torch.empty_like(q), torch.empty_like(q)
     kda_conv_prefill(qkv, conv_w, q, k, v, cu_seqlens, conv_state, slot, init, eps_l2, stream)
     return q, k, v
@@ -174,30 +191,44 @@ def conv_prefill(qkv, conv_w, cu_seqlens=None, conv_state=None, slot=None, init=
 # ---- the gated delta rule ---------------------------------------------------
 
 def _delta_args(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, stream, workspace):
-    s = _place(q, stream, k, v, g, beta, out, cu_seqlens, state, slot, init, workspace)
+    s = _place(stream, (q, k, v, g, beta, out, cu_seqlens, state, slot, init, workspace))
     n, req = _requests(q, 3, cu_seqlens)
-    lead, (Hk, K) = q.shape[:-2], q.shape[-2:]
-    H, V = v.shape[-2:]
-    _require(k.shape == q.shape and v.shape[:-2] == lead and out.shape == v.shape and
-             beta.shape == lead + (H,), "shapes: q, k [.., Hk, K], v, out [.., H, V], beta [.., H]")
-    _require(k.dtype == q.dtype and v.dtype == q.dtype, "q, k and v must have one dtype")
-    if g.dim() == v.dim():
-        _require(g.shape == lead + (H, K), "g must be [.., H, K] or [.., H]")
-        gate = K
-    else:
-        _require(g.shape == beta.shape, "g must be [.., H, K] or [.., H]")
-        gate = 1
-    _float32(g=g, beta=beta, state=state)
-    _int32(n, slot=slot, init=init)
+    qs, vs = q.shape, v.shape
+    if len(vs) != len(qs):
+        _bad("shapes: q, k [.., Hk, K], v, out [.., H, V], beta [.., H]")
+    lead, Hk, K = qs[:-2], qs[-2], qs[-1]
+    H, V = vs[-2:]
+    rows = lead + (H,)
+    if k.shape != qs or vs != rows + (V,) or out.shape != vs or beta.shape != rows:
+        _bad("shapes: q, k [.., Hk, K], v, out [.., H, V], beta [.., H]")
+    if not q.dtype == k.dtype == v.dtype:
+        _bad("q, k and v must have one dtype")
+    gate = K if g.dim() == len(vs) else 1
+    if g.shape != (rows + (K,) if gate == K else rows):
+        _bad("g must be [.., H, K] or [.., H]")
+    _float32("g", g)
+    _float32("beta", beta)
+    _float32("state", state)
+    _int32(n, "slot", slot)
+    _int32(n, "init", init)
     slots = 0
     if state is not None:
+        if state.shape[1:] != (H, K, V):
+            _bad("state must be [slots, H, K, V]")
         slots = state.shape[0]
-        _require(state.shape == (slots, H, K, V), "state must be [slots, H, K, V]")
     if scale is None:
         scale = K ** -0.5
     return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), _code(q), g.data_ptr(), beta.data_ptr(),
              out.data_ptr(), _code(out)) + req +
             (H, Hk, K, V, gate, _addr(state), _addr(slot), _addr(init), slots, scale), s)
+
+
+def _empty_as(t, dtype, stream):
+    """An output shaped like t, allocated for the stream of the call."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    with _alloc_stream(stream):
+        return torch.empty_like(t, dtype=dtype)
 
 
 def _workspace_args(workspace):
@@ -242,12 +273,14 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, state=None, slot=None, init=None,
             out_dtype=None, stream=None):
     """Convenience form of kda_prefill: returns out (``out_dtype``, default v's
     dtype) and allocates the workspace with torch."""
-    with _alloc_stream(stream):
-        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
-        n = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-        tokens = v.shape[0] * v.shape[1] if cu_seqlens is None else v.shape[0]
-        nbytes = kda_prefill_workspace_size(tokens, n, v.shape[-2], q.shape[-1], v.shape[-1])
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=v.device) if nbytes else None
+    out = _empty_as(v, out_dtype, stream)
+    n = v.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    H, V = v.shape[-2:]
+    nbytes = kda_prefill_workspace_size(v.numel() // max(H * V, 1), n, H, q.shape[-1], V)
+    ws = None
+    if nbytes:
+        with _alloc_stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=v.device)
     kda_prefill(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, ws, stream)
     return out
 
@@ -278,8 +311,7 @@ def recurrent(q, k, v, g, beta, cu_seqlens=None, state=None, slot=None, init=Non
               out_dtype=None, stream=None):
     """Convenience form of kda_recurrent: returns out (``out_dtype``, default
     v's dtype)."""
-    with _alloc_stream(stream):
-        out = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
+    out = _empty_as(v, out_dtype, stream)
     kda_recurrent(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, stream)
     return out
 
@@ -289,11 +321,12 @@ def recurrent(q, k, v, g, beta, cu_seqlens=None, state=None, slot=None, init=Non
 def kda_gated_norm(o, z, norm_w, out, eps_norm=1e-6, stream=None) -> None:
     """out = o / sqrt(mean(o^2) + eps) * norm_w * sigmoid(z) over the last
     dimension of o, z, out [.., H, d]; out may be o."""
-    s = _place(o, stream, z, norm_w, out)
-    _require(o.dim() >= 2 and z.shape == o.shape and out.shape == o.shape and
-             norm_w.shape == o.shape[-1:], "shapes: o, z, out [.., H, d], norm_w [d]")
-    _require(z.dtype == o.dtype, "z must have o's dtype")
-    _float32(norm_w=norm_w)
+    s = _place(stream, (o, z, norm_w, out))
+    if o.dim() < 2 or z.shape != o.shape or out.shape != o.shape or norm_w.shape != o.shape[-1:]:
+        _bad("shapes: o, z, out [.., H, d], norm_w [d]")
+    if z.dtype != o.dtype:
+        _bad("z must have o's dtype")
+    _float32("norm_w", norm_w)
     H, d = o.shape[-2:]
     rows = o.numel() // (H * d) if H * d else 0
     _check(_lib.kda_gated_norm(o.data_ptr(), z.data_ptr(), _code(o), norm_w.data_ptr(),
@@ -303,7 +336,6 @@ def kda_gated_norm(o, z, norm_w, out, eps_norm=1e-6, stream=None) -> None:
 def gated_norm(o, z, norm_w, eps_norm=1e-6, out_dtype=None, stream=None):
     """Convenience form of kda_gated_norm: returns out (``out_dtype``, default
     o's dtype)."""
-    with _alloc_stream(stream):
-        out = torch.empty(o.shape, dtype=out_dtype or o.dtype, device=o.device)
+    out = _empty_as(o, out_dtype, stream)
     kda_gated_norm(o, z, norm_w, out, eps_norm, stream)
     return out
