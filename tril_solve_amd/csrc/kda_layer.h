@@ -40,7 +40,20 @@ struct DeltaProblem {
     int32_t gate_stride;  // elements of g per (token, head): K or 1
     int32_t out_dt;       // kda_dtype of out
     float scale;
+    // Prompts cut into segments of `seg` tokens (0: not cut), at most `segs` of
+    // them over all requests (chunked form only; see prefill_segments)
+    int32_t seg, segs;
+    float *seg_state;  // [segs, H, K, V] the state behind a segment
+    float *seg_map;    // [segs, H, K, K] what a segment makes of the state before it
+    float *seg_first;  // [num_seqs, H, K, V] the state before the first segment
 };
+
+// Tokens per segment of a call on these sizes, or 0 where cutting does not pay.
+int32_t prefill_segments(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t V);
+// Most segments that the requests of a call can have.
+inline int64_t prefill_max_segments(int64_t total_tokens, int64_t num_seqs, int32_t seg) {
+    return total_tokens / seg + num_seqs;
+}
 
 struct ConvProblem {
     Requests req;

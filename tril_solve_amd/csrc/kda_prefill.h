@@ -382,7 +382,48 @@ __device__ __forceinline__ void substitute(const float (&a)[16], float (&x)[16])
 }
 #undef KDA_FMAC
 
-template <class EI, int K, int OUT>
+// Segment j of all requests' segments in order (every wavefront finds it by
+// itself; at most kWave requests). A request without tokens has one segment.
+// Segments past `segs`, which only a malformed cu_seqlens can have, do not
+// exist.
+constexpr int kMaxCutRequests = kWave;
+struct Segment {
+    int request, first, count, at;  // segments [first, first + count) of the request; at < count
+};
+__device__ __forceinline__ int lane_prefix(int x) {  // inclusive sum over the wavefront
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int y = __shfl_up(x, d, kWave);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+__device__ __forceinline__ int segments_to_lane(const DeltaProblem &p, int &own) {
+    const int lane = threadIdx.x & (kWave - 1);
+    own = 0;
+    if (lane < p.req.num_seqs) own = max(1, (request_rows(p.req, lane).y + p.seg - 1) / p.seg);
+    return lane_prefix(own);
+}
+__device__ __forceinline__ Segment find_segment(const DeltaProblem &p, int j) {
+    int own;
+    const int upto = segments_to_lane(p, own);
+    const uint64_t past = __ballot(upto > j);
+    if (past == 0) return Segment{-1, 0, 0, 0};
+    const int n = __builtin_ctzll(past);
+    Segment s;
+    s.request = n;
+    s.count = __builtin_amdgcn_readlane(own, n);
+    s.first = __builtin_amdgcn_readlane(upto, n) - s.count;
+    s.at = j - s.first;
+    return s;
+}
+
+// SUM: instead of outputs, what the segments but every request's last one do
+// to the state, S_after = M S_before + B, as the columns [B | M] of a V + K
+// columns wide state: B starts from zero (a first segment's from the request's
+// state, and then is S_after), M from the identity and with V = 0.
+template <class EI, int K, int OUT, bool SUM>
 __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProblem p) {
     typedef PreLds<K, OUT> L;
     constexpr int NT = K / 16;  // state row tiles
@@ -396,18 +437,28 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 
     const int lane0 = threadIdx.x & (kWave - 1);
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int n = blockIdx.x / p.H, h = blockIdx.x - n * p.H;
+    const int j = blockIdx.x / p.H, h = blockIdx.x - j * p.H;
+    Segment sg = {j, j, 1, 0};
+    if (p.seg != 0) {
+        sg = find_segment(p, j);
+        if (sg.request < 0 || (SUM && sg.at + 1 == sg.count)) return;
+        if (SUM && sg.at == 0 && (int)(blockIdx.y * kPreWaves * kPreCols) >= p.V) return;
+    }
+    const int n = sg.request;
     const int hk = h / (p.H / p.Hk);
     const int2 rows = request_rows(p.req, n);
-    const int len_all = __builtin_amdgcn_readfirstlane(rows.y);
-    const long row_first = __builtin_amdgcn_readfirstlane(rows.x);
+    const int skip = sg.at * p.seg;  // the request's tokens before the segment
+    const int len_all = __builtin_amdgcn_readfirstlane(
+        sg.at + 1 < sg.count ? p.seg : rows.y - skip);
+    const long row_first = __builtin_amdgcn_readfirstlane(rows.x + skip);
     const bool keep = p.pool.base != nullptr;
     const int slot = __builtin_amdgcn_readfirstlane(keep ? request_slot(p.pool, n) : 0);
 
     // this wavefront's columns: tile ct holds column col + ct of each lane
     const int col0 = (blockIdx.y * kPreWaves + wv) * kPreCols;
-    const bool cols = col0 < p.V;  // V is a multiple of 32
-    const int col = (cols ? col0 : 0) + 2 * (lane0 & 15);
+    const bool map = SUM && col0 >= p.V;  // V is a multiple of 32
+    const bool cols = SUM ? col0 < p.V + (sg.at ? K : 0) : col0 < p.V;
+    const int col = (cols ? map ? col0 - p.V : col0 : 0) + 2 * (lane0 & 15);
 
     // Token tensors from the request's first row and this head on, and the
     // bytes between their rows (fewer than 2^21).
@@ -437,7 +488,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 kNontemporal);
     };
     if (slot < 0) {  // padding: zero outputs, no state
-        if (cols)
+        if (!SUM && cols)
             for (int t = lane0 >> 4; t < len_all; t += 4)
 #pragma unroll
                 for (int c = 0; c < 2 * OE; c += 4)
@@ -449,22 +500,46 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
     // 32 (rt / 2) + 8 g4 + 4 (rt % 2) + s
     auto state_row = [](int rt, int s) { return 32 * (rt >> 1) + 4 * (rt & 1) + s; };
     f4 S[NT][2];
-    float *pool = p.pool.base + (((long)slot * p.H + h) * K + 8 * (lane0 >> 4)) * p.V + col;
-    if (cols && request_continues(p.pool, n)) {
+    // [K, V] of this head in slot `at` of a tensor [.., H, K, V], this lane's part
+    auto state_at = [&](float *base, int at) {
+        return base + (((long)at * p.H + h) * K + 8 * (lane0 >> 4)) * p.V + col;
+    };
+    auto load_state = [&](const float *src) {
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const f2 v = __builtin_nontemporal_load(
-                    reinterpret_cast<const f2 *>(pool + (long)state_row(rt, s) * p.V));
+                    reinterpret_cast<const f2 *>(src + (long)state_row(rt, s) * p.V));
                 S[rt][0][s] = v[0];
                 S[rt][1][s] = v[1];
             }
+    };
+    auto store_state = [&](float *dst, int stride) {
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                __builtin_nontemporal_store(
+                    f2{S[rt][0][s], S[rt][1][s]},
+                    reinterpret_cast<f2 *>(dst + (long)state_row(rt, s) * stride));
+    };
+    if (!SUM && sg.count > 1 && cols) {
+        load_state(sg.at == 0 ? state_at(p.seg_first, n) : state_at(p.seg_state, j - 1));
+    } else if (cols && sg.at == 0 && request_continues(p.pool, n)) {
+        load_state(state_at(p.pool.base, slot));
     } else {
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
-            S[rt][0] = S[rt][1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
+                    S[rt][ct][s] =
+                        map && 8 * (lane0 >> 4) + state_row(rt, s) == col + ct ? 1.0f : 0.0f;
     }
+    // the last segment of the later pass overwrites the pool's state
+    if (SUM && sg.at == 0 && cols) store_state(state_at(p.seg_first, n), p.V);
 
     // entries of the inverse and of P that no chunk writes are zero
     for (int i = threadIdx.x; i < (3 + NQ) * L::T32 / 4; i += kPreThreads)
@@ -495,7 +570,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
             kraw[i].load(rk, (first + i) * ks + c4 * EI::kBytes);
-            qraw[i].load(rq, (first + i) * ks + c4 * EI::kBytes);
+            if constexpr (!SUM) qraw[i].load(rq, (first + i) * ks + c4 * EI::kBytes);
         }
         if (wv == 3)
             braw = lane < len ? p.beta[(row_first + t0 + lane) * p.H + h] : 0.0f;
@@ -599,7 +674,8 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int i = 0; i < TPL; ++i) {
                 const f4 e = exp2(er[i] + mid), k = kraw[i].all();
                 put_row.template operator()<2>(L::KR, tok + i, k * e);
-                put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
+                if constexpr (!SUM)
+                    put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
                 put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
             }
         } else {
@@ -607,7 +683,8 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int i = 0; i < TPL; ++i) {
                 const int at = 4 * ((tok + i) * K + ch);
                 *reinterpret_cast<f4 *>(lds + L::SK + at) = kraw[i].all();
-                *reinterpret_cast<f4 *>(lds + L::SQ + at) = qraw[i].all() * p.scale;
+                if constexpr (!SUM)
+                    *reinterpret_cast<f4 *>(lds + L::SQ + at) = qraw[i].all() * p.scale;
                 *reinterpret_cast<f4 *>(lds + L::SA + at) = exp2(graw[i] * kLog2E);
             }
         }
@@ -633,12 +710,12 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             };
             if (wv < 2) {
                 m[0] = block.template operator()<3, 2>(L::KR, wv, wv);
-            } else if (wv == 2) {
+            } else if (wv == 3) {
+                m[0] = block.template operator()<3, 2>(L::KR, 1, 0);
+                if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
+            } else if constexpr (!SUM) {
                 m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
                 m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 1);
-            } else {
-                m[0] = block.template operator()<3, 2>(L::KR, 1, 0);
-                m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
             }
         } else {
             // running products of the decays from token j on
@@ -661,10 +738,10 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                         const int at = i * K + lane + 64 * c;
                         if (i > j) f[c] *= sa[at];
                         a = __builtin_fmaf(f[c], sk[at], a);
-                        b = __builtin_fmaf(f[c], sq[at], b);
+                        if constexpr (!SUM) b = __builtin_fmaf(f[c], sq[at], b);
                     }
                     a = sum64(a);
-                    b = sum64(b);
+                    if constexpr (!SUM) b = sum64(b);
                     if (lane == 0) {
                         sm[i * kPreC + j] = a;
                         sp[i * kPreC + j] = b;
@@ -718,22 +795,25 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 put_pair.template operator()<3>(L::TM, 16 * wv + 4 * g4 + s, 16 * wv + n16, y[s],
                                                 y[s + 1]);
         } else if (wv == 2) {
+            if constexpr (!SUM)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int s = 0; s < 4; s += 2) {
-                    const int r = 4 * g4 + s;
-                    put_pair.template operator()<NQ>(L::PM, 16 * b + r, 16 * b + n16,
-                                                     n16 <= r ? m[b][s] : 0.0f,
-                                                     n16 <= r + 1 ? m[b][s + 1] : 0.0f);
-                }
+                    for (int s = 0; s < 4; s += 2) {
+                        const int r = 4 * g4 + s;
+                        put_pair.template operator()<NQ>(L::PM, 16 * b + r, 16 * b + n16,
+                                                         n16 <= r ? m[b][s] : 0.0f,
+                                                         n16 <= r + 1 ? m[b][s + 1] : 0.0f);
+                    }
         } else {
             const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 + 4 * g4);
 #pragma unroll
             for (int s = 0; s < 4; s += 2) {
                 put_pair.template operator()<2>(L::TM, 16 + 4 * g4 + s, n16, -b4[s] * m[0][s],
                                                 -b4[s + 1] * m[0][s + 1]);
-                put_pair.template operator()<NQ>(L::PM, 16 + 4 * g4 + s, n16, m[1][s], m[1][s + 1]);
+                if constexpr (!SUM)
+                    put_pair.template operator()<NQ>(L::PM, 16 + 4 * g4 + s, n16, m[1][s],
+                                                     m[1][s + 1]);
             }
         }
         if (far) {
@@ -773,7 +853,8 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 before += g2[i];
                 const f4 e = exp2(before);
                 put_row.template operator()<2>(L::KR, tok + i, kraw[i].all() * e);
-                put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
+                if constexpr (!SUM)
+                    put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
             }
 #pragma unroll
             for (int i = TPL - 1; i >= 0; --i) {
@@ -784,7 +865,10 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         // the values of this wavefront's columns
         RawC<EI, 2> vraw[2][4];
         {
-            const Rsrc rv = rows_of(vb + (long)t0 * vs, vs, p.V * EI::kBytes, len);
+            // (no row at all for M's columns: V = 0)
+            const Rsrc rv = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<char *>(vb + (long)t0 * vs), 0,
+                map ? 0 : (len - 1) * vs + p.V * EI::kBytes, kRsrcWord3);
             const uint32_t at = 4 * g4 * vs + col * EI::kBytes;
 #pragma unroll
             for (int I = 0; I < 2; ++I)
@@ -807,7 +891,8 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         auto read_rows = [&](int j) {  // k-step j / 2, row tile j % 2
             const int at = 16 * (j & 1) * L::RS;
             ka_op[j & 1] = row_operand.template operator()<2>(L::KR + at, j >> 1);
-            qa_op[j & 1] = row_operand.template operator()<NQ>(L::QR + at, j >> 1);
+            if constexpr (!SUM)
+                qa_op[j & 1] = row_operand.template operator()<NQ>(L::QR + at, j >> 1);
         };
         auto read_em = [&](int kk) {
 #pragma unroll
@@ -834,10 +919,12 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) kS[I][ct] = mul<3>(ka_op[I], b[kk & 1][ct], kS[I][ct]);
+            if constexpr (!SUM)
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) o[I][ct] = mul<MQ>(qa_op[I], b[kk & 1][ct], o[I][ct]);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2 + NQ, 0);  // LDS reads
-            interleave<6 + 2 * MQ, 3>();
+                for (int ct = 0; ct < 2; ++ct)
+                    o[I][ct] = mul<MQ>(qa_op[I], b[kk & 1][ct], o[I][ct]);
+            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 2 : 2 + NQ, 0);  // LDS reads
+            interleave<SUM ? 6 : 6 + 2 * MQ, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time: U_0 = X_00 R_0, U_1 = X_11 (R_1 - L_10 U_0)
@@ -868,17 +955,17 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int ct = 0; ct < 2; ++ct) {
                 h0[ct] = split4<3>(x[ct]);
                 x[ct] = mul<3>(x1, join(h0[ct], none), R[1][ct]);
-                o[0][ct] = mul<MQ>(p0, join(h0[ct], none), o[0][ct]);
+                if constexpr (!SUM) o[0][ct] = mul<MQ>(p0, join(h0[ct], none), o[0][ct]);
             }
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(x1, join(none, split4<3>(x[ct])), z);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 u[ct] = join(h0[ct], split4<3>(x[ct]));
-                o[1][ct] = mul<MQ>(p1, u[ct], o[1][ct]);
+                if constexpr (!SUM) o[1][ct] = mul<MQ>(p1, u[ct], o[1][ct]);
             }
         }
-        {
+        if constexpr (!SUM) {
             const Rsrc ro = rows_of(ob + (long)t0 * os, os, p.V * OE, len);
             const uint32_t at = 4 * g4 * os + col * OE;
 #pragma unroll
@@ -932,35 +1019,40 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (keep && cols) {
-#pragma unroll
-        for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                __builtin_nontemporal_store(
-                    f2{S[rt][0][s], S[rt][1][s]},
-                    reinterpret_cast<f2 *>(pool + (long)state_row(rt, s) * p.V));
+    if (SUM && cols) {
+        if (map)
+            store_state(p.seg_map + (((long)j * p.H + h) * K + 8 * (lane0 >> 4)) * K + col, K);
+        else
+            store_state(state_at(p.seg_state, j), p.V);
+    } else if (keep && cols && sg.at + 1 == sg.count) {
+        store_state(state_at(p.pool.base, slot), p.V);
     }
 }
 
 template <class EI>
-hipError_t launch_prefill_of(const DeltaProblem &p, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.req.num_seqs * p.H),
-                    (unsigned)((p.V + kPreWaves * kPreCols - 1) / (kPreWaves * kPreCols)));
-    auto go = [&]<int K, int OUT>() {
-        hipLaunchKernelGGL((kda_prefill_kernel<EI, K, OUT>), grid, dim3(kPreThreads), 0, stream, p);
+hipError_t launch_prefill_of(const DeltaProblem &p, bool sum, hipStream_t stream) {
+    const int64_t parts = p.seg != 0 ? p.segs : p.req.num_seqs;
+    const int cols = p.V + (sum ? p.K : 0);
+    const dim3 grid((unsigned)(parts * p.H),
+                    (unsigned)((cols + kPreWaves * kPreCols - 1) / (kPreWaves * kPreCols)));
+    auto go = [&]<int K, int OUT, bool SUM>() {
+        hipLaunchKernelGGL((kda_prefill_kernel<EI, K, OUT, SUM>), grid, dim3(kPreThreads), 0,
+                           stream, p);
         return hipGetLastError();
     };
-    auto with_k = [&]<int OUT>() {
-        return p.K == 64 ? go.template operator()<64, OUT>() : go.template operator()<128, OUT>();
+    auto with_k = [&]<int OUT, bool SUM>() {
+        return p.K == 64 ? go.template operator()<64, OUT, SUM>()
+                         : go.template operator()<128, OUT, SUM>();
     };
-    return p.out_dt == 0   ? with_k.template operator()<0>()
-           : p.out_dt == 1 ? with_k.template operator()<1>()
-                           : with_k.template operator()<2>();
+    // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
+    return sum             ? with_k.template operator()<1, true>()
+           : p.out_dt == 0 ? with_k.template operator()<0, false>()
+           : p.out_dt == 1 ? with_k.template operator()<1, false>()
+                           : with_k.template operator()<2, false>();
 }
 
-hipError_t launch_prefill_f32(const DeltaProblem &p, hipStream_t stream);
-hipError_t launch_prefill_bf16(const DeltaProblem &p, hipStream_t stream);
-hipError_t launch_prefill_f16(const DeltaProblem &p, hipStream_t stream);
+hipError_t launch_prefill_f32(const DeltaProblem &p, bool sum, hipStream_t stream);
+hipError_t launch_prefill_bf16(const DeltaProblem &p, bool sum, hipStream_t stream);
+hipError_t launch_prefill_f16(const DeltaProblem &p, bool sum, hipStream_t stream);
 
 }  // namespace kda

@@ -4,8 +4,8 @@
 
 namespace kda {
 
-hipError_t launch_prefill_bf16(const DeltaProblem &p, hipStream_t stream) {
-    return launch_prefill_of<BF16>(p, stream);
+hipError_t launch_prefill_bf16(const DeltaProblem &p, bool sum, hipStream_t stream) {
+    return launch_prefill_of<BF16>(p, sum, stream);
 }
 
 }  // namespace kda

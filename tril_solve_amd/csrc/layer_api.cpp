@@ -140,14 +140,44 @@ bool idle(const DeltaProblem &p) {
     return p.req.num_seqs == 0 || (p.req.total_tokens == 0 && p.pool.base == nullptr);
 }
 
+// Bytes with which a call cuts its prompts into segments of seg tokens.
+size_t prefill_bytes(int64_t tokens, int64_t num_seqs, int32_t H, int32_t K, int32_t V,
+                     int32_t seg) {
+    if (seg == 0) return 0;
+    const size_t segs = (size_t)prefill_max_segments(tokens, num_seqs, seg);
+    return (size_t)H * K * 4 * (segs * (V + K) + (size_t)num_seqs * V);
+}
+
 kda_status prefill(const DeltaArgs &a, const int32_t *cu, int64_t num_seqs, int64_t tokens,
                    int64_t dense_T, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     DeltaProblem p;
     const kda_status st = check_delta(p, a, cu, num_seqs, tokens, dense_T);
     if (st != KDA_OK) return st;
-    if (workspace && !aligned(workspace, 16)) return KDA_ERR_INVALID_ARG;
-    (void)workspace_bytes;
+    if ((!workspace && workspace_bytes) || (workspace && !aligned(workspace, 16)))
+        return KDA_ERR_INVALID_ARG;
     if (idle(p)) return KDA_OK;
+    const int32_t seg = prefill_segments(tokens, num_seqs, a.H, a.V);
+    const size_t need = prefill_bytes(tokens, num_seqs, a.H, a.K, a.V, seg);
+    if (need && workspace_bytes >= need) {
+        const size_t T = (size_t)tokens, e = dtype_bytes(a.in_dtype);
+        const Span used[] = {{a.q, T * a.Hk * a.K * e},
+                             {a.k, T * a.Hk * a.K * e},
+                             {a.v, T * a.H * a.V * e},
+                             {a.g, T * a.H * a.gate_dim * 4},
+                             {a.beta, T * (size_t)a.H * 4},
+                             {a.out, T * a.H * a.V * dtype_bytes(a.out_dtype)},
+                             {cu, (size_t)(num_seqs + 1) * 4},
+                             {a.slot, (size_t)num_seqs * 4},
+                             {a.init, (size_t)num_seqs * 4},
+                             {a.state, (size_t)(a.state ? a.num_slots : 0) * a.H * a.K * a.V * 4}};
+        if (overlaps_any({workspace, need}, used)) return KDA_ERR_INVALID_ARG;
+        p.seg = seg;
+        p.segs = (int32_t)prefill_max_segments(tokens, num_seqs, seg);
+        const size_t states = (size_t)a.H * a.K * a.V;
+        p.seg_state = static_cast<float *>(workspace);
+        p.seg_map = p.seg_state + (size_t)p.segs * states;
+        p.seg_first = p.seg_map + (size_t)p.segs * a.H * a.K * a.K;
+    }
     return launch_prefill(p, (int)a.in_dtype, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
@@ -272,7 +302,8 @@ kda_status kda_prefill_workspace_size(int64_t total_tokens, int64_t num_seqs, in
     if (total_tokens > kMaxTokens || num_seqs > kMaxTokens || H > kMaxHeads ||
         (K != 64 && K != 128) || V % 32 != 0 || V > 256 || num_seqs > kMaxPairs / H)
         return KDA_ERR_UNSUPPORTED;
-    *bytes = 0;
+    *bytes = prefill_bytes(total_tokens, num_seqs, H, K, V,
+                           prefill_segments(total_tokens, num_seqs, H, V));
     return KDA_OK;
 }
 
