@@ -71,7 +71,8 @@ template <int N>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&part)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const uint32_t w = Elem<BF16>::pack(a, b);
+        uint32_t w = Elem<BF16>::pack(a, b);
+        asm("" : "+v"(w));  // else a's own conversion is made a second time
         part[i] = w;
         if (i + 1 < N) {
             a -= __builtin_bit_cast(float, w << 16);
@@ -94,13 +95,6 @@ __device__ __forceinline__ Half<N> split4(f4 x) {
     for (int i = 0; i < N; ++i) h.p[i] = w2{a[i], b[i]};
     return h;
 }
-template <int N>
-__device__ __forceinline__ Half<N> zero_half() {
-    Half<N> h;
-#pragma unroll
-    for (int i = 0; i < N; ++i) h.p[i] = w2{0u, 0u};
-    return h;
-}
 // An operand: eight values, N parts.
 template <int N>
 struct Operand {
@@ -112,6 +106,14 @@ __device__ __forceinline__ Operand<N> join(const Half<N> &a, const Half<N> &b) {
 #pragma unroll
     for (int i = 0; i < N; ++i) o.p[i] = w4{a.p[i][0], a.p[i][1], b.p[i][0], b.p[i][1]};
     return o;
+}
+template <int N>
+__device__ __forceinline__ Half<N> half_of(const Operand<N> &o, int which) {
+    Half<N> h;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        h.p[i] = which ? w2{o.p[i][2], o.p[i][3]} : w2{o.p[i][0], o.p[i][1]};
+    return h;
 }
 __device__ __forceinline__ f4 mfma(w4 a, w4 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a),
@@ -130,6 +132,24 @@ __device__ __forceinline__ f4 mul(const Operand<NA> &a, const Operand<NB> &b, f4
         c = mfma(a.p[1], b.p[0], c);
         c = mfma(a.p[0], b.p[1], c);
     }
+    return mfma(a.p[0], b.p[0], c);
+}
+
+// c + a b over one half (16 of the reduction) of an operand.
+__device__ __forceinline__ f4 mfma(w2 a, w2 b, f4 c) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a),
+                                                     __builtin_bit_cast(s4, b), c, 0, 0, 0);
+}
+template <int M, int NA, int NB>
+__device__ __forceinline__ f4 mul(const Half<NA> &a, const Half<NB> &b, f4 c) {
+    if constexpr (M == 6) {
+        c = mfma(a.p[2], b.p[0], c);
+        c = mfma(a.p[0], b.p[2], c);
+        c = mfma(a.p[1], b.p[1], c);
+    }
+    c = mfma(a.p[1], b.p[0], c);
+    c = mfma(a.p[0], b.p[1], c);
     return mfma(a.p[0], b.p[0], c);
 }
 
@@ -248,8 +268,8 @@ struct PreLds {
     static constexpr int PM = TM + 3 * T32;
     static constexpr int PATCH = PM + NQ * T32;
     static constexpr int TOT = PATCH + 2 * 16 * kPatch * 4;
-    // per channel: what S' is of S and the new S of S' + ... (steep: 1), and
-    // for a steep chunk e^{G_32}
+    // per channel: what S' is of the state in registers (steep: 1), what that
+    // state owes (see `apart`), and for a steep chunk e^{G_32}
     static constexpr int EM = TOT + kPreWaves * K * 4, EG = EM + K * 4, EF = EG + K * 4;
     static constexpr int BETA = EF + K * 4;
     static constexpr int kBytes = BETA + 2 * kPreC * 4;
@@ -577,6 +597,9 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
     };
     if (len_all > 0) load_rows(0);
 
+    // the decay (of this lane's channels, a power of two) that the state in
+    // registers still has to take: G_32 - m of the chunk before
+    f4 owed = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int t0 = 0, buf = 0; t0 < len_all; t0 += kPreC, buf ^= 1) {
         const int len = min(kPreC, len_all - t0);
         // the lane made opaque: the many addresses derived from it are formed
@@ -649,27 +672,41 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         for (int w = 0; w < kPreWaves; ++w)
             wt[w] = *reinterpret_cast<const f4 *>(tots + w * K + ch);
         const f4 first = wt[0] + wt[1], second = wt[2] + wt[3];  // m, G_32 - m
-        bool steep = false;  // (NaN or infinite where any gate is)
+        const f4 both = owed + first;
+        bool steep = false, deep = false;  // (steep: NaN or infinite where any gate is)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
             steep |= !(__builtin_fabsf(first[e]) <= kSteep) |
                      !(__builtin_fabsf(second[e]) <= kSteep);
+            deep |= __builtin_fabsf(both[e]) > 125.0f;
+        }
         const bool far = __ballot(steep) != 0;  // the same in every wavefront
+        const bool apart = far | (__ballot(deep) != 0);
         if (wv == 0 && grp == 0) {
             const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
-            *reinterpret_cast<f4 *>(lds + L::EM + 4 * ch) = far ? one : exp2(first);
-            *reinterpret_cast<f4 *>(lds + L::EG + 4 * ch) = far ? one : exp2(second);
+            *reinterpret_cast<f4 *>(lds + L::EM + 4 * ch) =
+                far ? one : exp2(apart ? first : both);
+            *reinterpret_cast<f4 *>(lds + L::EG + 4 * ch) = exp2(owed);
             *reinterpret_cast<f4 *>(lds + L::EF + 4 * ch) = exp2(first + second);
         }
+        owed = far ? f4{0.0f, 0.0f, 0.0f, 0.0f} : second;
         if (!far) {
             // from the chunk's middle to this lane's first token
-            f4 mid = wv == 0 ? -wt[1] : wv == 3 ? wt[2] : f4{0.0f, 0.0f, 0.0f, 0.0f};
+            f4 mid = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (wv >= 2) {
+                if (wv == 3) mid = wt[2];
 #pragma unroll
-            for (int g = 0; g < GRP; ++g)
+                for (int g = 0; g + 1 < GRP; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mid[e] += wv >= 2 ? (g < grp ? sums[g][e] : 0.0f)
-                                      : (g >= grp ? -sums[g][e] : 0.0f);
+                    for (int e = 0; e < 4; ++e) mid[e] += g < grp ? sums[g][e] : 0.0f;
+            } else {
+                mid = -sums[GRP - 1];
+                if (wv == 0) mid -= wt[1];
+#pragma unroll
+                for (int g = 0; g + 1 < GRP; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mid[e] -= g >= grp ? sums[g][e] : 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < TPL; ++i) {
                 const f4 e = exp2(er[i] + mid), k = kraw[i].all();
@@ -763,7 +800,8 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 }
             }
         }
-        // the inverse's diagonal blocks and -L_10, and P, as A operands
+        // the inverse's diagonal blocks times beta (of their column), -L_10 /
+        // beta (of the row) and P, as A operands
         if (wv < 2) {
             float *patch = reinterpret_cast<float *>(lds + L::PATCH) + wv * 16 * L::kPatch;
             const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 * wv + 4 * g4);
@@ -783,12 +821,13 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 for (int s = 0; s < 4; ++s) arow[4 * j + s] = v[s];
             }
             substitute(arow, x);
+            const float bc = beta[16 * wv + n16];
             f4 y;  // rows 4 g4 .. + 3 (two opaque bits: selects, not a switch on g4)
             const bool odd = opaque_lane(g4 & 1), high = opaque_lane(g4 >> 1);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const float a = odd ? x[4 + s] : x[s], b = odd ? x[12 + s] : x[8 + s];
-                y[s] = high ? b : a;
+                y[s] = (high ? b : a) * bc;
             }
 #pragma unroll
             for (int s = 0; s < 4; s += 2)
@@ -806,11 +845,10 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                                                          n16 <= r + 1 ? m[b][s + 1] : 0.0f);
                     }
         } else {
-            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 + 4 * g4);
 #pragma unroll
             for (int s = 0; s < 4; s += 2) {
-                put_pair.template operator()<2>(L::TM, 16 + 4 * g4 + s, n16, -b4[s] * m[0][s],
-                                                -b4[s + 1] * m[0][s + 1]);
+                put_pair.template operator()<2>(L::TM, 16 + 4 * g4 + s, n16, -m[0][s],
+                                                -m[0][s + 1]);
                 if constexpr (!SUM)
                     put_pair.template operator()<NQ>(L::PM, 16 + 4 * g4 + s, n16, m[1][s],
                                                      m[1][s + 1]);
@@ -905,6 +943,15 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int t = 0; t < 2; ++t) S[2 * kk + t][ct] *= em[t];
             b[kk & 1][ct] = join(split4<NQ>(S[2 * kk][ct]), split4<NQ>(S[2 * kk + 1][ct]));
         };
+        if (apart) {
+#pragma unroll
+            for (int rt = 0; rt < NT; ++rt) {
+                const f4 e =
+                    *reinterpret_cast<const f4 *>(lds + L::EG + 4 * (8 * g4 + state_row(rt, 0)));
+                S[rt][0] *= e;
+                S[rt][1] *= e;
+            }
+        }
         read_em(0);
         read_rows(0);
         split_state(0, 0);
@@ -927,38 +974,35 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             interleave<SUM ? 6 : 6 + 2 * MQ, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
-        // U, 16 rows at a time: U_0 = X_00 R_0, U_1 = X_11 (R_1 - L_10 U_0)
+        // U, 16 rows at a time, X the inverse's diagonal blocks times beta:
+        // R = V - (k e^G) S, U_0 = X_00 R_0, U_1 = X_11 (R_1 - (L_10 / beta) U_0)
         f4 R[2][2];
 #pragma unroll
-        for (int I = 0; I < 2; ++I) {
-            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 * I + 4 * g4);
+        for (int I = 0; I < 2; ++I)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
-                    R[I][ct][s] = b4[s] * (vraw[I][s].at(ct) - kS[I][ct][s]);
-        }
+                for (int ct = 0; ct < 2; ++ct) R[I][ct][s] = vraw[I][s].at(ct) - kS[I][ct][s];
         Operand<3> u[2];
         {
             const auto x0 = tok_operand.template operator()<3>(L::TM);
             const auto x1 = tok_operand.template operator()<3>(L::TM + 16 * L::TS);
             const auto p0 = tok_operand.template operator()<NQ>(L::PM);
             const auto p1 = tok_operand.template operator()<NQ>(L::PM + 16 * L::TS);
-            const Half<3> none = zero_half<3>();
             Half<3> h0[2];
             f4 x[2];
             // both column tiles step by step, so that one's products cover
             // the other's splits
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(x0, join(split4<3>(R[0][ct]), none), z);
+            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(half_of(x0, 0), split4<3>(R[0][ct]), z);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 h0[ct] = split4<3>(x[ct]);
-                x[ct] = mul<3>(x1, join(h0[ct], none), R[1][ct]);
-                if constexpr (!SUM) o[0][ct] = mul<MQ>(p0, join(h0[ct], none), o[0][ct]);
+                x[ct] = mul<3>(half_of(x1, 0), h0[ct], R[1][ct]);
+                if constexpr (!SUM) o[0][ct] = mul<MQ>(half_of(p0, 0), h0[ct], o[0][ct]);
             }
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(x1, join(none, split4<3>(x[ct])), z);
+            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(half_of(x1, 1), split4<3>(x[ct]), z);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 u[ct] = join(h0[ct], split4<3>(x[ct]));
@@ -974,28 +1018,30 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                 for (int s = 0; s < 4; ++s)
                     put_out(ro, at + (16 * I + s) * os, o[I][0][s], o[I][1][s]);
         }
-        // the state: S = e^{G_32 - m} (S' + (k e^{m - G})^T U); of a steep
+        // the state: S' + (k e^{m - G})^T U, which owes e^{G_32 - m}; of a steep
         // chunk e^{G_32} S + (k e^{G_32 - G})^T U
-        f4 eg[2];
         Operand<3> kt[2];
         // rows of tile rt are channels, reduced over tokens: 4 x 16 blocks of
         // the keys' rows, transposed by the read (lane 4 r + c of 16 gives the
-        // address of 4 channels of token r, lane j gets channel j's 4 tokens)
+        // address of 4 channels of token r, lane j gets channel j's 4 tokens).
+        // Of a row's bytes, bits 4 and 5 are c, 6 and 7 are rt / 2.
         const int trow = 4 * g4 + (n16 >> 2);
+        int tpiece[2];
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+            tpiece[hb] = (trow + 16 * hb) * L::RS +
+                         ((16 * (n16 & 3)) ^ L::swz_row(trow + 16 * hb));
         auto read_state = [&](int rt) {
-            eg[rt & 1] =
-                *reinterpret_cast<const f4 *>(lds + L::EG + 4 * (8 * g4 + state_row(rt, 0)));
-            const int at = 2 * (8 * (n16 & 3) + state_row(rt, 0));
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
+            for (int hb = 0; hb < 2; ++hb) {
+                const char *at = lds + (tpiece[hb] ^ (64 * (rt >> 1)));
 #pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    const int row = trow + 16 * hb;
-                    const w2 x = read_transposed(lds + L::KL + i * L::R32 + row * L::RS +
-                                                 (at ^ L::swz_row(row)));
+                for (int i = 0; i < 3; ++i) {
+                    const w2 x = read_transposed(at + L::KL + i * L::R32 + 8 * (rt & 1));
                     kt[rt & 1].p[i][2 * hb] = x[0];
                     kt[rt & 1].p[i][2 * hb + 1] = x[1];
                 }
+            }
         };
         if (far) {
 #pragma unroll
@@ -1013,10 +1059,23 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             if (rt + 1 < NT) read_state(rt + 1);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct)
-                S[rt][ct] = mul<6>(kt[rt & 1], u[ct], S[rt][ct]) * eg[rt & 1];
-            __builtin_amdgcn_sched_group_barrier(0x100, 7, 0);
-            interleave<12, 2>();
+                S[rt][ct] = mul<6>(kt[rt & 1], u[ct], S[rt][ct]);
+            __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+            interleave<12, 1>();
             __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // what the last chunk owes (the totals' place: no wavefront reads them now)
+    if (len_all > 0) {
+        float *left = reinterpret_cast<float *>(lds + L::TOT);
+        if (wv == 0 && lane0 < K / 4) *reinterpret_cast<f4 *>(left + 4 * lane0) = exp2(owed);
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < NT; ++rt) {
+            const f4 e =
+                *reinterpret_cast<const f4 *>(left + 8 * (lane0 >> 4) + state_row(rt, 0));
+            S[rt][0] *= e;
+            S[rt][1] *= e;
         }
     }
     if (SUM && cols) {
