@@ -119,38 +119,29 @@ __device__ __forceinline__ f4 mfma(w4 a, w4 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a),
                                                    __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
-// c + a b in M = 1, 3 or 6 products, the smallest first.
-template <int M, int NA, int NB>
-__device__ __forceinline__ f4 mul(const Operand<NA> &a, const Operand<NB> &b, f4 c) {
-    static_assert(NA >= (M == 6 ? 3 : M == 3 ? 2 : 1) && NB >= (M == 6 ? 3 : M == 3 ? 2 : 1));
-    if constexpr (M == 6) {
-        c = mfma(a.p[2], b.p[0], c);
-        c = mfma(a.p[0], b.p[2], c);
-        c = mfma(a.p[1], b.p[1], c);
-    }
-    if constexpr (M >= 3) {
-        c = mfma(a.p[1], b.p[0], c);
-        c = mfma(a.p[0], b.p[1], c);
-    }
-    return mfma(a.p[0], b.p[0], c);
-}
-
 // c + a b over one half (16 of the reduction) of an operand.
 __device__ __forceinline__ f4 mfma(w2 a, w2 b, f4 c) {
     typedef short s4 __attribute__((ext_vector_type(4)));
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a),
                                                      __builtin_bit_cast(s4, b), c, 0, 0, 0);
 }
-template <int M, int NA, int NB>
-__device__ __forceinline__ f4 mul(const Half<NA> &a, const Half<NB> &b, f4 c) {
-    if constexpr (M == 6) {
-        c = mfma(a.p[2], b.p[0], c);
-        c = mfma(a.p[0], b.p[2], c);
-        c = mfma(a.p[1], b.p[1], c);
-    }
-    c = mfma(a.p[1], b.p[0], c);
-    c = mfma(a.p[0], b.p[1], c);
-    return mfma(a.p[0], b.p[0], c);
+// c + a b in M = 3 or 6 products, the smallest first; several such sums are
+// formed product by product, since a product that waits for the one before it
+// takes 21 cycles instead of 16. part_a, part_b: the parts of product i.
+constexpr int part_a(int M, int i) {
+    constexpr int a[] = {2, 0, 1, 1, 0, 0};
+    return a[6 - M + i];
+}
+constexpr int part_b(int M, int i) {
+    constexpr int b[] = {0, 2, 1, 0, 1, 0};
+    return b[6 - M + i];
+}
+template <int M, class A, class B>
+__device__ __forceinline__ void mul_columns(const A &a, const B (&b)[2], f4 (&c)[2]) {
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) c[ct] = mfma(a.p[part_a(M, i)], b[ct].p[part_b(M, i)], c[ct]);
 }
 
 // Shapes the schedule of the code around it: N times one matrix instruction
@@ -740,10 +731,15 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                     l[kk] = row_operand.template operator()<N>(left + 16 * bi * L::RS, kk);
                     r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
                 }
-                f4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+                f4 c[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-                for (int kk = 0; kk < K / 32; ++kk) c = mul<M>(l[kk], r[kk], c);
-                return c;
+                for (int kk = 0; kk < K / 32; kk += 2)
+#pragma unroll
+                    for (int i = 0; i < M; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            c[e] = mfma(l[kk + e].p[part_a(M, i)], r[kk + e].p[part_b(M, i)], c[e]);
+                return c[0] + c[1];
             };
             if (wv < 2) {
                 m[0] = block.template operator()<3, 2>(L::KR, wv, wv);
@@ -964,12 +960,19 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             if (j + 1 < K / 16) read_rows(j + 1);
             if (kk + 1 < K / 32) split_state(kk + 1, I);
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
+            if constexpr (SUM) {
+                mul_columns<3>(ka_op[I], b[kk & 1], kS[I]);
+            } else {
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) kS[I][ct] = mul<3>(ka_op[I], b[kk & 1][ct], kS[I][ct]);
-            if constexpr (!SUM)
+                for (int i = 0; i < MQ; ++i)
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
-                    o[I][ct] = mul<MQ>(qa_op[I], b[kk & 1][ct], o[I][ct]);
+                    for (int ct = 0; ct < 2; ++ct) {
+                        const auto &bc = b[kk & 1][ct];
+                        if (i < 3)
+                            kS[I][ct] = mfma(ka_op[I].p[part_a(3, i)], bc.p[part_b(3, i)], kS[I][ct]);
+                        o[I][ct] = mfma(qa_op[I].p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
+                    }
+            }
             __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 2 : 2 + NQ, 0);  // LDS reads
             interleave<SUM ? 6 : 6 + 2 * MQ, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
@@ -989,25 +992,24 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             const auto x1 = tok_operand.template operator()<3>(L::TM + 16 * L::TS);
             const auto p0 = tok_operand.template operator()<NQ>(L::PM);
             const auto p1 = tok_operand.template operator()<NQ>(L::PM + 16 * L::TS);
-            Half<3> h0[2];
-            f4 x[2];
-            // both column tiles step by step, so that one's products cover
-            // the other's splits
+            Half<3> r[2], h0[2];
+            f4 x[2] = {z, z};
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(half_of(x0, 0), split4<3>(R[0][ct]), z);
+            for (int ct = 0; ct < 2; ++ct) r[ct] = split4<3>(R[0][ct]);
+            mul_columns<6>(half_of(x0, 0), r, x);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                h0[ct] = split4<3>(x[ct]);
-                x[ct] = mul<3>(half_of(x1, 0), h0[ct], R[1][ct]);
-                if constexpr (!SUM) o[0][ct] = mul<MQ>(half_of(p0, 0), h0[ct], o[0][ct]);
-            }
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) x[ct] = mul<6>(half_of(x1, 1), split4<3>(x[ct]), z);
+            for (int ct = 0; ct < 2; ++ct) h0[ct] = split4<3>(x[ct]);
+            mul_columns<3>(half_of(x1, 0), h0, R[1]);
+            if constexpr (!SUM) mul_columns<MQ>(half_of(p0, 0), h0, o[0]);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
-                u[ct] = join(h0[ct], split4<3>(x[ct]));
-                if constexpr (!SUM) o[1][ct] = mul<MQ>(p1, u[ct], o[1][ct]);
+                r[ct] = split4<3>(R[1][ct]);
+                x[ct] = z;
             }
+            mul_columns<6>(half_of(x1, 1), r, x);
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) u[ct] = join(h0[ct], split4<3>(x[ct]));
+            if constexpr (!SUM) mul_columns<MQ>(p1, u, o[1]);
         }
         if constexpr (!SUM) {
             const Rsrc ro = rows_of(ob + (long)t0 * os, os, p.V * OE, len);
@@ -1057,9 +1059,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
             if (rt + 1 < NT) read_state(rt + 1);
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct)
-                S[rt][ct] = mul<6>(kt[rt & 1], u[ct], S[rt][ct]);
+            mul_columns<6>(kt[rt & 1], u, S[rt]);
             __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
             interleave<12, 1>();
             __builtin_amdgcn_sched_barrier(0);
