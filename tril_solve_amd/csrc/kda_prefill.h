@@ -53,8 +53,7 @@
 namespace kda {
 
 constexpr int kPreC = 32;  // tokens per chunk
-constexpr int kPreWaves = 4;
-constexpr int kPreThreads = kWave * kPreWaves;
+constexpr int kPreWaves = 4;  // that prepare a chunk
 constexpr int kPreCols = 32;  // value columns per wavefront
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kSteep = 64.0f * kLog2E;  // in powers of two
@@ -163,6 +162,19 @@ __device__ __forceinline__ w2 read_transposed(const char *p) {
                                       (Lds)(__attribute__((address_space(3))) char *)p));
 }
 
+// Barrier among the wavefronts that add to `count`, which starts at zero; `sum`
+// is what it holds once all of them have come here. (s_barrier takes the whole
+// workgroup.) All of a workgroup's wavefronts are resident, so the wait ends.
+__device__ __forceinline__ void meet(int *count, int sum) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    while (__builtin_amdgcn_readfirstlane(__hip_atomic_load(
+               count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) < sum)
+        __builtin_amdgcn_s_sleep(1);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // N adjacent elements of one row as loaded (no conversion).
 template <class E, int N>
 struct RawC;
@@ -235,17 +247,18 @@ __device__ __forceinline__ void gather_groups(f4 x, f4 (&out)[G]) {
 }
 
 // LDS layout (bytes). Operands lie in rows of 2 K bytes (reduced over
-// channels) or 64 bytes (over tokens); the 16-byte pieces of a row are
-// exchanged by an exclusive or with the row number so that the 16 rows of one
-// operand read, and the 4 rows of 4 adjacent pieces of a transposed one, fall
-// in different banks without padding.
-// OUT: kda_dtype of the output.
-template <int K, int OUT>
+// channels) or of 32 and 64 bytes (over 16 and 32 tokens); the 16-byte pieces
+// of a row are exchanged by an exclusive or with the row number so that the 16
+// rows of one operand read, and the 4 rows of 4 adjacent pieces of a transposed
+// one, fall in different banks without padding.
+// OUT: kda_dtype of the output; N: chunks whose operands are held at once.
+template <int K, int OUT, int N>
 struct PreLds {
     static constexpr int RS = 2 * K, TS = 2 * kPreC;
     static constexpr int kPatch = 20;  // floats between rows of a block of L
-    static constexpr int R32 = kPreC * RS, T32 = kPreC * TS;
+    static constexpr int R32 = kPreC * RS;
     static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of queries, P and S'
+    // N chunks' operands, each:
     // keys and queries times e^{G - m} (steep: e^G), keys times e^{m - G}
     // (steep: e^{G_32 - G})
     static constexpr int KR = 0, QR = KR + 2 * R32, KL = QR + NQ * R32;
@@ -254,16 +267,23 @@ struct PreLds {
     static constexpr int SK = 0, SQ = SK + kPreC * K * 4, SA = SQ + kPreC * K * 4;
     static constexpr int SM = SA + kPreC * K * 4, SP = SM + kPreC * kPreC * 4;
     static constexpr int kSteepBytes = SP + kPreC * kPreC * 4;
+    // a lower triangle of 32 x 32: the block of rows 0..15 (16 tokens), then
+    // rows 16..31 (32 tokens)
+    static constexpr int LOW = 16 * TS / 2, T32 = LOW + 16 * TS;
     // diagonal blocks of the inverse and -L_10; P
     static constexpr int TM = kOperands > kSteepBytes ? kOperands : kSteepBytes;
     static constexpr int PM = TM + 3 * T32;
-    static constexpr int PATCH = PM + NQ * T32;
-    static constexpr int TOT = PATCH + 2 * 16 * kPatch * 4;
+    static constexpr int kBuffer = PM + NQ * T32;
+    static_assert(kBuffer % 256 == 0);
     // per channel: what S' is of the state in registers (steep: 1), what that
-    // state owes (see `apart`), and for a steep chunk e^{G_32}
-    static constexpr int EM = TOT + kPreWaves * K * 4, EG = EM + K * 4, EF = EG + K * 4;
-    static constexpr int BETA = EF + K * 4;
-    static constexpr int kBytes = BETA + 2 * kPreC * 4;
+    // state owes (see `apart`), and for a steep chunk e^{G_32}; N chunks'
+    static constexpr int FACTORS = N * kBuffer, kFactors = 3 * K * 4;
+    static constexpr int EM = 0, EG = K * 4, EF = 2 * K * 4;
+    static constexpr int TOT = FACTORS + N * kFactors, kTot = kPreWaves * K * 4;
+    static constexpr int PATCH = TOT + N * kTot;
+    static constexpr int BETA = PATCH + 2 * 16 * kPatch * 4;
+    static constexpr int FLAGS = BETA + N * kPreC * 4;
+    static constexpr int kBytes = FLAGS + 16;
     // exchange of 16-byte pieces
     static __device__ __forceinline__ int swz_row(int row) {
         // bits 1, 0 of the row move it by 4 pieces, bits 2, 3 within them; (K =
@@ -434,9 +454,21 @@ __device__ __forceinline__ Segment find_segment(const DeltaProblem &p, int j) {
 // to the state, S_after = M S_before + B, as the columns [B | M] of a V + K
 // columns wide state: B starts from zero (a first segment's from the request's
 // state, and then is S_after), M from the identity and with V = 0.
-template <class EI, int K, int OUT, bool SUM>
-__global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProblem p) {
-    typedef PreLds<K, OUT> L;
+// ROLES: four wavefronts prepare the next chunk while others (kCols) take their
+// columns of this one through it; else four wavefronts do both in turn.
+enum class PrePass { whole, roles, sums };
+template <bool SUM, bool ROLES>
+struct PreShape {
+    static constexpr int kCols = SUM ? 8 : 4;  // wavefronts with columns
+    static constexpr int kThreads = kWave * (ROLES ? kCols + kPreWaves : kCols);
+    static constexpr int kPerSimd = SUM ? 3 : 2;  // wavefronts, by their registers
+    static_assert(ROLES || kCols == kPreWaves);
+};
+template <class EI, int K, int OUT, bool SUM, bool ROLES>
+__global__ __launch_bounds__((PreShape<SUM, ROLES>::kThreads), (PreShape<SUM, ROLES>::kPerSimd)) void
+kda_prefill_kernel(DeltaProblem p) {
+    typedef PreLds<K, OUT, ROLES ? 2 : 1> L;
+    constexpr int CW = PreShape<SUM, ROLES>::kCols;
     constexpr int NT = K / 16;  // state row tiles
     // A wavefront prepares 8 tokens: K / 4 lanes of 4 channels to a token, in
     // GRP groups of lanes with TPL tokens each.
@@ -448,12 +480,14 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 
     const int lane0 = threadIdx.x & (kWave - 1);
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const bool prepares = !ROLES || wv >= CW, walks = !ROLES || wv < CW;
+    const int pw = ROLES ? wv - CW : wv;  // a preparing wavefront's number
     const int j = blockIdx.x / p.H, h = blockIdx.x - j * p.H;
     Segment sg = {j, j, 1, 0};
     if (p.seg != 0) {
         sg = find_segment(p, j);
         if (sg.request < 0 || (SUM && sg.at + 1 == sg.count)) return;
-        if (SUM && sg.at == 0 && (int)(blockIdx.y * kPreWaves * kPreCols) >= p.V) return;
+        if (SUM && sg.at == 0 && (int)(blockIdx.y * CW * kPreCols) >= p.V) return;
     }
     const int n = sg.request;
     const int hk = h / (p.H / p.Hk);
@@ -466,9 +500,9 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
     const int slot = __builtin_amdgcn_readfirstlane(keep ? request_slot(p.pool, n) : 0);
 
     // this wavefront's columns: tile ct holds column col + ct of each lane
-    const int col0 = (blockIdx.y * kPreWaves + wv) * kPreCols;
+    const int col0 = (blockIdx.y * CW + wv) * kPreCols;
     const bool map = SUM && col0 >= p.V;  // V is a multiple of 32
-    const bool cols = SUM ? col0 < p.V + (sg.at ? K : 0) : col0 < p.V;
+    const bool cols = walks && (SUM ? col0 < p.V + (sg.at ? K : 0) : col0 < p.V);
     const int col = (cols ? map ? col0 - p.V : col0 : 0) + 2 * (lane0 & 15);
 
     // Token tensors from the request's first row and this head on, and the
@@ -510,6 +544,362 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
     // the state: lane group g4's rows of tile rt are channels
     // 32 (rt / 2) + 8 g4 + 4 (rt % 2) + s
     auto state_row = [](int rt, int s) { return 32 * (rt >> 1) + 4 * (rt & 1) + s; };
+    // ======== preparing a chunk: 8 tokens to a wavefront
+    // this wavefront's tokens as loaded and (wavefront 3) the chunk's write
+    // strengths
+    struct Rows {
+        RawC<EI, 4> k[TPL], q[TPL];
+        f4 g[TPL];
+        float beta;
+    };
+    Rows now;
+    now.beta = 0.0f;
+    auto load_rows = [&](int t0, Rows &to) {
+        const int len = min(kPreC, len_all - t0);
+        const Rsrc rk = rows_of(kb + (long)t0 * ks, ks, K * EI::kBytes, len);
+        const Rsrc rq = rows_of(qb + (long)t0 * ks, ks, K * EI::kBytes, len);
+        const Rsrc rg = rows_of(gb + (long)t0 * gs, gs, gd * 4, len);
+        const int lane = opaque_lane(lane0);
+        const uint32_t first = 8 * pw + lane / (K / 4) * TPL, c4 = lane % (K / 4) * 4;
+        if (gd == 1) {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                const float x = load1<F32>(rg, (first + i) * gs);
+                to.g[i] = f4{x, x, x, x};
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) to.g[i] = load4<F32>(rg, (first + i) * gs + c4 * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) {
+            to.k[i].load(rk, (first + i) * ks + c4 * EI::kBytes);
+            if constexpr (!SUM) to.q[i].load(rq, (first + i) * ks + c4 * EI::kBytes);
+        }
+        if (pw == 3)
+            to.beta = lane < len ? p.beta[(row_first + t0 + lane) * p.H + h] : 0.0f;
+    };
+    // Decays of a lane's tokens, summed from its wavefront's first token on,
+    // and the totals of the wavefront's groups of lanes.
+    f4 er[TPL], sums[GRP];
+    auto sum_decays = [&](int buf) {
+        const int lane = opaque_lane(lane0), grp = lane / (K / 4), ch = lane % (K / 4) * 4;
+        float *tots = reinterpret_cast<float *>(lds + L::TOT + buf * L::kTot);
+        {
+            f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(now.g[i][e], kLog2E, x[e]);
+                er[i] = x;
+            }
+            gather_groups<GRP>(x, sums);
+            f4 all = sums[0];
+#pragma unroll
+            for (int g = 1; g < GRP; ++g) all += sums[g];
+            if (grp == 0) *reinterpret_cast<f4 *>(tots + pw * K + ch) = all;
+        }
+        if (pw == 3 && lane < kPreC)
+            reinterpret_cast<float *>(lds + L::BETA)[buf * kPreC + lane] = now.beta;
+    };
+    // the decay (of this lane's channels, a power of two) that the state in
+    // registers still has to take: G_32 - m of the chunk before
+    f4 owed = {0.0f, 0.0f, 0.0f, 0.0f};
+    // a barrier of the preparing wavefronts
+    int *count = reinterpret_cast<int *>(lds + L::FLAGS) + 2, met = 0;
+    auto meet_all = [&] {
+        if constexpr (ROLES)
+            meet(count, met += kPreWaves);
+        else
+            __syncthreads();
+    };
+    // What the chunk at t0 puts into buffer `buf`, from its loaded rows and the
+    // wavefronts' totals; far, apart: see there.
+    auto prepare = [&](int buf, bool &far, bool &apart) {
+        // the lane made opaque: the many addresses derived from it are formed
+        // where they are used instead of being kept (and spilled) across chunks
+        const int lane = opaque_lane(lane0);
+        const int g4 = lane >> 4, n16 = lane & 15;
+        // this lane's group, channels and first token of the wavefront's 8
+        const int grp = lane / (K / 4), ch = lane % (K / 4) * 4, tok = 8 * pw + TPL * grp;
+        char *op = lds + buf * L::kBuffer, *fac = lds + L::FACTORS + buf * L::kFactors;
+        const float *tots = reinterpret_cast<const float *>(lds + L::TOT + buf * L::kTot);
+        const float *beta = reinterpret_cast<const float *>(lds + L::BETA) + buf * kPreC;
+
+        auto put_row = [&]<int N>(int at, int row, f4 x) {
+            char *d = op + at + row * L::RS + ((2 * ch) ^ L::swz_row(row));
+            const Half<N> hx = split4<N>(x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) *reinterpret_cast<w2 *>(d + i * L::R32) = hx.p[i];
+        };
+        // entries (row, c) and (row + 1, c), row even, of an operand reduced
+        // over tokens; low: rows 16..31
+        auto put_pair = [&]<int N>(int at, bool low, int row, int c, float x, float y) {
+            char *d = op + at + (low ? L::LOW + row * L::TS +
+                                           ((2 * operand_pos(c)) ^ L::swz_tok(row))
+                                     : row * (L::TS / 2) + 2 * c);
+            uint32_t part[N];
+            split2<N>(x, y, part);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                *reinterpret_cast<uint16_t *>(d + i * L::T32) = (uint16_t)part[i];
+                *reinterpret_cast<uint16_t *>(d + i * L::T32 + (low ? L::TS : L::TS / 2)) =
+                    (uint16_t)(part[i] >> 16);
+            }
+        };
+        // ---- 1. the operands reduced over channels
+        f4 wt[kPreWaves];  // every wavefront's 8 tokens
+#pragma unroll
+        for (int w = 0; w < kPreWaves; ++w)
+            wt[w] = *reinterpret_cast<const f4 *>(tots + w * K + ch);
+        const f4 first = wt[0] + wt[1], second = wt[2] + wt[3];  // m, G_32 - m
+        const f4 both = owed + first;
+        bool steep = false, deep = false;  // (steep: NaN or infinite where any gate is)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            steep |= !(__builtin_fabsf(first[e]) <= kSteep) |
+                     !(__builtin_fabsf(second[e]) <= kSteep);
+            deep |= __builtin_fabsf(both[e]) > 125.0f;
+        }
+        far = __ballot(steep) != 0;  // the same in every wavefront
+        apart = far | (__ballot(deep) != 0);
+        if (pw == 0 && grp == 0) {
+            const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
+            *reinterpret_cast<f4 *>(fac + L::EM + 4 * ch) =
+                far ? one : exp2(apart ? first : both);
+            *reinterpret_cast<f4 *>(fac + L::EG + 4 * ch) = exp2(owed);
+            *reinterpret_cast<f4 *>(fac + L::EF + 4 * ch) = exp2(first + second);
+        }
+        if (ROLES && pw == 0 && lane0 == 0)
+            reinterpret_cast<int *>(lds + L::FLAGS)[buf] = (far ? 1 : 0) | (apart ? 2 : 0);
+        owed = far ? f4{0.0f, 0.0f, 0.0f, 0.0f} : second;
+        if (!far) {
+            // from the chunk's middle to this lane's first token
+            f4 mid = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (pw >= 2) {
+                if (pw == 3) mid = wt[2];
+#pragma unroll
+                for (int g = 0; g + 1 < GRP; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mid[e] += g < grp ? sums[g][e] : 0.0f;
+            } else {
+                mid = -sums[GRP - 1];
+                if (pw == 0) mid -= wt[1];
+#pragma unroll
+                for (int g = 0; g + 1 < GRP; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mid[e] -= g >= grp ? sums[g][e] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                const f4 e = exp2(er[i] + mid), k = now.k[i].all();
+                put_row.template operator()<2>(L::KR, tok + i, k * e);
+                if constexpr (!SUM)
+                    put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
+                put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                const int at = 4 * ((tok + i) * K + ch);
+                *reinterpret_cast<f4 *>(op + L::SK + at) = now.k[i].all();
+                if constexpr (!SUM)
+                    *reinterpret_cast<f4 *>(op + L::SQ + at) = now.q[i].all() * p.scale;
+                *reinterpret_cast<f4 *>(op + L::SA + at) = exp2(now.g[i] * kLog2E);
+            }
+        }
+        meet_all();
+
+        const int rpos = n16 * L::RS + ((g4 << 4) ^ L::swz_row(n16));
+        // 16 rows of an operand reduced over channels, k-step kk
+        auto row_operand = [&]<int N>(int at, int kk) -> Operand<N> {
+            Operand<N> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o.p[i] = *reinterpret_cast<const w4 *>(op + at + i * L::R32 + (rpos ^ (64 * kk)));
+            return o;
+        };
+        // ---- 2. 16 x 16 blocks of L / beta and P: wavefronts 0 and 1 a
+        // diagonal block of L each (and its inverse), 2 those of P, 3 the two
+        // blocks below
+        f4 m[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        if (!far) {
+            // rows 16 bi .. of `left` against rows 16 bj .. of the keys
+            auto block = [&]<int M, int N>(int left, int bi, int bj) -> f4 {
+                Operand<N> l[K / 32], r[K / 32];
+#pragma unroll
+                for (int kk = 0; kk < K / 32; ++kk) {
+                    l[kk] = row_operand.template operator()<N>(left + 16 * bi * L::RS, kk);
+                    r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
+                }
+                f4 c[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+                for (int kk = 0; kk < K / 32; kk += 2)
+#pragma unroll
+                    for (int i = 0; i < M; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            c[e] = mfma(l[kk + e].p[part_a(M, i)], r[kk + e].p[part_b(M, i)], c[e]);
+                return c[0] + c[1];
+            };
+            if (pw < 2) {
+                m[0] = block.template operator()<3, 2>(L::KR, pw, pw);
+            } else if (pw == 3) {
+                m[0] = block.template operator()<3, 2>(L::KR, 1, 0);
+                if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
+            } else if constexpr (!SUM) {
+                m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
+                m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 1);
+            }
+        } else {
+            // running products of the decays from token j on
+            const float *sk = reinterpret_cast<const float *>(op + L::SK);
+            const float *sq = reinterpret_cast<const float *>(op + L::SQ);
+            const float *sa = reinterpret_cast<const float *>(op + L::SA);
+            float *sm = reinterpret_cast<float *>(op + L::SM);
+            float *sp = reinterpret_cast<float *>(op + L::SP);
+#pragma unroll 1
+            for (int j = pw; j < kPreC; j += kPreWaves) {
+                constexpr int CPL = K / kWave;  // channels per lane, 64 apart
+                float f[CPL];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) f[c] = sk[j * K + lane + 64 * c];
+#pragma unroll 1
+                for (int i = j; i < kPreC; ++i) {
+                    float a = 0.0f, b = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c) {
+                        const int at = i * K + lane + 64 * c;
+                        if (i > j) f[c] *= sa[at];
+                        a = __builtin_fmaf(f[c], sk[at], a);
+                        if constexpr (!SUM) b = __builtin_fmaf(f[c], sq[at], b);
+                    }
+                    a = sum64(a);
+                    if constexpr (!SUM) b = sum64(b);
+                    if (lane == 0) {
+                        sm[i * kPreC + j] = a;
+                        sp[i * kPreC + j] = b;
+                    }
+                }
+            }
+            meet_all();
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int top = (4 * g4 + s) * kPreC + n16, low = top + 16 * kPreC;
+                if (pw < 2) m[0][s] = sm[pw == 0 ? top : low + 16];
+                if (pw == 2) {
+                    m[0][s] = sp[top];
+                    m[1][s] = sp[low + 16];
+                }
+                if (pw == 3) {
+                    m[0][s] = sm[low];
+                    m[1][s] = sp[low];
+                }
+            }
+        }
+        // the inverse's diagonal blocks times beta (of their column), -L_10 /
+        // beta (of the row) and P, as A operands
+        if (pw < 2) {
+            float *patch = reinterpret_cast<float *>(lds + L::PATCH) + pw * 16 * L::kPatch;
+            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 * pw + 4 * g4);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int r = 4 * g4 + s;
+                patch[r * L::kPatch + n16] = n16 < r ? -b4[s] * m[0][s] : 0.0f;
+            }
+            float arow[16], x[16];  // every 16-lane row the same
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = j == n16 ? 1.0f : 0.0f;
+            wave_sync();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f4 v = *reinterpret_cast<const f4 *>(&patch[n16 * L::kPatch + 4 * j]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) arow[4 * j + s] = v[s];
+            }
+            substitute(arow, x);
+            const float bc = beta[16 * pw + n16];
+            f4 y;  // rows 4 g4 .. + 3 (two opaque bits: selects, not a switch on g4)
+            const bool odd = opaque_lane(g4 & 1), high = opaque_lane(g4 >> 1);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float a = odd ? x[4 + s] : x[s], b = odd ? x[12 + s] : x[8 + s];
+                y[s] = (high ? b : a) * bc;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; s += 2)
+                put_pair.template operator()<3>(L::TM, pw == 1, 4 * g4 + s, 16 * pw + n16, y[s],
+                                                y[s + 1]);
+        } else if (pw == 2) {
+            if constexpr (!SUM)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int s = 0; s < 4; s += 2) {
+                        const int r = 4 * g4 + s;
+                        put_pair.template operator()<NQ>(L::PM, b == 1, r, 16 * b + n16,
+                                                         n16 <= r ? m[b][s] : 0.0f,
+                                                         n16 <= r + 1 ? m[b][s + 1] : 0.0f);
+                    }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; s += 2) {
+                put_pair.template operator()<2>(L::TM, true, 4 * g4 + s, n16, -m[0][s],
+                                                -m[0][s + 1]);
+                if constexpr (!SUM)
+                    put_pair.template operator()<NQ>(L::PM, true, 4 * g4 + s, n16, m[1][s],
+                                                     m[1][s + 1]);
+            }
+        }
+        if (far) {
+            // k e^G, q e^G and k e^{G_32 - G} over the FP32 copies; sums from
+            // the chunk's ends, so that no difference of large sums is taken
+            // (formed anew from the loaded gates, through copies that the
+            // compiler cannot tell from new values, so that nothing is held in
+            // registers for this branch)
+            f4 before = {0.0f, 0.0f, 0.0f, 0.0f}, after = before, g2[TPL], ends[GRP], x = before;
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float g = now.g[i][e];
+                    asm("" : "+v"(g));
+                    g2[i][e] = g * kLog2E;
+                }
+                x += g2[i];
+            }
+            gather_groups<GRP>(x, ends);
+#pragma unroll 1
+            for (int w = 0; w < kPreWaves; ++w) {
+                const f4 y = *reinterpret_cast<const f4 *>(tots + w * K + ch);
+                if (w < pw) before += y;
+                if (w > pw) after += y;
+            }
+#pragma unroll
+            for (int g = 0; g < GRP; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    before[e] += g < grp ? ends[g][e] : 0.0f;
+                    after[e] += g > grp ? ends[g][e] : 0.0f;
+                }
+            meet_all();  // the copies (and L and P) have been read
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                before += g2[i];
+                const f4 e = exp2(before);
+                put_row.template operator()<2>(L::KR, tok + i, now.k[i].all() * e);
+                if constexpr (!SUM)
+                    put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
+            }
+#pragma unroll
+            for (int i = TPL - 1; i >= 0; --i) {
+                put_row.template operator()<3>(L::KL, tok + i, now.k[i].all() * exp2(after));
+                after += g2[i];
+            }
+        }
+    };
+
+    // ======== this wavefront's columns
     f4 S[NT][2];
     // [K, V] of this head in slot `at` of a tensor [.., H, K, V], this lane's part
     auto state_at = [&](float *base, int at) {
@@ -535,385 +925,69 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
                     f2{S[rt][0][s], S[rt][1][s]},
                     reinterpret_cast<f2 *>(dst + (long)state_row(rt, s) * stride));
     };
-    if (!SUM && sg.count > 1 && cols) {
-        load_state(sg.at == 0 ? state_at(p.seg_first, n) : state_at(p.seg_state, j - 1));
-    } else if (cols && sg.at == 0 && request_continues(p.pool, n)) {
-        load_state(state_at(p.pool.base, slot));
-    } else {
-#pragma unroll
-        for (int rt = 0; rt < NT; ++rt)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
-                    S[rt][ct][s] =
-                        map && 8 * (lane0 >> 4) + state_row(rt, s) == col + ct ? 1.0f : 0.0f;
-    }
-    // the last segment of the later pass overwrites the pool's state
-    if (SUM && sg.at == 0 && cols) store_state(state_at(p.seg_first, n), p.V);
-
-    // entries of the inverse and of P that no chunk writes are zero
-    for (int i = threadIdx.x; i < (3 + NQ) * L::T32 / 4; i += kPreThreads)
-        reinterpret_cast<uint32_t *>(lds + L::TM)[i] = 0;
-
-    // this wavefront's tokens of the next chunk, as loaded, and (wavefront 3)
-    // the chunk's write strengths
-    RawC<EI, 4> kraw[TPL], qraw[TPL];
-    f4 graw[TPL];
-    float braw = 0.0f;
-    auto load_rows = [&](int t0) {
-        const int len = min(kPreC, len_all - t0);
-        const Rsrc rk = rows_of(kb + (long)t0 * ks, ks, K * EI::kBytes, len);
-        const Rsrc rq = rows_of(qb + (long)t0 * ks, ks, K * EI::kBytes, len);
-        const Rsrc rg = rows_of(gb + (long)t0 * gs, gs, gd * 4, len);
-        const int lane = opaque_lane(lane0);
-        const uint32_t first = 8 * wv + lane / (K / 4) * TPL, c4 = lane % (K / 4) * 4;
-        if (gd == 1) {
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-                const float x = load1<F32>(rg, (first + i) * gs);
-                graw[i] = f4{x, x, x, x};
-            }
+    auto start_state = [&] {
+        if (!SUM && sg.count > 1 && cols) {
+            load_state(sg.at == 0 ? state_at(p.seg_first, n) : state_at(p.seg_state, j - 1));
+        } else if (cols && sg.at == 0 && request_continues(p.pool, n)) {
+            load_state(state_at(p.pool.base, slot));
         } else {
 #pragma unroll
-            for (int i = 0; i < TPL; ++i) graw[i] = load4<F32>(rg, (first + i) * gs + c4 * 4);
-        }
+            for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) {
-            kraw[i].load(rk, (first + i) * ks + c4 * EI::kBytes);
-            if constexpr (!SUM) qraw[i].load(rq, (first + i) * ks + c4 * EI::kBytes);
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct)
+                        S[rt][ct][s] =
+                            map && 8 * (lane0 >> 4) + state_row(rt, s) == col + ct ? 1.0f : 0.0f;
         }
-        if (wv == 3)
-            braw = lane < len ? p.beta[(row_first + t0 + lane) * p.H + h] : 0.0f;
+        // the last segment of the later pass overwrites the pool's state
+        if (SUM && sg.at == 0 && cols) store_state(state_at(p.seg_first, n), p.V);
     };
-    if (len_all > 0) load_rows(0);
-
-    // the decay (of this lane's channels, a power of two) that the state in
-    // registers still has to take: G_32 - m of the chunk before
-    f4 owed = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int t0 = 0, buf = 0; t0 < len_all; t0 += kPreC, buf ^= 1) {
+    // the values of this wavefront's columns
+    RawC<EI, 2> vraw[2][4];
+    auto load_values = [&](int t0) {
         const int len = min(kPreC, len_all - t0);
-        // the lane made opaque: the many addresses derived from it are formed
-        // where they are used instead of being kept (and spilled) across chunks
+        // (no row at all for M's columns: V = 0)
+        const Rsrc rv = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(vb + (long)t0 * vs), 0,
+            map ? 0 : (len - 1) * vs + p.V * EI::kBytes, kRsrcWord3);
+        const uint32_t at = 4 * (opaque_lane(lane0) >> 4) * vs + col * EI::kBytes;
+#pragma unroll
+        for (int I = 0; I < 2; ++I)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) vraw[I][s].load(rv, at + (16 * I + s) * vs);
+    };
+    auto use = [&](int t0, int buf, bool far, bool apart) {
+        const int len = min(kPreC, len_all - t0);
         const int lane = opaque_lane(lane0);
         const int g4 = lane >> 4, n16 = lane & 15;
-        // this lane's group, channels and first token of the wavefront's 8
-        const int grp = lane / (K / 4), ch = lane % (K / 4) * 4, tok = 8 * wv + TPL * grp;
         const int rpos = n16 * L::RS + ((g4 << 4) ^ L::swz_row(n16));
-        const int tpos = n16 * L::TS + ((g4 << 4) ^ L::swz_tok(n16));
-
-        auto put_row = [&]<int N>(int at, int row, f4 x) {
-            char *d = lds + at + row * L::RS + ((2 * ch) ^ L::swz_row(row));
-            const Half<N> hx = split4<N>(x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) *reinterpret_cast<w2 *>(d + i * L::R32) = hx.p[i];
-        };
+        const char *op = lds + buf * L::kBuffer, *fac = lds + L::FACTORS + buf * L::kFactors;
         // 16 rows of an operand reduced over channels, k-step kk
         auto row_operand = [&]<int N>(int at, int kk) -> Operand<N> {
             Operand<N> o;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                o.p[i] = *reinterpret_cast<const w4 *>(lds + at + i * L::R32 + (rpos ^ (64 * kk)));
+                o.p[i] = *reinterpret_cast<const w4 *>(op + at + i * L::R32 + (rpos ^ (64 * kk)));
             return o;
         };
-        auto tok_operand = [&]<int N>(int at) -> Operand<N> {
+        // a lower triangle's rows 0..15, and 16..31
+        auto top_operand = [&]<int N>(int at) -> Half<N> {
+            Half<N> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o.p[i] = *reinterpret_cast<const w2 *>(op + at + i * L::T32 + n16 * (L::TS / 2) +
+                                                       8 * g4);
+            return o;
+        };
+        auto low_operand = [&]<int N>(int at) -> Operand<N> {
             Operand<N> o;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                o.p[i] = *reinterpret_cast<const w4 *>(lds + at + i * L::T32 + tpos);
+                o.p[i] = *reinterpret_cast<const w4 *>(op + at + i * L::T32 + L::LOW +
+                                                       n16 * L::TS + ((g4 << 4) ^ L::swz_tok(n16)));
             return o;
         };
-        // entries (row, c) and (row + 1, c), row even, of an operand reduced
-        // over tokens
-        auto put_pair = [&]<int N>(int at, int row, int c, float x, float y) {
-            char *d = lds + at + row * L::TS + ((2 * operand_pos(c)) ^ L::swz_tok(row));
-            uint32_t part[N];
-            split2<N>(x, y, part);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                *reinterpret_cast<uint16_t *>(d + i * L::T32) = (uint16_t)part[i];
-                *reinterpret_cast<uint16_t *>(d + i * L::T32 + L::TS) = (uint16_t)(part[i] >> 16);
-            }
-        };
-
-        // ---- 1. decays of this lane's tokens, summed from its wavefront's
-        // first token on
-        f4 er[TPL], sums[GRP];
-        float *tots = reinterpret_cast<float *>(lds + L::TOT);
-        {
-            f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(graw[i][e], kLog2E, x[e]);
-                er[i] = x;
-            }
-            gather_groups<GRP>(x, sums);
-            f4 all = sums[0];
-#pragma unroll
-            for (int g = 1; g < GRP; ++g) all += sums[g];
-            if (grp == 0) *reinterpret_cast<f4 *>(tots + wv * K + ch) = all;
-        }
-        float *beta = reinterpret_cast<float *>(lds + L::BETA) + buf * kPreC;
-        if (wv == 3 && lane < kPreC) beta[lane] = braw;
-        __syncthreads();  // totals; every read of the previous chunk's operands is done
-
-        f4 wt[kPreWaves];  // every wavefront's 8 tokens
-#pragma unroll
-        for (int w = 0; w < kPreWaves; ++w)
-            wt[w] = *reinterpret_cast<const f4 *>(tots + w * K + ch);
-        const f4 first = wt[0] + wt[1], second = wt[2] + wt[3];  // m, G_32 - m
-        const f4 both = owed + first;
-        bool steep = false, deep = false;  // (steep: NaN or infinite where any gate is)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            steep |= !(__builtin_fabsf(first[e]) <= kSteep) |
-                     !(__builtin_fabsf(second[e]) <= kSteep);
-            deep |= __builtin_fabsf(both[e]) > 125.0f;
-        }
-        const bool far = __ballot(steep) != 0;  // the same in every wavefront
-        const bool apart = far | (__ballot(deep) != 0);
-        if (wv == 0 && grp == 0) {
-            const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
-            *reinterpret_cast<f4 *>(lds + L::EM + 4 * ch) =
-                far ? one : exp2(apart ? first : both);
-            *reinterpret_cast<f4 *>(lds + L::EG + 4 * ch) = exp2(owed);
-            *reinterpret_cast<f4 *>(lds + L::EF + 4 * ch) = exp2(first + second);
-        }
-        owed = far ? f4{0.0f, 0.0f, 0.0f, 0.0f} : second;
-        if (!far) {
-            // from the chunk's middle to this lane's first token
-            f4 mid = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (wv >= 2) {
-                if (wv == 3) mid = wt[2];
-#pragma unroll
-                for (int g = 0; g + 1 < GRP; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mid[e] += g < grp ? sums[g][e] : 0.0f;
-            } else {
-                mid = -sums[GRP - 1];
-                if (wv == 0) mid -= wt[1];
-#pragma unroll
-                for (int g = 0; g + 1 < GRP; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mid[e] -= g >= grp ? sums[g][e] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-                const f4 e = exp2(er[i] + mid), k = kraw[i].all();
-                put_row.template operator()<2>(L::KR, tok + i, k * e);
-                if constexpr (!SUM)
-                    put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
-                put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-                const int at = 4 * ((tok + i) * K + ch);
-                *reinterpret_cast<f4 *>(lds + L::SK + at) = kraw[i].all();
-                if constexpr (!SUM)
-                    *reinterpret_cast<f4 *>(lds + L::SQ + at) = qraw[i].all() * p.scale;
-                *reinterpret_cast<f4 *>(lds + L::SA + at) = exp2(graw[i] * kLog2E);
-            }
-        }
-        __syncthreads();
-
-        // ---- 2. 16 x 16 blocks of L / beta and P: wavefronts 0 and 1 a
-        // diagonal block of L each (and its inverse), 2 those of P, 3 the two
-        // blocks below
-        f4 m[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        if (!far) {
-            // rows 16 bi .. of `left` against rows 16 bj .. of the keys
-            auto block = [&]<int M, int N>(int left, int bi, int bj) -> f4 {
-                Operand<N> l[K / 32], r[K / 32];
-#pragma unroll
-                for (int kk = 0; kk < K / 32; ++kk) {
-                    l[kk] = row_operand.template operator()<N>(left + 16 * bi * L::RS, kk);
-                    r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
-                }
-                f4 c[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-                for (int kk = 0; kk < K / 32; kk += 2)
-#pragma unroll
-                    for (int i = 0; i < M; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            c[e] = mfma(l[kk + e].p[part_a(M, i)], r[kk + e].p[part_b(M, i)], c[e]);
-                return c[0] + c[1];
-            };
-            if (wv < 2) {
-                m[0] = block.template operator()<3, 2>(L::KR, wv, wv);
-            } else if (wv == 3) {
-                m[0] = block.template operator()<3, 2>(L::KR, 1, 0);
-                if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
-            } else if constexpr (!SUM) {
-                m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
-                m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 1);
-            }
-        } else {
-            // running products of the decays from token j on
-            const float *sk = reinterpret_cast<const float *>(lds + L::SK);
-            const float *sq = reinterpret_cast<const float *>(lds + L::SQ);
-            const float *sa = reinterpret_cast<const float *>(lds + L::SA);
-            float *sm = reinterpret_cast<float *>(lds + L::SM);
-            float *sp = reinterpret_cast<float *>(lds + L::SP);
-#pragma unroll 1
-            for (int j = wv; j < kPreC; j += kPreWaves) {
-                constexpr int CPL = K / kWave;  // channels per lane, 64 apart
-                float f[CPL];
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) f[c] = sk[j * K + lane + 64 * c];
-#pragma unroll 1
-                for (int i = j; i < kPreC; ++i) {
-                    float a = 0.0f, b = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < CPL; ++c) {
-                        const int at = i * K + lane + 64 * c;
-                        if (i > j) f[c] *= sa[at];
-                        a = __builtin_fmaf(f[c], sk[at], a);
-                        if constexpr (!SUM) b = __builtin_fmaf(f[c], sq[at], b);
-                    }
-                    a = sum64(a);
-                    if constexpr (!SUM) b = sum64(b);
-                    if (lane == 0) {
-                        sm[i * kPreC + j] = a;
-                        sp[i * kPreC + j] = b;
-                    }
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int top = (4 * g4 + s) * kPreC + n16, low = top + 16 * kPreC;
-                if (wv < 2) m[0][s] = sm[wv == 0 ? top : low + 16];
-                if (wv == 2) {
-                    m[0][s] = sp[top];
-                    m[1][s] = sp[low + 16];
-                }
-                if (wv == 3) {
-                    m[0][s] = sm[low];
-                    m[1][s] = sp[low];
-                }
-            }
-        }
-        // the inverse's diagonal blocks times beta (of their column), -L_10 /
-        // beta (of the row) and P, as A operands
-        if (wv < 2) {
-            float *patch = reinterpret_cast<float *>(lds + L::PATCH) + wv * 16 * L::kPatch;
-            const f4 b4 = *reinterpret_cast<const f4 *>(beta + 16 * wv + 4 * g4);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 4 * g4 + s;
-                patch[r * L::kPatch + n16] = n16 < r ? -b4[s] * m[0][s] : 0.0f;
-            }
-            float arow[16], x[16];  // every 16-lane row the same
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = j == n16 ? 1.0f : 0.0f;
-            wave_sync();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f4 v = *reinterpret_cast<const f4 *>(&patch[n16 * L::kPatch + 4 * j]);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) arow[4 * j + s] = v[s];
-            }
-            substitute(arow, x);
-            const float bc = beta[16 * wv + n16];
-            f4 y;  // rows 4 g4 .. + 3 (two opaque bits: selects, not a switch on g4)
-            const bool odd = opaque_lane(g4 & 1), high = opaque_lane(g4 >> 1);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float a = odd ? x[4 + s] : x[s], b = odd ? x[12 + s] : x[8 + s];
-                y[s] = (high ? b : a) * bc;
-            }
-#pragma unroll
-            for (int s = 0; s < 4; s += 2)
-                put_pair.template operator()<3>(L::TM, 16 * wv + 4 * g4 + s, 16 * wv + n16, y[s],
-                                                y[s + 1]);
-        } else if (wv == 2) {
-            if constexpr (!SUM)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int s = 0; s < 4; s += 2) {
-                        const int r = 4 * g4 + s;
-                        put_pair.template operator()<NQ>(L::PM, 16 * b + r, 16 * b + n16,
-                                                         n16 <= r ? m[b][s] : 0.0f,
-                                                         n16 <= r + 1 ? m[b][s + 1] : 0.0f);
-                    }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; s += 2) {
-                put_pair.template operator()<2>(L::TM, 16 + 4 * g4 + s, n16, -m[0][s],
-                                                -m[0][s + 1]);
-                if constexpr (!SUM)
-                    put_pair.template operator()<NQ>(L::PM, 16 + 4 * g4 + s, n16, m[1][s],
-                                                     m[1][s + 1]);
-            }
-        }
-        if (far) {
-            // k e^G, q e^G and k e^{G_32 - G} over the FP32 copies; sums from
-            // the chunk's ends, so that no difference of large sums is taken
-            // (formed anew from the loaded gates, through copies that the
-            // compiler cannot tell from new values, so that nothing is held in
-            // registers for this branch)
-            f4 before = {0.0f, 0.0f, 0.0f, 0.0f}, after = before, g2[TPL], ends[GRP], x = before;
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float g = graw[i][e];
-                    asm("" : "+v"(g));
-                    g2[i][e] = g * kLog2E;
-                }
-                x += g2[i];
-            }
-            gather_groups<GRP>(x, ends);
-#pragma unroll 1
-            for (int w = 0; w < kPreWaves; ++w) {
-                const f4 y = *reinterpret_cast<const f4 *>(tots + w * K + ch);
-                if (w < wv) before += y;
-                if (w > wv) after += y;
-            }
-#pragma unroll
-            for (int g = 0; g < GRP; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    before[e] += g < grp ? ends[g][e] : 0.0f;
-                    after[e] += g > grp ? ends[g][e] : 0.0f;
-                }
-            __syncthreads();  // the copies (and L and P) have been read
-#pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-                before += g2[i];
-                const f4 e = exp2(before);
-                put_row.template operator()<2>(L::KR, tok + i, kraw[i].all() * e);
-                if constexpr (!SUM)
-                    put_row.template operator()<NQ>(L::QR, tok + i, qraw[i].all() * (e * p.scale));
-            }
-#pragma unroll
-            for (int i = TPL - 1; i >= 0; --i) {
-                put_row.template operator()<3>(L::KL, tok + i, kraw[i].all() * exp2(after));
-                after += g2[i];
-            }
-        }
-        // the values of this wavefront's columns
-        RawC<EI, 2> vraw[2][4];
-        {
-            // (no row at all for M's columns: V = 0)
-            const Rsrc rv = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<char *>(vb + (long)t0 * vs), 0,
-                map ? 0 : (len - 1) * vs + p.V * EI::kBytes, kRsrcWord3);
-            const uint32_t at = 4 * g4 * vs + col * EI::kBytes;
-#pragma unroll
-            for (int I = 0; I < 2; ++I)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) vraw[I][s].load(rv, at + (16 * I + s) * vs);
-        }
-        __syncthreads();
-
-        // ---- 3. this wavefront's columns
-        if (t0 + kPreC < len_all) load_rows(t0 + kPreC);
-        if (!cols) continue;
         // The operands of each group of products are read from LDS one group
         // ahead, and the state's next rows are scaled and split in the
         // products' shadow.
@@ -931,7 +1005,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         auto read_em = [&](int kk) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                em[t] = *reinterpret_cast<const f4 *>(lds + L::EM +
+                em[t] = *reinterpret_cast<const f4 *>(fac + L::EM +
                                                       4 * (8 * g4 + state_row(2 * kk + t, 0)));
         };
         auto split_state = [&](int kk, int ct) {  // S' (also of a steep chunk, where it is S)
@@ -943,7 +1017,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 #pragma unroll
             for (int rt = 0; rt < NT; ++rt) {
                 const f4 e =
-                    *reinterpret_cast<const f4 *>(lds + L::EG + 4 * (8 * g4 + state_row(rt, 0)));
+                    *reinterpret_cast<const f4 *>(fac + L::EG + 4 * (8 * g4 + state_row(rt, 0)));
                 S[rt][0] *= e;
                 S[rt][1] *= e;
             }
@@ -986,21 +1060,22 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) R[I][ct][s] = vraw[I][s].at(ct) - kS[I][ct][s];
+        if (ROLES && t0 + kPreC < len_all) load_values(t0 + kPreC);
         Operand<3> u[2];
         {
-            const auto x0 = tok_operand.template operator()<3>(L::TM);
-            const auto x1 = tok_operand.template operator()<3>(L::TM + 16 * L::TS);
-            const auto p0 = tok_operand.template operator()<NQ>(L::PM);
-            const auto p1 = tok_operand.template operator()<NQ>(L::PM + 16 * L::TS);
+            const auto x0 = top_operand.template operator()<3>(L::TM);
+            const auto x1 = low_operand.template operator()<3>(L::TM);
+            const auto p0 = top_operand.template operator()<NQ>(L::PM);
+            const auto p1 = low_operand.template operator()<NQ>(L::PM);
             Half<3> r[2], h0[2];
             f4 x[2] = {z, z};
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) r[ct] = split4<3>(R[0][ct]);
-            mul_columns<6>(half_of(x0, 0), r, x);
+            mul_columns<6>(x0, r, x);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) h0[ct] = split4<3>(x[ct]);
             mul_columns<3>(half_of(x1, 0), h0, R[1]);
-            if constexpr (!SUM) mul_columns<MQ>(half_of(p0, 0), h0, o[0]);
+            if constexpr (!SUM) mul_columns<MQ>(p0, h0, o[0]);
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 r[ct] = split4<3>(R[1][ct]);
@@ -1036,7 +1111,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
         auto read_state = [&](int rt) {
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
-                const char *at = lds + (tpiece[hb] ^ (64 * (rt >> 1)));
+                const char *at = op + (tpiece[hb] ^ (64 * (rt >> 1)));
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     const w2 x = read_transposed(at + L::KL + i * L::R32 + 8 * (rt & 1));
@@ -1049,7 +1124,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
 #pragma unroll
             for (int rt = 0; rt < NT; ++rt) {
                 const f4 e =
-                    *reinterpret_cast<const f4 *>(lds + L::EF + 4 * (8 * g4 + state_row(rt, 0)));
+                    *reinterpret_cast<const f4 *>(fac + L::EF + 4 * (8 * g4 + state_row(rt, 0)));
                 S[rt][0] *= e;
                 S[rt][1] *= e;
             }
@@ -1064,12 +1139,74 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
             interleave<12, 1>();
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+
+    // ======== the walk over the chunks
+    if constexpr (ROLES) {
+        if (prepares) {
+            // (16,384 tokens on 32 workgroups: 2.19 -> 2.09 ms; with eight other
+            // wavefronts they would wait: 681 -> 720 us cut)
+            if (!SUM) __builtin_amdgcn_s_setprio(2);
+            Rows next;
+            next.beta = 0.0f;
+            if (len_all > 0) {
+                if (pw == 0 && lane0 == 0) *count = 0;
+                load_rows(0, now);
+                sum_decays(0);
+                __syncthreads();
+            }
+            for (int t0 = 0, buf = 0; t0 < len_all; t0 += kPreC, buf ^= 1) {
+                const bool more = t0 + kPreC < len_all;
+                bool far, apart;
+                if (more) load_rows(t0 + kPreC, next);
+                prepare(buf, far, apart);
+                if (more) {
+                    now = next;
+                    sum_decays(buf ^ 1);
+                }
+                __syncthreads();  // this chunk's operands, the next one's totals
+            }
+            if (len_all > 0) {
+                // what the last chunk owes (nothing reads the totals now)
+                if (pw == 0 && lane0 < K / 4)
+                    *reinterpret_cast<f4 *>(lds + L::TOT + 16 * lane0) = exp2(owed);
+                __syncthreads();
+            }
+            return;
+        }
+        start_state();
+        if (len_all > 0) {
+            if (cols) load_values(0);
+            __syncthreads();  // totals
+            __syncthreads();  // the first chunk's operands
+        }
+        for (int t0 = 0, buf = 0; t0 < len_all; t0 += kPreC, buf ^= 1) {
+            const int flags = __builtin_amdgcn_readfirstlane(
+                reinterpret_cast<const int *>(lds + L::FLAGS)[buf]);
+            if (cols) use(t0, buf, flags & 1, flags & 2);
+            __syncthreads();
+        }
+    } else {
+        start_state();
+        if (len_all > 0) load_rows(0, now);
+        for (int t0 = 0; t0 < len_all; t0 += kPreC) {
+            bool far, apart;
+            sum_decays(0);
+            __syncthreads();  // totals; nothing reads the chunk before any more
+            prepare(0, far, apart);
+            if (cols) load_values(t0);
+            __syncthreads();
+            if (t0 + kPreC < len_all) load_rows(t0 + kPreC, now);
+            if (cols) use(t0, 0, far, apart);
+        }
+        if (len_all > 0) {
+            if (pw == 0 && lane0 < K / 4)
+                *reinterpret_cast<f4 *>(lds + L::TOT + 16 * lane0) = exp2(owed);
+            __syncthreads();
+        }
     }
-    // what the last chunk owes (the totals' place: no wavefront reads them now)
-    if (len_all > 0) {
-        float *left = reinterpret_cast<float *>(lds + L::TOT);
-        if (wv == 0 && lane0 < K / 4) *reinterpret_cast<f4 *>(left + 4 * lane0) = exp2(owed);
-        __syncthreads();
+    if (len_all > 0) {  // what the last chunk owes
+        const float *left = reinterpret_cast<const float *>(lds + L::TOT);
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
             const f4 e =
@@ -1088,30 +1225,36 @@ __global__ __launch_bounds__(kPreThreads, 2) void kda_prefill_kernel(DeltaProble
     }
 }
 
+// Wavefronts that do one thing each shorten a chunk of a lone workgroup, but
+// take a compute unit's whole LDS.
 template <class EI>
-hipError_t launch_prefill_of(const DeltaProblem &p, bool sum, hipStream_t stream) {
+hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t stream) {
     const int64_t parts = p.seg != 0 ? p.segs : p.req.num_seqs;
-    const int cols = p.V + (sum ? p.K : 0);
-    const dim3 grid((unsigned)(parts * p.H),
-                    (unsigned)((cols + kPreWaves * kPreCols - 1) / (kPreWaves * kPreCols)));
-    auto go = [&]<int K, int OUT, bool SUM>() {
-        hipLaunchKernelGGL((kda_prefill_kernel<EI, K, OUT, SUM>), grid, dim3(kPreThreads), 0,
-                           stream, p);
+    auto go = [&]<int K, int OUT, bool SUM, bool ROLES>() {
+        typedef PreShape<SUM, ROLES> Shape;
+        const int cols = p.V + (SUM ? K : 0), each = Shape::kCols * kPreCols;
+        const dim3 grid((unsigned)(parts * p.H), (unsigned)((cols + each - 1) / each));
+        hipLaunchKernelGGL((kda_prefill_kernel<EI, K, OUT, SUM, ROLES>), grid,
+                           dim3(Shape::kThreads), 0, stream, p);
         return hipGetLastError();
     };
-    auto with_k = [&]<int OUT, bool SUM>() {
-        return p.K == 64 ? go.template operator()<64, OUT, SUM>()
-                         : go.template operator()<128, OUT, SUM>();
+    auto with_k = [&]<int OUT, bool SUM, bool ROLES>() {
+        return p.K == 64 ? go.template operator()<64, OUT, SUM, ROLES>()
+                         : go.template operator()<128, OUT, SUM, ROLES>();
+    };
+    auto with_roles = [&]<int OUT>() {
+        return pass == PrePass::roles ? with_k.template operator()<OUT, false, true>()
+                                      : with_k.template operator()<OUT, false, false>();
     };
     // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
-    return sum             ? with_k.template operator()<1, true>()
-           : p.out_dt == 0 ? with_k.template operator()<0, false>()
-           : p.out_dt == 1 ? with_k.template operator()<1, false>()
-                           : with_k.template operator()<2, false>();
+    return pass == PrePass::sums ? with_k.template operator()<1, true, true>()
+           : p.out_dt == 0       ? with_roles.template operator()<0>()
+           : p.out_dt == 1       ? with_roles.template operator()<1>()
+                                 : with_roles.template operator()<2>();
 }
 
-hipError_t launch_prefill_f32(const DeltaProblem &p, bool sum, hipStream_t stream);
-hipError_t launch_prefill_bf16(const DeltaProblem &p, bool sum, hipStream_t stream);
-hipError_t launch_prefill_f16(const DeltaProblem &p, bool sum, hipStream_t stream);
+hipError_t launch_prefill_f32(const DeltaProblem &p, PrePass pass, hipStream_t stream);
+hipError_t launch_prefill_bf16(const DeltaProblem &p, PrePass pass, hipStream_t stream);
+hipError_t launch_prefill_f16(const DeltaProblem &p, PrePass pass, hipStream_t stream);
 
 }  // namespace kda

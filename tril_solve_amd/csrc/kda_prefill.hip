@@ -78,10 +78,16 @@ __global__ __launch_bounds__(256) void kda_prefill_join_kernel(DeltaProblem p) {
     }
 }
 
-hipError_t launch_pass(const DeltaProblem &p, int in_dt, bool sum, hipStream_t stream) {
-    return in_dt == 0   ? launch_prefill_f32(p, sum, stream)
-           : in_dt == 1 ? launch_prefill_bf16(p, sum, stream)
-                        : launch_prefill_f16(p, sum, stream);
+// Workgroups per request and head.
+int column_blocks(int V) {
+    constexpr int each = PreShape<false, true>::kCols * kPreCols;
+    return (V + each - 1) / each;
+}
+
+hipError_t launch_pass(const DeltaProblem &p, int in_dt, PrePass pass, hipStream_t stream) {
+    return in_dt == 0   ? launch_prefill_f32(p, pass, stream)
+           : in_dt == 1 ? launch_prefill_bf16(p, pass, stream)
+                        : launch_prefill_f16(p, pass, stream);
 }
 
 }  // namespace
@@ -90,18 +96,18 @@ hipError_t launch_pass(const DeltaProblem &p, int in_dt, bool sum, hipStream_t s
 // columns) workgroups leave most of the 256 compute units idle; a cut prompt
 // takes the chunks of its segments at once, for about 2.4 times the work.
 int32_t prefill_segments(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t V) {
-    const int64_t walks = num_seqs * H * ((V + kPreWaves * kPreCols - 1) / (kPreWaves * kPreCols));
+    const int64_t walks = num_seqs * H * column_blocks(V);
     const int64_t chunks = total_tokens / kPreC;
-    if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 96 || chunks < 16 * num_seqs)
+    if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 64 || chunks < 16 * num_seqs)
         return 0;
-    const int64_t parts = 512 * num_seqs / walks;  // two workgroups per compute unit
+    const int64_t parts = 256 * num_seqs / walks;  // a workgroup per compute unit
     const int64_t seg = (chunks + parts - 1) / parts;
     return (int32_t)(kPreC * (seg < 4 ? 4 : seg));
 }
 
 hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) {
     if (p.seg != 0) {
-        hipError_t e = launch_pass(p, in_dt, true, stream);
+        hipError_t e = launch_pass(p, in_dt, PrePass::sums, stream);
         if (e != hipSuccess) return e;
         const dim3 grid((unsigned)(p.req.num_seqs * p.H), (unsigned)(p.V / 16));
         if (p.K == 64)
@@ -111,7 +117,8 @@ hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) 
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return launch_pass(p, in_dt, false, stream);
+    const int64_t walks = (p.seg != 0 ? p.segs : p.req.num_seqs) * (int64_t)p.H * column_blocks(p.V);
+    return launch_pass(p, in_dt, walks <= 256 ? PrePass::roles : PrePass::whole, stream);
 }
 
 }  // namespace kda

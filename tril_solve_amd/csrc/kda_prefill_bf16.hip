@@ -4,8 +4,8 @@
 
 namespace kda {
 
-hipError_t launch_prefill_bf16(const DeltaProblem &p, bool sum, hipStream_t stream) {
-    return launch_prefill_of<BF16>(p, sum, stream);
+hipError_t launch_prefill_bf16(const DeltaProblem &p, PrePass pass, hipStream_t stream) {
+    return launch_prefill_of<BF16>(p, pass, stream);
 }
 
 }  // namespace kda

@@ -4,8 +4,8 @@
 
 namespace kda {
 
-hipError_t launch_prefill_f16(const DeltaProblem &p, bool sum, hipStream_t stream) {
-    return launch_prefill_of<F16>(p, sum, stream);
+hipError_t launch_prefill_f16(const DeltaProblem &p, PrePass pass, hipStream_t stream) {
+    return launch_prefill_of<F16>(p, pass, stream);
 }
 
 }  // namespace kda
