@@ -920,10 +920,14 @@ kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                __builtin_nontemporal_store(
-                    f2{S[rt][0][s], S[rt][1][s]},
-                    reinterpret_cast<f2 *>(dst + (long)state_row(rt, s) * stride));
+            for (int s = 0; s < 4; ++s) {
+                const f2 v = {S[rt][0][s], S[rt][1][s]};
+                f2 *at = reinterpret_cast<f2 *>(dst + (long)state_row(rt, s) * stride);
+                if (SUM)  // read next
+                    *at = v;
+                else
+                    __builtin_nontemporal_store(v, at);
+            }
     };
     auto start_state = [&] {
         if (!SUM && sg.count > 1 && cols) {

@@ -7,18 +7,22 @@ namespace kda {
 namespace {
 
 // The states between a request's segments, S_{s + 1} = M_s S_s + B_s, in place
-// of the B_s: one workgroup per request, head and 16 value columns, a quarter
-// of the rows to a wavefront, on the FP32 matrix cores. The rows of the next
-// M_s, which do not depend on the state, are loaded during a step; the state
-// goes from one step's accumulators to the next one's operands through LDS.
-// Reduction index 4 (4 a + e) + g of a 16 x 16 x 4 product means channel
-// 16 a + 4 g + e, which is row e of lane group g in accumulator tile a.
+// of the B_s: one workgroup per request, head and 16 value columns, 16 rows to
+// a wavefront, on the FP32 matrix cores. What bounds it is a compute unit's
+// loads of M, 64 KB a step (2.3 us). It forms S^T = S^T M^T +
+// B^T, whose accumulators hold four adjacent columns of a row, so that B and S
+// move 16 bytes at a time. The rows of the next two M_s, which do not depend
+// on the state, are on their way during a step; the state goes from one step's
+// accumulators to the next one's operands through LDS. Reduction index
+// 4 (4 a + e) + g of the 16 x 16 x 4 products means channel 16 a + 4 g + e.
+constexpr int kAhead = 2;  // steps whose M is loaded ahead (even: two LDS buffers in turn)
 template <int K>
-__global__ __launch_bounds__(256) void kda_prefill_join_kernel(DeltaProblem p) {
-    constexpr int NT = K / 16, TPW = NT / 4;  // row tiles, those of a wavefront
-    __shared__ f4 st[2][NT][kWave];
+__global__ __launch_bounds__(4 * K, 2) void kda_prefill_join_kernel(DeltaProblem p) {
+    constexpr int NT = K / 16;  // wavefronts
+    constexpr int kRow = K + 4;  // floats between columns of the state in LDS
+    __shared__ __align__(16) float st[2][16 * kRow];
     const int lane = threadIdx.x & (kWave - 1), g4 = lane >> 4, n16 = lane & 15;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int row = threadIdx.x / kWave * 16 + n16;  // of M and the state
     const int n = blockIdx.x / p.H, h = blockIdx.x - n * p.H;
     int own;
     const int upto = segments_to_lane(p, own);
@@ -27,55 +31,53 @@ __global__ __launch_bounds__(256) void kda_prefill_join_kernel(DeltaProblem p) {
     const int end = min(first + count, p.segs) - 1;  // the last segment has no M and B
     if (first + 1 >= end || (p.pool.base != nullptr && request_slot(p.pool, n) < 0)) return;
 
-    const int col = blockIdx.y * 16 + n16;
-    auto states = [&](int j, int t) {  // rows 16 (TPW wv + t) + 4 g4 ..
-        return p.seg_state +
-               (((long)j * p.H + h) * K + 16 * (TPW * wv + t) + 4 * g4) * p.V + col;
+    auto state = [&](int j) -> f4 & {
+        return *reinterpret_cast<f4 *>(p.seg_state + (((long)j * p.H + h) * K + row) * p.V +
+                                       blockIdx.y * 16 + 4 * g4);
     };
-    f4 x[TPW], m[TPW][NT], b[TPW];
-    auto load = [&](int j) {
-#pragma unroll
-        for (int t = 0; t < TPW; ++t) {
-            const float *row = p.seg_map +
-                (((long)j * p.H + h) * K + 16 * (TPW * wv + t) + n16) * K + 4 * g4;
-#pragma unroll
-            for (int a = 0; a < NT; ++a) m[t][a] = *reinterpret_cast<const f4 *>(row + 16 * a);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b[t][e] = states(j, t)[(long)e * p.V];
-        }
+    struct Step {
+        f4 m[NT], b;
     };
-    load(first + 1);
+    Step ahead[kAhead];
+    auto load = [&](int j, Step &to) {
+        const float *m = p.seg_map + (((long)j * p.H + h) * K + row) * K + 4 * g4;
 #pragma unroll
-    for (int t = 0; t < TPW; ++t)
+        for (int a = 0; a < NT; ++a) to.m[a] = *reinterpret_cast<const f4 *>(m + 16 * a);
+        to.b = state(j);
+    };
+    f4 x;
+    auto step = [&](int j, Step &at, float *buf) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] = states(first, t)[(long)e * p.V];
-    for (int j = first + 1, buf = 0; j < end; ++j, buf ^= 1) {
-#pragma unroll
-        for (int t = 0; t < TPW; ++t) st[buf][TPW * wv + t][lane] = x[t];
-        f4 m_now[TPW][NT];
-#pragma unroll
-        for (int t = 0; t < TPW; ++t) {
-            x[t] = b[t];
-#pragma unroll
-            for (int a = 0; a < NT; ++a) m_now[t][a] = m[t][a];
-        }
+        for (int e = 0; e < 4; ++e) buf[(4 * g4 + e) * kRow + row] = x[e];
         __syncthreads();  // (the reads of the step before the last are done, too)
-        if (j + 1 < end) load(j + 1);
+        f4 s[NT];
 #pragma unroll
-        for (int a = 0; a < NT; ++a) {
-            const f4 s = st[buf][a][lane];
+        for (int a = 0; a < NT; ++a)
+            s[a] = *reinterpret_cast<const f4 *>(buf + n16 * kRow + 16 * a + 4 * g4);
+        f4 y = {0.0f, 0.0f, 0.0f, 0.0f};  // two sums: neither waits for itself
+        x = at.b;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+        for (int a = 0; a < NT; ++a)
 #pragma unroll
-                for (int t = 0; t < TPW; ++t)
-                    x[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(m_now[t][a][e], s[e], x[t], 0, 0,
-                                                                0);
+            for (int e = 0; e < 4; e += 2) {
+                x = __builtin_amdgcn_mfma_f32_16x16x4f32(s[a][e], at.m[a][e], x, 0, 0, 0);
+                y = __builtin_amdgcn_mfma_f32_16x16x4f32(s[a][e + 1], at.m[a][e + 1], y, 0, 0, 0);
+            }
+        load(min(j + kAhead, end - 1), at);
+        x += y;
+        state(j) = x;
+    };
+    x = state(first);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(min(first + 1 + i, end - 1), ahead[i]);
+    // (left from within: with steps or loads under conditions the compiler
+    // would wait for every load in flight)
+    for (int j = first + 1;;)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            step(j, ahead[i], st[i & 1]);
+            if (++j == end) return;
         }
-#pragma unroll
-        for (int t = 0; t < TPW; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) states(j, t)[(long)e * p.V] = x[t][e];
-    }
 }
 
 // Workgroups per request and head.
@@ -101,8 +103,12 @@ int32_t prefill_segments(int64_t total_tokens, int64_t num_seqs, int32_t H, int3
     if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 64 || chunks < 16 * num_seqs)
         return 0;
     const int64_t parts = 256 * num_seqs / walks;  // a workgroup per compute unit
-    const int64_t seg = (chunks + parts - 1) / parts;
-    return (int32_t)(kPreC * (seg < 4 ? 4 : seg));
+    int64_t seg = (chunks + parts - 1) / parts;
+    // A chunk more per segment takes 7 us of both passes, a segment more 2.3 us
+    // of the walk over them: at least four chunks, and about the square root of
+    // a third of a request's.
+    while (seg < 4 || 3 * seg * seg * num_seqs < chunks) ++seg;
+    return (int32_t)(kPreC * seg);
 }
 
 hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) {
@@ -113,11 +119,13 @@ hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) 
         if (p.K == 64)
             hipLaunchKernelGGL((kda_prefill_join_kernel<64>), grid, dim3(256), 0, stream, p);
         else
-            hipLaunchKernelGGL((kda_prefill_join_kernel<128>), grid, dim3(256), 0, stream, p);
+            hipLaunchKernelGGL((kda_prefill_join_kernel<128>), grid, dim3(512), 0, stream, p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int64_t walks = (p.seg != 0 ? p.segs : p.req.num_seqs) * (int64_t)p.H * column_blocks(p.V);
+    // (of the segments, p.segs - num_seqs at least exist)
+    const int64_t parts = p.seg != 0 ? p.segs - p.req.num_seqs : p.req.num_seqs;
+    const int64_t walks = parts * p.H * column_blocks(p.V);
     return launch_pass(p, in_dt, walks <= 256 ? PrePass::roles : PrePass::whole, stream);
 }
 
