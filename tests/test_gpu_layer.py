@@ -454,6 +454,154 @@ def test_delta_pool_past_4gib(kt, form):
     assert bool((pool[2000] == 7.0).all()) and bool((pool[:2000] == 0).all())
 
 
+# Prompts that are cut into segments (at least 16 chunks of 32 tokens a request,
+# few heads): the same tolerances, since the products that carry a state over a
+# segment are those that carry it over a chunk.
+
+CUT_LENS = [[512], [513], [640, 600], [1100, 0, 31, 1, 1500], [1000, 1025, 63, 32]]
+
+
+def _cut_size(kt, c):
+    return kt.kda_prefill_workspace_size(sum(c["lengths"]), len(c["lengths"]), c["H"], c["K"],
+                                         c["V"])
+
+
+@pytest.mark.parametrize("lengths", CUT_LENS)
+def test_prefill_cut_lengths(kt, lengths):
+    c = _delta_inputs(lengths, 2, 2, 128, 128, "f32", 140 + len(lengths))
+    assert _cut_size(kt, c) > 0
+    _delta_check(kt, "prefill", c)
+
+
+@pytest.mark.parametrize("H,Hk,K,V", [(1, 1, 64, 32), (6, 3, 128, 96), (2, 1, 128, 256),
+                                      (4, 1, 64, 160), (64, 16, 64, 64)])
+@pytest.mark.parametrize("gate", ["channel", "head"])
+def test_prefill_cut_heads(kt, gate, H, Hk, K, V):
+    c = _delta_inputs([700], H, Hk, K, V, "f32", 150 + V, gate=gate)
+    assert _cut_size(kt, c) > 0
+    _delta_check(kt, "prefill", c)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f16"),
+                                             ("bf16", "f32"), ("f32", "f16")])
+@pytest.mark.parametrize("rate", ["slow", "mixed", "steep"])
+def test_prefill_cut_types_and_decays(kt, rate, dtype, out_dtype):
+    """Also decays that leave nothing of a state within a segment (its map all
+    but zero), and resets."""
+    for K in (64, 128):
+        c = _delta_inputs([900, 570], 2, 2, K, 64, dtype, 160 + K, rate=rate)
+        assert _cut_size(kt, c) > 0
+        _delta_check(kt, "prefill", c, out_dtype=out_dtype)
+
+
+def test_prefill_cut_pools(kt):
+    """No pool; slots of their own; padding entries; every init."""
+    c = _delta_inputs([600, 33, 0, 1700], 2, 2, 64, 64, "f32", 170)
+    assert _cut_size(kt, c) > 0
+    _delta_check(kt, "prefill", c, pool=False)
+    _delta_check(kt, "prefill", c, slot=None, init=None)
+    _delta_check(kt, "prefill", c, init=np.zeros(4, np.int32), scale=0.7)
+    _delta_check(kt, "prefill", c, slot=np.array([3, -1, 1, 77], np.int32))
+
+
+def _with_workspace(kt, c, nbytes, fill=float("nan"), cu=None):
+    """kda_prefill with a workspace of nbytes inside a larger filled buffer:
+    out, state and the buffer before and after the workspace."""
+    buf = torch.full((nbytes // 4 + 512,), fill, device=DEV)
+    ws = buf[256:256 + nbytes // 4]
+    S, out = _dev(c["state"]), torch.zeros_like(c["v"])
+    kt.kda_prefill(c["q"], c["k"], c["v"], _dev(c["g"]), _dev(c["beta"]), out,
+                   _cu(c["lengths"]) if cu is None else _dev(cu), state=S, slot=_dev(c["slot"]),
+                   init=_dev(c["init"]), workspace=ws if nbytes else None)
+    torch.cuda.synchronize()
+    return out, S, torch.cat([buf[:256], buf[256 + nbytes // 4:]]), ws
+
+
+def test_prefill_workspace_contents(kt):
+    """What a workspace holds before does not matter, and nothing is written
+    outside of it; with one that is too small, or none, requests run whole and
+    it keeps its bits."""
+    c = _delta_inputs([900, 0, 1300], 2, 2, 128, 128, "bf16", 171)
+    n = _cut_size(kt, c)
+    a = _with_workspace(kt, c, n)
+    b = _with_workspace(kt, c, n, fill=5.0)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert bool(a[2].isnan().all()) and bool((b[2] == 5.0).all())
+    whole = _with_workspace(kt, c, 0)
+    short = _with_workspace(kt, c, n - 16, fill=5.0)
+    assert torch.equal(whole[0], short[0]) and torch.equal(whole[1], short[1])
+    assert bool((short[3] == 5.0).all())
+    big = _with_workspace(kt, c, n + 64)
+    assert torch.equal(a[0], big[0]) and torch.equal(a[1], big[1])
+    dense = _delta_inputs([800, 800], 2, 2, 128, 64, "bf16", 172)
+    rows = lambda x: x.view((2, 800) + x.shape[1:])  # noqa: E731
+    g, beta = _dev(dense["g"]), _dev(dense["beta"])
+    S1, S2 = _dev(dense["state"]), _dev(dense["state"])
+    packed = kt.prefill(dense["q"], dense["k"], dense["v"], g, beta, _cu([800, 800]), state=S1)
+    got = kt.prefill(rows(dense["q"]), rows(dense["k"]), rows(dense["v"]), rows(g), rows(beta),
+                     state=S2)
+    assert torch.equal(got.view(packed.shape), packed) and torch.equal(S1, S2)
+
+
+def test_prefill_cut_row_offsets_out_of_order(kt):
+    """Offsets that go back or past the rows are clamped: more segments than the
+    workspace holds are left out, and nothing outside of it is written."""
+    c = _delta_inputs([1100, 0, 1100, 0], 2, 2, 64, 64, "bf16", 173)
+    n = _cut_size(kt, c)
+    assert n > 0
+    for cu in ([0, 2200, 0, 2200, 2200], [0, 1100, 5000, -3, 2200], [2200, 0, 0, 0, 9]):
+        out, S, around, _ = _with_workspace(kt, c, n, fill=5.0, cu=np.array(cu, np.int32))
+        assert bool((around == 5.0).all())
+
+
+def test_prefill_cut_streams_and_graphs(kt):
+    """Two cut calls at once on streams and workspaces of their own, and a
+    replayed one with eager calls in between, give the bits of a call alone."""
+    c = _delta_inputs([1500, 600], 2, 2, 128, 128, "bf16", 174)
+    first, S0 = _delta_run(kt, "prefill", c)
+    g, beta, cu = _dev(c["g"]), _dev(c["beta"]), _cu(c["lengths"])
+    rest = dict(slot=_dev(c["slot"]), init=_dev(c["init"]))
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for side in sides:
+        S, out = _dev(c["state"]), torch.empty_like(first)
+        ws = torch.empty(_cut_size(kt, c), dtype=torch.uint8, device=DEV)
+        got.append((S, out, ws))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for side, (S, out, ws) in zip(sides, got):
+            with torch.cuda.stream(side):
+                S.copy_(_dev(c["state"]))
+            kt.kda_prefill(c["q"], c["k"], c["v"], g, beta, out, cu, state=S, workspace=ws,
+                           stream=side, **rest)
+    torch.cuda.synchronize()
+    for S, out, _ in got:
+        assert torch.equal(out, first) and torch.equal(S, S0)
+    S, out, ws = got[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kt.kda_prefill(c["q"], c["k"], c["v"], g, beta, out, cu, state=S, workspace=ws, **rest)
+    for _ in range(3):
+        S.copy_(_dev(c["state"]))
+        out.fill_(3.0)
+        ws.fill_(77)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first) and torch.equal(S, S0)
+        _delta_run(kt, "prefill", c)
+
+
+@pytest.mark.parametrize("requests,H", [(1, 257), (3, 100), (200, 2)])
+def test_prefill_many_workgroups(kt, requests, H):
+    """More workgroups than compute units: wavefronts that prepare and walk."""
+    c = _delta_inputs([37] * requests, H, H, 64, 32, "bf16", 175)
+    assert _cut_size(kt, c) == 0
+    _delta_check(kt, "prefill", c)
+    c = _delta_inputs([37] * requests, H, H, 128, 32, "f32", 176, rate="mixed")
+    _delta_check(kt, "prefill", c)
+
+
 # ----------------------------------------------------------------------- norm
 
 @pytest.mark.parametrize("out_dtype", ["f32", "bf16", "f16"])

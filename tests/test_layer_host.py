@@ -41,6 +41,14 @@ def test_delta_refusals(kt, form):
            dict(o=8 * G), dict(S=4 * G), dict(o=9 * G)]
     if form == "prefill":
         bad.append(dict(ws=11 * G + 8, wsb=64))
+        bad.append(dict(wsb=64))
+        # prompts that are cut: the workspace is used, and may not overlap
+        n = kt.kda_prefill_workspace_size(2048, 2, 4, 128, 128)
+        assert 0 < n < G
+        for at in (1, 2, 3, 4, 5, 6, 8):
+            bad.append(dict(T=2048, ws=at * G, wsb=n))
+        bad += [dict(T=2048, ws=7 * G + 16 - n, wsb=n), dict(T=2048, ws=9 * G, wsb=n),
+                dict(T=2048, ws=10 * G, wsb=n)]
     for kw in bad:
         assert _delta(kt, form, **kw) == E, kw
     for kw in [dict(K=96, gate=96), dict(K=256, gate=256), dict(V=48), dict(V=288), dict(H=8192),
@@ -62,7 +70,18 @@ def test_prefill_workspace_query(kt):
         with pytest.raises(kt.KdaError) as e:
             kt.kda_prefill_workspace_size(*args)
         assert e.value.status == kt.KDA_ERR_UNSUPPORTED
-    assert kt.kda_prefill_workspace_size(0, 0, 4, 128, 128) == 0
+    size = kt.kda_prefill_workspace_size
+    assert size(0, 0, 4, 128, 128) == 0
+    # no cut: short prompts, many heads or requests
+    assert size(511, 1, 4, 128, 128) == 0 and size(1023, 2, 4, 128, 128) == 0
+    assert size(65536, 1, 65, 128, 128) == 0 and size(65536, 1, 33, 128, 256) == 0
+    assert size(1 << 20, 65, 1, 128, 128) == 0 and size(0, 1, 1, 64, 32) == 0
+    # segments of whole chunks: [segments, H, K, V + K] and [requests, H, K, V]
+    for T, n, H, K, V in [(512, 1, 1, 128, 128), (16384, 1, 32, 128, 128), (5000, 7, 3, 64, 96),
+                          (2 ** 31 - 100, 1, 1, 128, 256), (2 ** 31 - 100, 64, 1, 64, 32)]:
+        words = size(T, n, H, K, V) // 4 - n * H * K * V
+        segments = words // (H * K * (V + K))
+        assert words == segments * H * K * (V + K) and 2 <= segments - n <= 256 * n
 
 
 def _conv(kt, dense=False, x=1 * G, d=0, cw=2 * G, q=3 * G, k=4 * G, v=5 * G, cu=6 * G, n=2, T=64,
