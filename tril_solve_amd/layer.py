@@ -135,11 +135,11 @@ def chunk_map(seq_lens, total_tokens: int, chunk_size: int = 64, stream=None):
     if chunk_size not in CHUNK_SIZES:
         _bad(f"chunk size {chunk_size} (16, 32 or 64)")
     n = seq_lens.numel()
+    _int32(n, "seq_lens", seq_lens)
     with _alloc_stream(stream):
-        cu = torch.empty(n + 1, dtype=torch.int32, device=seq_lens.device)
-        pairs = torch.empty((total_tokens // chunk_size + n, 2), dtype=torch.int32,
-                            device=seq_lens.device)
-        count = torch.empty(1, dtype=torch.int32, device=seq_lens.device)
+        cu = seq_lens.new_empty(n + 1)
+        pairs = seq_lens.new_empty((total_tokens // chunk_size + n, 2))
+        count = seq_lens.new_empty(1)
     kda_chunk_map(seq_lens, total_tokens, chunk_size, cu, pairs, count, stream)
     return cu, pairs, count
 
