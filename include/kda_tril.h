@@ -413,14 +413,21 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  *   out    [T, H, V] of out_dtype.
  *   state  [num_slots, H, K, V].
  * K 64 or 128, V a multiple of 32 up to 256, num_seqs x H < 2^23, else
- * KDA_ERR_UNSUPPORTED. Arithmetic is FP32 with FP32 state and sums; the
- * chunked form's products take each FP32 factor as two bfloat16 parts (about
- * 2^-17 of each term).
+ * KDA_ERR_UNSUPPORTED. State, decays and sums are FP32. The chunked form's
+ * products take each FP32 factor as two or three bfloat16 parts: what the
+ * state and an FP32 output are summed from is kept to about 2^-24 of each
+ * term, corrections to them and what a 16-bit output is summed from to about
+ * 2^-17 (state within 1e-6 of exact arithmetic over 16,384 tokens).
  *
- * workspace: kda_prefill_* uses the workspace, when one of at least
- * kda_prefill_workspace_size bytes is given, to cut long requests into
- * segments that run side by side; without it (NULL, 0) each request runs in
- * one piece. 16-byte aligned; concurrent calls need different workspaces.
+ * workspace: with one of at least kda_prefill_workspace_size bytes,
+ * kda_prefill_* cuts long prompts on few heads into segments of whole chunks
+ * that run side by side (the results agree to rounding with those of one
+ * piece). The size is 0 where that would not pay: for more than 64 (request,
+ * head, 128 value columns) triples or 64 requests, or fewer than 512 tokens
+ * per request on average. With a smaller one, or none (NULL, 0), each request
+ * runs in one piece. 16-byte aligned, overlapping no other argument; its
+ * contents need not be kept; concurrent calls (and captured graphs that may
+ * replay at once) need different ones.
  */
 kda_status kda_prefill_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t K,
                                       int32_t V, size_t *bytes);

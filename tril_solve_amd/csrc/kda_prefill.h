@@ -10,10 +10,10 @@
 // which is the recurrence S <- diag(e^g) S, u = beta (v - S^T k), S += k u^T,
 // o = scale S^T q of 32 tokens at once (the decode step's recurrence).
 //
-// One workgroup of four wavefronts per request, value head and 128 value
-// columns walks the request's chunks. Every product runs on the bfloat16
-// matrix cores with FP32 accumulators, each FP32 factor taken as a sum of
-// bfloat16 parts (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)):
+// A workgroup per request, value head and 128 value columns walks the request's
+// chunks. Every product runs on the bfloat16 matrix cores with FP32
+// accumulators, each FP32 factor taken as a sum of bfloat16 parts
+// (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)):
 //   6 products (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; about 2^-24 of
 //     each term) for what the state is summed from, (k e^{G_32 - G})^T U and
 //     the inverse times the right-hand side, and for everything an FP32
@@ -31,9 +31,9 @@
 //     state, tile 2 i + b holding channels 32 i + 8 g + 4 b + s, so that keys
 //     and queries keep their order. The chain k S -> U -> O, S thus stays
 //     inside the wavefront's registers.
-//   * The A operands (decayed keys and queries, the inverse of I + L, P) are
-//     the same for all columns: the wavefronts prepare them together in LDS,
-//     8 tokens each.
+//   * The A operands (decayed keys and queries, the inverse of I + L times
+//     beta, P) are the same for all columns: four wavefronts prepare them
+//     together in LDS, 8 tokens each.
 //   * Decays enter as factors relative to the chunk's middle, G_16 =: m:
 //     e^{G_i - G_j} = e^{G_i - m} e^{m - G_j}, and with S' = e^m S
 //       (k e^G) S = (k e^{G - m}) S',  (q e^G) S likewise,
@@ -43,7 +43,21 @@
 //     the decay of 16 adjacent tokens stays within e^{-64}. A chunk that has a
 //     steeper channel (or a gate that is not finite) forms its L and P from
 //     running products of the decays instead, every factor of which is the
-//     decay between two tokens, and takes the left-hand forms above.
+//     decay between two tokens, and takes the left-hand forms above. The factor
+//     e^{G_32 - m} is left owing and taken together with the next chunk's e^m.
+//
+// Two forms. With many workgroups, four wavefronts prepare a chunk and then
+// walk their columns through it, two workgroups to a compute unit (74 KB of
+// LDS each). With at most 256, wavefronts of either kind work side by side, one
+// chunk apart, on twice the LDS: 64 walks of 2,048 tokens 363 -> 271 us, 32
+// of 16,384 tokens 2.86 -> 2.09 ms; but 1,024 walks of 512 tokens, four rounds
+// of workgroups whose beginnings and ends nothing covers, 313 -> 335 us.
+//
+// What bounds it: instruction issue and, with all units at work, power (1.6 to
+// 1.8 of 2.4 GHz). A wavefront's chunk is about 250 matrix instructions and
+// 1,090 vector instructions, 16 and 4 cycles each, most of them the splits into
+// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 311 us: 2.8 TB/s
+// of the 5.1 that a copy reaches, 0.8 of 2.5 PFLOP/s of the products as run.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -140,7 +154,8 @@ __device__ __forceinline__ void mul_columns(const A &a, const B (&b)[2], f4 (&c)
 #pragma unroll
     for (int i = 0; i < M; ++i)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) c[ct] = mfma(a.p[part_a(M, i)], b[ct].p[part_b(M, i)], c[ct]);
+        for (int ct = 0; ct < 2; ++ct)
+            c[ct] = mfma(a.p[part_a(M, i)], b[ct].p[part_b(M, i)], c[ct]);
 }
 
 // Shapes the schedule of the code around it: N times one matrix instruction
@@ -465,8 +480,9 @@ struct PreShape {
     static_assert(ROLES || kCols == kPreWaves);
 };
 template <class EI, int K, int OUT, bool SUM, bool ROLES>
-__global__ __launch_bounds__((PreShape<SUM, ROLES>::kThreads), (PreShape<SUM, ROLES>::kPerSimd)) void
-kda_prefill_kernel(DeltaProblem p) {
+__global__
+__launch_bounds__((PreShape<SUM, ROLES>::kThreads), (PreShape<SUM, ROLES>::kPerSimd))
+void kda_prefill_kernel(DeltaProblem p) {
     typedef PreLds<K, OUT, ROLES ? 2 : 1> L;
     constexpr int CW = PreShape<SUM, ROLES>::kCols;
     constexpr int NT = K / 16;  // state row tiles
@@ -1047,7 +1063,8 @@ kda_prefill_kernel(DeltaProblem p) {
                     for (int ct = 0; ct < 2; ++ct) {
                         const auto &bc = b[kk & 1][ct];
                         if (i < 3)
-                            kS[I][ct] = mfma(ka_op[I].p[part_a(3, i)], bc.p[part_b(3, i)], kS[I][ct]);
+                            kS[I][ct] =
+                                mfma(ka_op[I].p[part_a(3, i)], bc.p[part_b(3, i)], kS[I][ct]);
                         o[I][ct] = mfma(qa_op[I].p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
                     }
             }
@@ -1229,8 +1246,6 @@ kda_prefill_kernel(DeltaProblem p) {
     }
 }
 
-// Wavefronts that do one thing each shorten a chunk of a lone workgroup, but
-// take a compute unit's whole LDS.
 template <class EI>
 hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t stream) {
     const int64_t parts = p.seg != 0 ? p.segs : p.req.num_seqs;
@@ -1242,19 +1257,21 @@ hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t st
                            dim3(Shape::kThreads), 0, stream, p);
         return hipGetLastError();
     };
-    auto with_k = [&]<int OUT, bool SUM, bool ROLES>() {
-        return p.K == 64 ? go.template operator()<64, OUT, SUM, ROLES>()
-                         : go.template operator()<128, OUT, SUM, ROLES>();
+    auto with_out = [&]<int K, int OUT>() {
+        // FP32 rows on their way leave a wavefront that does both without
+        // registers (spills; 1,024 walks of 512 tokens 420 -> 542 us)
+        constexpr bool kRoles = EI::kBytes == 4 && K == 128;
+        if (kRoles || pass == PrePass::roles) return go.template operator()<K, OUT, false, true>();
+        return go.template operator()<K, OUT, false, kRoles>();
     };
-    auto with_roles = [&]<int OUT>() {
-        return pass == PrePass::roles ? with_k.template operator()<OUT, false, true>()
-                                      : with_k.template operator()<OUT, false, false>();
+    auto with_k = [&]<int K>() {
+        // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
+        return pass == PrePass::sums ? go.template operator()<K, 1, true, true>()
+               : p.out_dt == 0       ? with_out.template operator()<K, 0>()
+               : p.out_dt == 1       ? with_out.template operator()<K, 1>()
+                                     : with_out.template operator()<K, 2>();
     };
-    // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
-    return pass == PrePass::sums ? with_k.template operator()<1, true, true>()
-           : p.out_dt == 0       ? with_roles.template operator()<0>()
-           : p.out_dt == 1       ? with_roles.template operator()<1>()
-                                 : with_roles.template operator()<2>();
+    return p.K == 64 ? with_k.template operator()<64>() : with_k.template operator()<128>();
 }
 
 hipError_t launch_prefill_f32(const DeltaProblem &p, PrePass pass, hipStream_t stream);
