@@ -1212,11 +1212,15 @@ void kda_prefill_kernel(DeltaProblem p) {
         if (len_all > 0) load_rows(0, now);
         for (int t0 = 0; t0 < len_all; t0 += kPreC) {
             bool far, apart;
+            // The other workgroup of the compute unit gives way to a walk (8 x 2,048
+            // tokens: 628 -> 598 us; K = 64, with three workgroups: 163 -> 170 us).
+            if (K == 128) __builtin_amdgcn_s_setprio(0);
             sum_decays(0);
             __syncthreads();  // totals; nothing reads the chunk before any more
             prepare(0, far, apart);
             if (cols) load_values(t0);
             __syncthreads();
+            if (K == 128) __builtin_amdgcn_s_setprio(2);
             if (t0 + kPreC < len_all) load_rows(t0 + kPreC, now);
             if (cols) use(t0, 0, far, apart);
         }

@@ -274,13 +274,13 @@ def prefill(q, k, v, g, beta, cu_seqlens=None, state=None, slot=None, init=None,
     """Convenience form of kda_prefill: returns out (``out_dtype``, default v's
     dtype) and allocates the workspace with torch."""
     out = _empty_as(v, out_dtype, stream)
-    n = v.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    H, V = v.shape[-2:]
-    nbytes = kda_prefill_workspace_size(v.numel() // max(H * V, 1), n, H, q.shape[-1], V)
-    ws = None
-    if nbytes:
-        with _alloc_stream(stream):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=v.device)
+    n, (H, V) = v.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1, v.shape[-2:]
+    tokens, ws = v.numel() // max(H * V, 1), None
+    if tokens >= 512 * n:  # else no workspace is wanted
+        nbytes = kda_prefill_workspace_size(tokens, n, H, q.shape[-1], V)
+        if nbytes:
+            with _alloc_stream(stream):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=v.device)
     kda_prefill(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, ws, stream)
     return out
 
