@@ -448,7 +448,7 @@ __device__ __forceinline__ int lane_prefix(int x) {  // inclusive sum over the w
 __device__ __forceinline__ int segments_to_lane(const DeltaProblem &p, int &own) {
     const int lane = threadIdx.x & (kWave - 1);
     own = 0;
-    if (lane < p.req.num_seqs) own = max(1, (request_rows(p.req, lane).y + p.seg - 1) / p.seg);
+    if (lane < p.req.num_seqs) own = 1 + max(request_rows(p.req, lane).y - 1, 0) / p.seg;
     return lane_prefix(own);
 }
 __device__ __forceinline__ Segment find_segment(const DeltaProblem &p, int j) {
