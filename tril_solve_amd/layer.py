@@ -81,7 +81,7 @@ def _addr(t):
 
 def _int32(n, name, t):
     """An int32 vector of n entries (or None)."""
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n):
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n):
         _bad(f"{name} must be int32 [{n}]")
 
 
@@ -90,19 +90,19 @@ def _float32(name, t):
         _bad(f"{name} must be float32")
 
 
-def _requests(x, lead, cu_seqlens):
-    """(number of requests, their C arguments) of a token tensor whose token
-    dimension is followed by `lead` - 1 others."""
+def _requests(shape, lead, cu_seqlens):
+    """(number of requests, their C arguments) of token tensors of this shape,
+    the token dimension followed by `lead` - 1 others."""
     if cu_seqlens is None:
-        if x.dim() != lead + 1:
+        if len(shape) != lead + 1:
             _bad("dense inputs are [B, T, ...]")
-        return x.shape[0], (x.shape[0], x.shape[1])
-    if x.dim() != lead:
+        return shape[0], (shape[0], shape[1])
+    if len(shape) != lead:
         _bad("packed inputs are [T, ...]")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+    n = cu_seqlens.numel() - 1
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or n < 0:
         _bad("cu_seqlens must be int32 [requests + 1]")
-    n = cu_seqlens.shape[0] - 1
-    return n, (cu_seqlens.data_ptr(), n, x.shape[0])
+    return n, (cu_seqlens.data_ptr(), n, shape[0])
 
 
 # ---- chunk maps ------------------------------------------------------------
@@ -152,10 +152,10 @@ def kda_conv_prefill(qkv, conv_w, q, k, v, cu_seqlens=None, conv_state=None, slo
     ``cu_seqlens``) or dense [B, T, 3, H, d] inputs into q, k, v [.., H, d];
     ``conv_state`` [slots, 3, H, W - 1, d] is updated in place."""
     s = _place(stream, (qkv, conv_w, q, k, v, cu_seqlens, conv_state, slot, init))
-    n, req = _requests(qkv, 4, cu_seqlens)
-    shape, W = qkv.shape, conv_w.shape[1] if conv_w.dim() == 4 else 0
-    H, d = shape[-2:]
-    if shape[-3] != 3 or conv_w.shape != (3, W, H, d):
+    shape, taps = qkv.shape, conv_w.shape
+    n, req = _requests(shape, 4, cu_seqlens)
+    W, (H, d) = taps[1] if len(taps) == 4 else 0, shape[-2:]
+    if shape[-3] != 3 or taps != (3, W, H, d):
         _bad("shapes: qkv [.., 3, H, d], conv_w [3, W, H, d]")
     rows = shape[:-3] + (H, d)
     if q.shape != rows or k.shape != rows or v.shape != rows:
@@ -168,9 +168,10 @@ def kda_conv_prefill(qkv, conv_w, q, k, v, cu_seqlens=None, conv_state=None, slo
     _int32(n, "init", init)
     slots = 0
     if conv_state is not None:
-        if conv_state.shape[1:] != (3, H, W - 1, d):
+        windows = conv_state.shape
+        if windows[1:] != (3, H, W - 1, d):
             _bad("conv_state must be [slots, 3, H, W - 1, d]")
-        slots = conv_state.shape[0]
+        slots = windows[0]
     fn = _lib.kda_conv_prefill_dense if cu_seqlens is None else _lib.kda_conv_prefill_packed
     _check(fn(qkv.data_ptr(), _code(qkv), conv_w.data_ptr(), q.data_ptr(), k.data_ptr(),
               v.data_ptr(), *req, H, d, W, _addr(conv_state), _addr(slot), _addr(init), slots,
@@ -192,19 +193,16 @@ def conv_prefill(qkv, conv_w, cu_seqlens=None, conv_state=None, slot=None, init=
 
 def _delta_args(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, stream, workspace):
     s = _place(stream, (q, k, v, g, beta, out, cu_seqlens, state, slot, init, workspace))
-    n, req = _requests(q, 3, cu_seqlens)
     qs, vs = q.shape, v.shape
-    if len(vs) != len(qs):
-        _bad("shapes: q, k [.., Hk, K], v, out [.., H, V], beta [.., H]")
-    lead, Hk, K = qs[:-2], qs[-2], qs[-1]
-    H, V = vs[-2:]
-    rows = lead + (H,)
-    if k.shape != qs or vs != rows + (V,) or out.shape != vs or beta.shape != rows:
+    n, req = _requests(qs, 3, cu_seqlens)
+    rows, (Hk, K), (H, V) = vs[:-1], qs[-2:], vs[-2:]
+    if k.shape != qs or vs[:-2] != qs[:-2] or out.shape != vs or beta.shape != rows:
         _bad("shapes: q, k [.., Hk, K], v, out [.., H, V], beta [.., H]")
     if not q.dtype == k.dtype == v.dtype:
         _bad("q, k and v must have one dtype")
-    gate = K if g.dim() == len(vs) else 1
-    if g.shape != (rows + (K,) if gate == K else rows):
+    gs = g.shape
+    gate = K if len(gs) == len(vs) else 1
+    if gs != (rows + (K,) if gate == K else rows):
         _bad("g must be [.., H, K] or [.., H]")
     _float32("g", g)
     _float32("beta", beta)
@@ -213,9 +211,10 @@ def _delta_args(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, str
     _int32(n, "init", init)
     slots = 0
     if state is not None:
-        if state.shape[1:] != (H, K, V):
+        states = state.shape
+        if states[1:] != (H, K, V):
             _bad("state must be [slots, H, K, V]")
-        slots = state.shape[0]
+        slots = states[0]
     if scale is None:
         scale = K ** -0.5
     return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), _code(q), g.data_ptr(), beta.data_ptr(),
@@ -322,13 +321,14 @@ def kda_gated_norm(o, z, norm_w, out, eps_norm=1e-6, stream=None) -> None:
     """out = o / sqrt(mean(o^2) + eps) * norm_w * sigmoid(z) over the last
     dimension of o, z, out [.., H, d]; out may be o."""
     s = _place(stream, (o, z, norm_w, out))
-    if o.dim() < 2 or z.shape != o.shape or out.shape != o.shape or norm_w.shape != o.shape[-1:]:
+    shape = o.shape
+    if len(shape) < 2 or z.shape != shape or out.shape != shape or norm_w.shape != shape[-1:]:
         _bad("shapes: o, z, out [.., H, d], norm_w [d]")
     if z.dtype != o.dtype:
         _bad("z must have o's dtype")
     _float32("norm_w", norm_w)
-    H, d = o.shape[-2:]
-    rows = o.numel() // (H * d) if H * d else 0
+    H, d = shape[-2:]
+    rows = o.numel() // (H * d) if H and d else 0
     _check(_lib.kda_gated_norm(o.data_ptr(), z.data_ptr(), _code(o), norm_w.data_ptr(),
                                out.data_ptr(), _code(out), rows, H, d, eps_norm, s))
 
