@@ -68,7 +68,6 @@ namespace kda {
 
 constexpr int kPreC = 32;  // tokens per chunk
 constexpr int kPreWaves = 4;  // that prepare a chunk
-constexpr int kPreCols = 32;  // value columns per wavefront
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kSteep = 64.0f * kLog2E;  // in powers of two
 
@@ -149,12 +148,12 @@ constexpr int part_b(int M, int i) {
     constexpr int b[] = {0, 2, 1, 0, 1, 0};
     return b[6 - M + i];
 }
-template <int M, class A, class B>
-__device__ __forceinline__ void mul_columns(const A &a, const B (&b)[2], f4 (&c)[2]) {
+template <int M, int CT, class A, class B>
+__device__ __forceinline__ void mul_columns(const A &a, const B (&b)[CT], f4 (&c)[CT]) {
 #pragma unroll
     for (int i = 0; i < M; ++i)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
+        for (int ct = 0; ct < CT; ++ct)
             c[ct] = mfma(a.p[part_a(M, i)], b[ct].p[part_b(M, i)], c[ct]);
 }
 
@@ -221,6 +220,22 @@ struct RawC<E, 2> {
     __device__ __forceinline__ float at(int i) const {
         return Elem<E>::widen(i ? w >> 16 : w & 0xFFFFu);
     }
+};
+template <class E>
+struct RawC<E, 1> {
+    uint16_t w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
+        w = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    }
+    __device__ __forceinline__ float at(int) const { return Elem<E>::widen(w); }
+};
+template <>
+struct RawC<F32, 1> {
+    float w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t off) {
+        w = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    }
+    __device__ __forceinline__ float at(int) const { return w; }
 };
 template <>
 struct RawC<F32, 2> {
@@ -471,20 +486,23 @@ __device__ __forceinline__ Segment find_segment(const DeltaProblem &p, int j) {
 // state, and then is S_after), M from the identity and with V = 0.
 // ROLES: four wavefronts prepare the next chunk while others (kCols) take their
 // columns of this one through it; else four wavefronts do both in turn.
-enum class PrePass { whole, roles, sums };
-template <bool SUM, bool ROLES>
+// CT: tiles of 16 columns to a wavefront.
+enum class PrePass { whole, roles, narrow, sums };
+template <bool SUM, bool ROLES, int CT>
 struct PreShape {
     static constexpr int kCols = SUM ? 8 : 4;  // wavefronts with columns
+    static constexpr int kWidth = kCols * 16 * CT;  // columns of a workgroup
     static constexpr int kThreads = kWave * (ROLES ? kCols + kPreWaves : kCols);
     static constexpr int kPerSimd = SUM ? 3 : 2;  // wavefronts, by their registers
     static_assert(ROLES || kCols == kPreWaves);
 };
-template <class EI, int K, int OUT, bool SUM, bool ROLES>
+template <class EI, int K, int OUT, bool SUM, bool ROLES, int CT>
 __global__
-__launch_bounds__((PreShape<SUM, ROLES>::kThreads), (PreShape<SUM, ROLES>::kPerSimd))
+__launch_bounds__((PreShape<SUM, ROLES, CT>::kThreads), (PreShape<SUM, ROLES, CT>::kPerSimd))
 void kda_prefill_kernel(DeltaProblem p) {
     typedef PreLds<K, OUT, ROLES ? 2 : 1> L;
-    constexpr int CW = PreShape<SUM, ROLES>::kCols;
+    typedef PreShape<SUM, ROLES, CT> Shape;
+    constexpr int CW = Shape::kCols;
     constexpr int NT = K / 16;  // state row tiles
     // A wavefront prepares 8 tokens: K / 4 lanes of 4 channels to a token, in
     // GRP groups of lanes with TPL tokens each.
@@ -503,7 +521,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     if (p.seg != 0) {
         sg = find_segment(p, j);
         if (sg.request < 0 || (SUM && sg.at + 1 == sg.count)) return;
-        if (SUM && sg.at == 0 && (int)(blockIdx.y * CW * kPreCols) >= p.V) return;
+        if (SUM && sg.at == 0 && (int)(blockIdx.y * Shape::kWidth) >= p.V) return;
     }
     const int n = sg.request;
     const int hk = h / (p.H / p.Hk);
@@ -516,10 +534,10 @@ void kda_prefill_kernel(DeltaProblem p) {
     const int slot = __builtin_amdgcn_readfirstlane(keep ? request_slot(p.pool, n) : 0);
 
     // this wavefront's columns: tile ct holds column col + ct of each lane
-    const int col0 = (blockIdx.y * CW + wv) * kPreCols;
+    const int col0 = (blockIdx.y * CW + wv) * 16 * CT;
     const bool map = SUM && col0 >= p.V;  // V is a multiple of 32
     const bool cols = walks && (SUM ? col0 < p.V + (sg.at ? K : 0) : col0 < p.V);
-    const int col = (cols ? map ? col0 - p.V : col0 : 0) + 2 * (lane0 & 15);
+    const int col = (cols ? map ? col0 - p.V : col0 : 0) + CT * (lane0 & 15);
 
     // Token tensors from the request's first row and this head on, and the
     // bytes between their rows (fewer than 2^21).
@@ -539,21 +557,28 @@ void kda_prefill_kernel(DeltaProblem p) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0,
                                                  (len - 1) * stride + width, kRsrcWord3);
     };
-    auto put_out = [&](Rsrc r, uint32_t off, float a, float b) {
-        if constexpr (OUT == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w2, f2{a, b}), r, off, 0,
-                                                  kNontemporal);
-        else
-            __builtin_amdgcn_raw_buffer_store_b32(
-                OUT == 1 ? Elem<BF16>::pack(a, b) : Elem<F16>::pack(a, b), r, off, 0,
-                kNontemporal);
+    auto put_out = [&](Rsrc r, uint32_t off, const f4 (&o)[CT], int s) {
+        if constexpr (OUT == 0 && CT == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w2, f2{o[0][s], o[1][s]}), r,
+                                                  off, 0, kNontemporal);
+        else if constexpr (OUT == 0)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (float)o[0][s]), r,
+                                                  off, 0, kNontemporal);
+        else {
+            const float a = o[0][s], b = o[CT - 1][s];
+            const uint32_t w = OUT == 1 ? Elem<BF16>::pack(a, b) : Elem<F16>::pack(a, b);
+            if constexpr (CT == 2)
+                __builtin_amdgcn_raw_buffer_store_b32(w, r, off, 0, kNontemporal);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, r, off, 0, kNontemporal);
+        }
     };
     if (slot < 0) {  // padding: zero outputs, no state
         if (!SUM && cols)
             for (int t = lane0 >> 4; t < len_all; t += 4)
 #pragma unroll
-                for (int c = 0; c < 2 * OE; c += 4)
-                    *reinterpret_cast<uint32_t *>(ob + (long)t * os + col * OE + c) = 0u;
+                for (int c = 0; c < CT * OE; c += 2)
+                    *reinterpret_cast<uint16_t *>(ob + (long)t * os + col * OE + c) = 0;
         return;
     }
 
@@ -916,7 +941,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     };
 
     // ======== this wavefront's columns
-    f4 S[NT][2];
+    f4 S[NT][CT];
     // [K, V] of this head in slot `at` of a tensor [.., H, K, V], this lane's part
     auto state_at = [&](float *base, int at) {
         return base + (((long)at * p.H + h) * K + 8 * (lane0 >> 4)) * p.V + col;
@@ -926,10 +951,14 @@ void kda_prefill_kernel(DeltaProblem p) {
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const f2 v = __builtin_nontemporal_load(
-                    reinterpret_cast<const f2 *>(src + (long)state_row(rt, s) * p.V));
-                S[rt][0][s] = v[0];
-                S[rt][1][s] = v[1];
+                const float *at = src + (long)state_row(rt, s) * p.V;
+                if constexpr (CT == 2) {
+                    const f2 v = __builtin_nontemporal_load(reinterpret_cast<const f2 *>(at));
+                    S[rt][0][s] = v[0];
+                    S[rt][1][s] = v[1];
+                } else {
+                    S[rt][0][s] = __builtin_nontemporal_load(at);
+                }
             }
     };
     auto store_state = [&](float *dst, int stride) {
@@ -937,12 +966,16 @@ void kda_prefill_kernel(DeltaProblem p) {
         for (int rt = 0; rt < NT; ++rt)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const f2 v = {S[rt][0][s], S[rt][1][s]};
-                f2 *at = reinterpret_cast<f2 *>(dst + (long)state_row(rt, s) * stride);
-                if (SUM)  // read next
-                    *at = v;
-                else
-                    __builtin_nontemporal_store(v, at);
+                float *at = dst + (long)state_row(rt, s) * stride;
+                if constexpr (CT == 2) {
+                    const f2 v = {S[rt][0][s], S[rt][1][s]};
+                    if (SUM)  // read next
+                        *reinterpret_cast<f2 *>(at) = v;
+                    else
+                        __builtin_nontemporal_store(v, reinterpret_cast<f2 *>(at));
+                } else {
+                    __builtin_nontemporal_store((float)S[rt][0][s], at);
+                }
             }
     };
     auto start_state = [&] {
@@ -956,7 +989,7 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
+                    for (int ct = 0; ct < CT; ++ct)
                         S[rt][ct][s] =
                             map && 8 * (lane0 >> 4) + state_row(rt, s) == col + ct ? 1.0f : 0.0f;
         }
@@ -964,7 +997,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         if (SUM && sg.at == 0 && cols) store_state(state_at(p.seg_first, n), p.V);
     };
     // the values of this wavefront's columns
-    RawC<EI, 2> vraw[2][4];
+    RawC<EI, CT> vraw[2][4];
     auto load_values = [&](int t0) {
         const int len = min(kPreC, len_all - t0);
         // (no row at all for M's columns: V = 0)
@@ -1012,9 +1045,11 @@ void kda_prefill_kernel(DeltaProblem p) {
         // ahead, and the state's next rows are scaled and split in the
         // products' shadow.
         const f4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-        f4 kS[2][2] = {{z, z}, {z, z}}, o[2][2] = {{z, z}, {z, z}};
+        f4 kS[2][CT], o[2][CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) kS[0][ct] = kS[1][ct] = o[0][ct] = o[1][ct] = z;
         Operand<2> ka_op[2];
-        Operand<NQ> qa_op[2], b[2][2];
+        Operand<NQ> qa_op[2], b[2][CT];
         f4 em[2];
         auto read_rows = [&](int j) {  // k-step j / 2, row tile j % 2
             const int at = 16 * (j & 1) * L::RS;
@@ -1038,29 +1073,29 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int rt = 0; rt < NT; ++rt) {
                 const f4 e =
                     *reinterpret_cast<const f4 *>(fac + L::EG + 4 * (8 * g4 + state_row(rt, 0)));
-                S[rt][0] *= e;
-                S[rt][1] *= e;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[rt][ct] *= e;
             }
         }
         read_em(0);
         read_rows(0);
-        split_state(0, 0);
-        split_state(0, 1);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) split_state(0, ct);
         read_em(1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < K / 16; ++j) {
             const int kk = j >> 1, I = j & 1;
             if (j + 1 < K / 16) read_rows(j + 1);
-            if (kk + 1 < K / 32) split_state(kk + 1, I);
+            if (kk + 1 < K / 32 && I < CT) split_state(kk + 1, I);
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
             if constexpr (SUM) {
-                mul_columns<3>(ka_op[I], b[kk & 1], kS[I]);
+                mul_columns<3, CT>(ka_op[I], b[kk & 1], kS[I]);
             } else {
 #pragma unroll
                 for (int i = 0; i < MQ; ++i)
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) {
+                    for (int ct = 0; ct < CT; ++ct) {
                         const auto &bc = b[kk & 1][ct];
                         if (i < 3)
                             kS[I][ct] =
@@ -1069,43 +1104,46 @@ void kda_prefill_kernel(DeltaProblem p) {
                     }
             }
             __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 2 : 2 + NQ, 0);  // LDS reads
-            interleave<SUM ? 6 : 6 + 2 * MQ, SUM ? 5 : 3>();
+            interleave<SUM ? 3 * CT : (3 + MQ) * CT, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time, X the inverse's diagonal blocks times beta:
         // R = V - (k e^G) S, U_0 = X_00 R_0, U_1 = X_11 (R_1 - (L_10 / beta) U_0)
-        f4 R[2][2];
+        f4 R[2][CT];
 #pragma unroll
         for (int I = 0; I < 2; ++I)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) R[I][ct][s] = vraw[I][s].at(ct) - kS[I][ct][s];
+                for (int ct = 0; ct < CT; ++ct) R[I][ct][s] = vraw[I][s].at(ct) - kS[I][ct][s];
         if (ROLES && t0 + kPreC < len_all) load_values(t0 + kPreC);
-        Operand<3> u[2];
+        Operand<3> u[CT];
         {
             const auto x0 = top_operand.template operator()<3>(L::TM);
             const auto x1 = low_operand.template operator()<3>(L::TM);
             const auto p0 = top_operand.template operator()<NQ>(L::PM);
             const auto p1 = low_operand.template operator()<NQ>(L::PM);
-            Half<3> r[2], h0[2];
-            f4 x[2] = {z, z};
+            Half<3> r[CT], h0[CT];
+            f4 x[CT];
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) r[ct] = split4<3>(R[0][ct]);
-            mul_columns<6>(x0, r, x);
+            for (int ct = 0; ct < CT; ++ct) {
+                r[ct] = split4<3>(R[0][ct]);
+                x[ct] = z;
+            }
+            mul_columns<6, CT>(x0, r, x);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) h0[ct] = split4<3>(x[ct]);
-            mul_columns<3>(half_of(x1, 0), h0, R[1]);
-            if constexpr (!SUM) mul_columns<MQ>(p0, h0, o[0]);
+            for (int ct = 0; ct < CT; ++ct) h0[ct] = split4<3>(x[ct]);
+            mul_columns<3, CT>(half_of(x1, 0), h0, R[1]);
+            if constexpr (!SUM) mul_columns<MQ, CT>(p0, h0, o[0]);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
+            for (int ct = 0; ct < CT; ++ct) {
                 r[ct] = split4<3>(R[1][ct]);
                 x[ct] = z;
             }
-            mul_columns<6>(half_of(x1, 1), r, x);
+            mul_columns<6, CT>(half_of(x1, 1), r, x);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) u[ct] = join(h0[ct], split4<3>(x[ct]));
-            if constexpr (!SUM) mul_columns<MQ>(p1, u, o[1]);
+            for (int ct = 0; ct < CT; ++ct) u[ct] = join(h0[ct], split4<3>(x[ct]));
+            if constexpr (!SUM) mul_columns<MQ, CT>(p1, u, o[1]);
         }
         if constexpr (!SUM) {
             const Rsrc ro = rows_of(ob + (long)t0 * os, os, p.V * OE, len);
@@ -1114,7 +1152,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int I = 0; I < 2; ++I)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    put_out(ro, at + (16 * I + s) * os, o[I][0][s], o[I][1][s]);
+                    put_out(ro, at + (16 * I + s) * os, o[I], s);
         }
         // the state: S' + (k e^{m - G})^T U, which owes e^{G_32 - m}; of a steep
         // chunk e^{G_32} S + (k e^{G_32 - G})^T U
@@ -1146,8 +1184,8 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int rt = 0; rt < NT; ++rt) {
                 const f4 e =
                     *reinterpret_cast<const f4 *>(fac + L::EF + 4 * (8 * g4 + state_row(rt, 0)));
-                S[rt][0] *= e;
-                S[rt][1] *= e;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[rt][ct] *= e;
             }
         }
         read_state(0);
@@ -1155,9 +1193,9 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
             if (rt + 1 < NT) read_state(rt + 1);
-            mul_columns<6>(kt[rt & 1], u, S[rt]);
+            mul_columns<6, CT>(kt[rt & 1], u, S[rt]);
             __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
-            interleave<12, 1>();
+            interleave<6 * CT, 1>();
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -1236,8 +1274,8 @@ void kda_prefill_kernel(DeltaProblem p) {
         for (int rt = 0; rt < NT; ++rt) {
             const f4 e =
                 *reinterpret_cast<const f4 *>(left + 8 * (lane0 >> 4) + state_row(rt, 0));
-            S[rt][0] *= e;
-            S[rt][1] *= e;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) S[rt][ct] *= e;
         }
     }
     if (SUM && cols) {
@@ -1253,11 +1291,12 @@ void kda_prefill_kernel(DeltaProblem p) {
 template <class EI>
 hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t stream) {
     const int64_t parts = p.seg != 0 ? p.segs : p.req.num_seqs;
-    auto go = [&]<int K, int OUT, bool SUM, bool ROLES>() {
-        typedef PreShape<SUM, ROLES> Shape;
-        const int cols = p.V + (SUM ? K : 0), each = Shape::kCols * kPreCols;
-        const dim3 grid((unsigned)(parts * p.H), (unsigned)((cols + each - 1) / each));
-        hipLaunchKernelGGL((kda_prefill_kernel<EI, K, OUT, SUM, ROLES>), grid,
+    auto go = [&]<int K, int OUT, bool SUM, bool ROLES, int CT>() {
+        typedef PreShape<SUM, ROLES, CT> Shape;
+        const int cols = p.V + (SUM ? K : 0);
+        const dim3 grid((unsigned)(parts * p.H),
+                        (unsigned)((cols + Shape::kWidth - 1) / Shape::kWidth));
+        hipLaunchKernelGGL((kda_prefill_kernel<EI, K, OUT, SUM, ROLES, CT>), grid,
                            dim3(Shape::kThreads), 0, stream, p);
         return hipGetLastError();
     };
@@ -1265,12 +1304,14 @@ hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t st
         // FP32 rows on their way leave a wavefront that does both without
         // registers (spills; 1,024 walks of 512 tokens 420 -> 542 us)
         constexpr bool kRoles = EI::kBytes == 4 && K == 128;
-        if (kRoles || pass == PrePass::roles) return go.template operator()<K, OUT, false, true>();
-        return go.template operator()<K, OUT, false, kRoles>();
+        if (pass == PrePass::narrow) return go.template operator()<K, OUT, false, true, 1>();
+        if (kRoles || pass == PrePass::roles)
+            return go.template operator()<K, OUT, false, true, 2>();
+        return go.template operator()<K, OUT, false, kRoles, 2>();
     };
     auto with_k = [&]<int K>() {
         // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
-        return pass == PrePass::sums ? go.template operator()<K, 1, true, true>()
+        return pass == PrePass::sums ? go.template operator()<K, 1, true, true, 2>()
                : p.out_dt == 0       ? with_out.template operator()<K, 0>()
                : p.out_dt == 1       ? with_out.template operator()<K, 1>()
                                      : with_out.template operator()<K, 2>();

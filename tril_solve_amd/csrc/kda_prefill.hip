@@ -80,9 +80,10 @@ __global__ __launch_bounds__(4 * K, 2) void kda_prefill_join_kernel(DeltaProblem
         }
 }
 
-// Workgroups per request and head.
+// Workgroups per request and head, wavefronts having CT tiles of 16 columns.
+template <int CT>
 int column_blocks(int V) {
-    constexpr int each = PreShape<false, true>::kCols * kPreCols;
+    constexpr int each = PreShape<false, true, CT>::kWidth;
     return (V + each - 1) / each;
 }
 
@@ -100,7 +101,7 @@ hipError_t launch_pass(const DeltaProblem &p, int in_dt, PrePass pass, hipStream
 // of 16,384 tokens 2,090 -> 680 us, of 512 tokens 74 -> 64 us, 64 walks of
 // 2,048 tokens 271 -> 198 us; but 96 walks of 4,096 tokens 534 -> 555 us.
 int32_t prefill_segments(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t V) {
-    const int64_t walks = num_seqs * H * column_blocks(V);
+    const int64_t walks = num_seqs * H * column_blocks<2>(V);
     const int64_t chunks = total_tokens / kPreC;
     if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 64 || chunks < 16 * num_seqs)
         return 0;
@@ -129,8 +130,11 @@ hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) 
     // least exist): 256 walks of 512 tokens 82 us with roles and 102 without,
     // 320 walks 148 and 139, 1,024 walks 350 and 329 (K = 128, bf16).
     const int64_t parts = p.seg != 0 ? p.segs - p.req.num_seqs : p.req.num_seqs;
-    const int64_t walks = parts * p.H * column_blocks(p.V);
-    return launch_pass(p, in_dt, walks <= 256 ? PrePass::roles : PrePass::whole, stream);
+    const int64_t walks = parts * p.H;
+    const PrePass pass = walks * column_blocks<1>(p.V) <= 256   ? PrePass::narrow
+                         : walks * column_blocks<2>(p.V) <= 256 ? PrePass::roles
+                                                                : PrePass::whole;
+    return launch_pass(p, in_dt, pass, stream);
 }
 
 }  // namespace kda
