@@ -1300,14 +1300,19 @@ hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t st
                            dim3(Shape::kThreads), 0, stream, p);
         return hipGetLastError();
     };
+    // Columns of 16 to a wavefront halve its part of a chunk: while that still
+    // takes at most a workgroup per compute unit (64 walks of 64 tokens 15.8 ->
+    // 12.8 us, 128 walks of 300 tokens 51 -> 44 us), and for up to 64 columns in
+    // all, which 32 to a wavefront would leave to two of four wavefronts (1,024
+    // walks of 512 tokens, K = 128, V = 64, 266 -> 247 us; K = V = 64 195 and 197).
     auto with_out = [&]<int K, int OUT>() {
         // FP32 rows on their way leave a wavefront that does both without
         // registers (spills; 1,024 walks of 512 tokens 420 -> 542 us)
         constexpr bool kRoles = EI::kBytes == 4 && K == 128;
         if (pass == PrePass::narrow) return go.template operator()<K, OUT, false, true, 1>();
-        if (kRoles || pass == PrePass::roles)
-            return go.template operator()<K, OUT, false, true, 2>();
-        return go.template operator()<K, OUT, false, kRoles, 2>();
+        if (pass == PrePass::roles) return go.template operator()<K, OUT, false, true, 2>();
+        return p.V <= 64 ? go.template operator()<K, OUT, false, kRoles, 1>()
+                         : go.template operator()<K, OUT, false, kRoles, 2>();
     };
     auto with_k = [&]<int K>() {
         // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
