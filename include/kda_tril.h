@@ -424,7 +424,7 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  * that run side by side (the results agree to rounding with those of one
  * piece). The size is 0 where that would not pay: for more than 64 (request,
  * head, 128 value columns) triples or 64 requests, or fewer than 512 tokens
- * per request on average. With a smaller one, or none (NULL, 0), each request
+ * per request on average (1,280 with more than 32 triples). With a smaller one, or none (NULL, 0), each request
  * runs in one piece. 16-byte aligned, overlapping no other argument; its
  * contents need not be kept; concurrent calls (and captured graphs that may
  * replay at once) need different ones.

@@ -477,7 +477,7 @@ def test_prefill_cut_lengths(kt, lengths):
                                       (4, 1, 64, 160), (64, 16, 64, 64)])
 @pytest.mark.parametrize("gate", ["channel", "head"])
 def test_prefill_cut_heads(kt, gate, H, Hk, K, V):
-    c = _delta_inputs([700], H, Hk, K, V, "f32", 150 + V, gate=gate)
+    c = _delta_inputs([700 if H <= 32 else 1300], H, Hk, K, V, "f32", 150 + V, gate=gate)
     assert _cut_size(kt, c) > 0
     _delta_check(kt, "prefill", c)
 

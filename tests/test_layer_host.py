@@ -74,6 +74,7 @@ def test_prefill_workspace_query(kt):
     assert size(0, 0, 4, 128, 128) == 0
     # no cut: short prompts, many heads or requests
     assert size(511, 1, 4, 128, 128) == 0 and size(1023, 2, 4, 128, 128) == 0
+    assert size(1279, 1, 64, 128, 128) == 0 and size(1280, 1, 64, 128, 128) > 0
     assert size(65536, 1, 65, 128, 128) == 0 and size(65536, 1, 33, 128, 256) == 0
     assert size(1 << 20, 65, 1, 128, 128) == 0 and size(0, 1, 1, 64, 32) == 0
     # segments of whole chunks: [segments, H, K, V + K] and [requests, H, K, V]

@@ -10,8 +10,8 @@
 // which is the recurrence S <- diag(e^g) S, u = beta (v - S^T k), S += k u^T,
 // o = scale S^T q of 32 tokens at once (the decode step's recurrence).
 //
-// A workgroup per request, value head and 128 value columns walks the request's
-// chunks. Every product runs on the bfloat16 matrix cores with FP32
+// A workgroup per request, value head and 128 (or 64) value columns walks the
+// request's chunks. Every product runs on the bfloat16 matrix cores with FP32
 // accumulators, each FP32 factor taken as a sum of bfloat16 parts
 // (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)):
 //   6 products (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; about 2^-24 of
@@ -24,7 +24,7 @@
 // Against FP32 matrix instructions (16 x 16 x 32 in eight of 32 cycles) that
 // is 6 or 3 of 16 cycles. Sums, the state and the decays stay FP32.
 //
-//   * Each wavefront owns 32 value columns of the state in registers
+//   * Each wavefront owns 32 (or 16) value columns of the state in registers
 //     (accumulator layout). Two accumulator tiles b = 0, 1 are the B operand of
 //     the next product as they stand when its reduction index 8 g + 4 b + s
 //     means row 4 g + s of tile b: tokens 16 b + 4 g + s of U, and, for the
@@ -56,7 +56,7 @@
 // What bounds it: instruction issue and, with all units at work, power (1.6 to
 // 1.8 of 2.4 GHz). A wavefront's chunk is about 250 matrix instructions and
 // 1,090 vector instructions, 16 and 4 cycles each, most of them the splits into
-// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 311 us: 2.8 TB/s
+// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 305 us: 2.9 TB/s
 // of the 5.1 that a copy reaches, 0.8 of 2.5 PFLOP/s of the products as run.
 #pragma once
 

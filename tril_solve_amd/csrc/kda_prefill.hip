@@ -98,12 +98,14 @@ hipError_t launch_pass(const DeltaProblem &p, int in_dt, PrePass pass, hipStream
 // A request's walk over its chunks is serial, so a few (request, head, 128
 // columns) workgroups leave most of the 256 compute units idle; a cut prompt
 // takes the chunks of its segments at once, for about twice the work: 32 walks
-// of 16,384 tokens 2,090 -> 680 us, of 512 tokens 74 -> 64 us, 64 walks of
-// 2,048 tokens 271 -> 198 us; but 96 walks of 4,096 tokens 534 -> 555 us.
+// of 16,384 tokens 1,880 -> 660-780 us, of 768 tokens 89 -> 76 us, 64 walks of
+// 2,048 tokens 224 -> 199 us; but 8 walks of 512 tokens 58 and 58, 64 walks of
+// 1,024 tokens 117 -> 120 us, 96 walks of 4,096 tokens 534 -> 555 us.
 int32_t prefill_segments(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t V) {
     const int64_t walks = num_seqs * H * column_blocks<2>(V);
     const int64_t chunks = total_tokens / kPreC;
-    if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 64 || chunks < 16 * num_seqs)
+    if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 64 ||
+        chunks < (walks > 32 ? 40 : 16) * num_seqs)
         return 0;
     const int64_t parts = 256 * num_seqs / walks;  // a workgroup per compute unit
     int64_t seg = (chunks + parts - 1) / parts;
