@@ -18,11 +18,12 @@
 //     each term) for what the state is summed from, (k e^{G_32 - G})^T U and
 //     the inverse times the right-hand side, and for everything an FP32
 //     output is summed from;
-//   3 products (hi hi, hi mid, mid hi; about 2^-17) where the result enters
-//     only as a correction (L and (k e^G) S: 5e-7 and 1e-7 of the state), and
-//     for what a 16-bit output is summed from.
+//   5 (without lo hi; 2^-19) for L, and for (k e^G) S beside an FP32 output;
+//   3 (hi hi, hi mid, mid hi; about 2^-17) for (k e^G) S else, a correction
+//     that costs the state 1e-7, and for what a 16-bit output is summed from.
+// (State against 64 bits: 3e-7 to 8e-7; with 3 products for L 5e-7 to 1.2e-6.)
 // Against FP32 matrix instructions (16 x 16 x 32 in eight of 32 cycles) that
-// is 6 or 3 of 16 cycles. Sums, the state and the decays stay FP32.
+// is 3 to 6 of 16 cycles. Sums, the state and the decays stay FP32.
 //
 //   * Each wavefront owns 32 (or 16) value columns of the state in registers
 //     (accumulator layout). Two accumulator tiles b = 0, 1 are the B operand of
@@ -45,6 +46,9 @@
 //     running products of the decays instead, every factor of which is the
 //     decay between two tokens, and takes the left-hand forms above. The factor
 //     e^{G_32 - m} is left owing and taken together with the next chunk's e^m.
+//     Sums of decays past 2^8 over 16 tokens are formed in fixed point: in FP32
+//     they keep 2^-17 of a power of two at 2^-74, which neighbours far from the
+//     middle lose between them (state 1.6e-6 off, then 4e-7).
 //
 // Two forms. With many workgroups, four wavefronts prepare a chunk and then
 // walk their columns through it, two workgroups to a compute unit (74 KB of
@@ -70,6 +74,8 @@ constexpr int kPreC = 32;  // tokens per chunk
 constexpr int kPreWaves = 4;  // that prepare a chunk
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kSteep = 64.0f * kLog2E;  // in powers of two
+constexpr float kFine = 8.0f;             // likewise
+constexpr float kFixed = 16777216.0f;     // units of 2^-24 of a power of two
 
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
@@ -137,7 +143,8 @@ __device__ __forceinline__ f4 mfma(w2 a, w2 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a),
                                                      __builtin_bit_cast(s4, b), c, 0, 0, 0);
 }
-// c + a b in M = 3 or 6 products, the smallest first; several such sums are
+// c + a b in M = 3, 5 or 6 products, the smallest first (5: b in three parts, a
+// in two); several such sums are
 // formed product by product, since a product that waits for the one before it
 // takes 21 cycles instead of 16. part_a, part_b: the parts of product i.
 constexpr int part_a(int M, int i) {
@@ -249,6 +256,26 @@ struct RawC<F32, 2> {
 __device__ __forceinline__ f4 exp2(f4 x) {
     return f4{__builtin_amdgcn_exp2f(x[0]), __builtin_amdgcn_exp2f(x[1]),
               __builtin_amdgcn_exp2f(x[2]), __builtin_amdgcn_exp2f(x[3])};
+}
+// Powers of two in units of 2^-24, as integers: sums of them are exact.
+typedef int i4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i4 fixed(f4 x, float unit) {
+    return i4{(int)__builtin_rintf(x[0] * unit), (int)__builtin_rintf(x[1] * unit),
+              (int)__builtin_rintf(x[2] * unit), (int)__builtin_rintf(x[3] * unit)};
+}
+// 2^(x 2^-24) for |x| < 125 2^24: 2^(1 + fraction), its exponent moved by the
+// integer part less one.
+__device__ __forceinline__ f4 exp2(i4 x) {
+    f4 e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int s = x[i] >> 1;
+        const float y = __builtin_amdgcn_exp2f(
+            __builtin_bit_cast(float, (s & 0x7FFFFF) | 0x3F800000));
+        e[i] = __builtin_bit_cast(float, __builtin_bit_cast(int, y) + (s & (int)0xFF800000) -
+                                             0x800000);
+    }
+    return e;
 }
 __device__ __forceinline__ f4 rcp(f4 x) {
     return f4{__builtin_amdgcn_rcpf(x[0]), __builtin_amdgcn_rcpf(x[1]),
@@ -509,6 +536,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     constexpr int GRP = 4 * kWave / K, TPL = 8 / GRP;
     constexpr int NQ = L::NQ;
     constexpr int MQ = OUT == 0 ? 6 : 3;  // products for P, P U and (q e^G) S
+    constexpr int MK = OUT == 0 ? 5 : 3;  // for (k e^G) S
     constexpr int OE = OUT == 0 ? 4 : 2;  // bytes of an output element
     __shared__ __align__(16) char lds[L::kBytes];
 
@@ -646,6 +674,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     // the decay (of this lane's channels, a power of two) that the state in
     // registers still has to take: G_32 - m of the chunk before
     f4 owed = {0.0f, 0.0f, 0.0f, 0.0f};
+    i4 owed_i = {0, 0, 0, 0};  // (in fixed point; the first wavefront's)
     // a barrier of the preparing wavefronts
     int *count = reinterpret_cast<int *>(lds + L::FLAGS) + 2, met = 0;
     auto meet_all = [&] {
@@ -695,50 +724,86 @@ void kda_prefill_kernel(DeltaProblem p) {
             wt[w] = *reinterpret_cast<const f4 *>(tots + w * K + ch);
         const f4 first = wt[0] + wt[1], second = wt[2] + wt[3];  // m, G_32 - m
         const f4 both = owed + first;
-        bool steep = false, deep = false;  // (steep: NaN or infinite where any gate is)
+        bool steep = false, deep = false, wide = false;  // (steep: also where not finite)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             steep |= !(__builtin_fabsf(first[e]) <= kSteep) |
                      !(__builtin_fabsf(second[e]) <= kSteep);
-            deep |= __builtin_fabsf(both[e]) > 125.0f;
+            deep |= __builtin_fabsf(both[e]) > 124.0f;
+            wide |= !(__builtin_fabsf(first[e]) <= kFine) | !(__builtin_fabsf(second[e]) <= kFine);
         }
         far = __ballot(steep) != 0;  // the same in every wavefront
         apart = far | (__ballot(deep) != 0);
-        if (pw == 0 && grp == 0) {
-            const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
-            *reinterpret_cast<f4 *>(fac + L::EM + 4 * ch) =
-                far ? one : exp2(apart ? first : both);
-            *reinterpret_cast<f4 *>(fac + L::EG + 4 * ch) = exp2(owed);
-            *reinterpret_cast<f4 *>(fac + L::EF + 4 * ch) = exp2(first + second);
-        }
-        if (ROLES && pw == 0 && lane0 == 0)
-            reinterpret_cast<int *>(lds + L::FLAGS)[buf] = (far ? 1 : 0) | (apart ? 2 : 0);
-        owed = far ? f4{0.0f, 0.0f, 0.0f, 0.0f} : second;
-        if (!far) {
-            // from the chunk's middle to this lane's first token
-            f4 mid = {0.0f, 0.0f, 0.0f, 0.0f};
+        // m and G_32 - m in fixed point (the first wavefront's)
+        i4 first_i = {0, 0, 0, 0}, second_i = first_i;
+        // the factor of token i of this lane's: keys, queries and their inverse
+        auto put_token = [&](int i, f4 e) {
+            const f4 k = now.k[i].all();
+            put_row.template operator()<2>(L::KR, tok + i, k * e);
+            if constexpr (!SUM)
+                put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
+            put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
+        };
+        // from the chunk's middle to this lane's first token, of the wavefronts'
+        // totals and this one's groups
+        auto from_middle = [&](const auto &w, const auto &own) {
+            auto mid = w[0] - w[0];
             if (pw >= 2) {
-                if (pw == 3) mid = wt[2];
+                if (pw == 3) mid = w[2];
 #pragma unroll
                 for (int g = 0; g + 1 < GRP; ++g)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mid[e] += g < grp ? sums[g][e] : 0.0f;
+                    for (int e = 0; e < 4; ++e)
+                        if (g < grp) mid[e] += own[g][e];
             } else {
-                mid = -sums[GRP - 1];
-                if (pw == 0) mid -= wt[1];
+                mid = -own[GRP - 1];
+                if (pw == 0) mid -= w[1];
 #pragma unroll
                 for (int g = 0; g + 1 < GRP; ++g)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mid[e] -= g >= grp ? sums[g][e] : 0.0f;
+                    for (int e = 0; e < 4; ++e)
+                        if (g >= grp) mid[e] -= own[g][e];
             }
+            return mid;
+        };
+        if (!far && __ballot(wide) == 0) {
+            if (pw == 0) {
+                first_i = fixed(first, kFixed);
+                second_i = fixed(second, kFixed);
+            }
+            const f4 mid = from_middle(wt, sums);
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) put_token(i, exp2(er[i] + mid));
+        } else if (!far) {
+            // Far from the middle the FP32 sums of steep decays keep too few bits
+            // of a power of two (2^-17 of 2^74), and adjacent tokens would lose
+            // them: the sums once more in fixed point, where they are exact.
+            i4 x = {0, 0, 0, 0}, ei[TPL], own[GRP], wi[kPreWaves];
 #pragma unroll
             for (int i = 0; i < TPL; ++i) {
-                const f4 e = exp2(er[i] + mid), k = now.k[i].all();
-                put_row.template operator()<2>(L::KR, tok + i, k * e);
-                if constexpr (!SUM)
-                    put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
-                put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
+                x += fixed(now.g[i], kLog2E * kFixed);
+                ei[i] = x;
             }
+            f4 parts[GRP];
+            gather_groups<GRP>(__builtin_bit_cast(f4, x), parts);
+            i4 all = {0, 0, 0, 0};
+#pragma unroll
+            for (int g = 0; g < GRP; ++g) {
+                own[g] = __builtin_bit_cast(i4, parts[g]);
+                all += own[g];
+            }
+            // (the inverse's place: written after the next barrier)
+            int *totals = reinterpret_cast<int *>(op + L::TM);
+            if (grp == 0) *reinterpret_cast<i4 *>(totals + pw * K + ch) = all;
+            meet_all();
+#pragma unroll
+            for (int w = 0; w < kPreWaves; ++w)
+                wi[w] = *reinterpret_cast<const i4 *>(totals + w * K + ch);
+            first_i = wi[0] + wi[1];
+            second_i = wi[2] + wi[3];
+            const i4 mid = from_middle(wi, own);
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) put_token(i, exp2(ei[i] + mid));
         } else {
 #pragma unroll
             for (int i = 0; i < TPL; ++i) {
@@ -749,6 +814,17 @@ void kda_prefill_kernel(DeltaProblem p) {
                 *reinterpret_cast<f4 *>(op + L::SA + at) = exp2(now.g[i] * kLog2E);
             }
         }
+        if (pw == 0 && grp == 0) {
+            const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
+            *reinterpret_cast<f4 *>(fac + L::EM + 4 * ch) =
+                far ? one : exp2(apart ? first_i : owed_i + first_i);
+            *reinterpret_cast<f4 *>(fac + L::EG + 4 * ch) = exp2(owed_i);
+            *reinterpret_cast<f4 *>(fac + L::EF + 4 * ch) = exp2(first + second);
+        }
+        if (ROLES && pw == 0 && lane0 == 0)
+            reinterpret_cast<int *>(lds + L::FLAGS)[buf] = (far ? 1 : 0) | (apart ? 2 : 0);
+        owed = far ? f4{0.0f, 0.0f, 0.0f, 0.0f} : second;
+        owed_i = far ? i4{0, 0, 0, 0} : second_i;
         meet_all();
 
         const int rpos = n16 * L::RS + ((g4 << 4) ^ L::swz_row(n16));
@@ -767,11 +843,13 @@ void kda_prefill_kernel(DeltaProblem p) {
         if (!far) {
             // rows 16 bi .. of `left` against rows 16 bj .. of the keys
             auto block = [&]<int M, int N>(int left, int bi, int bj) -> f4 {
-                Operand<N> l[K / 32], r[K / 32];
+                constexpr int NR = M == 5 ? 3 : N;
+                Operand<N> l[K / 32];
+                Operand<NR> r[K / 32];
 #pragma unroll
                 for (int kk = 0; kk < K / 32; ++kk) {
                     l[kk] = row_operand.template operator()<N>(left + 16 * bi * L::RS, kk);
-                    r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
+                    r[kk] = row_operand.template operator()<NR>(L::KL + 16 * bj * L::RS, kk);
                 }
                 f4 c[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
@@ -784,9 +862,9 @@ void kda_prefill_kernel(DeltaProblem p) {
                 return c[0] + c[1];
             };
             if (pw < 2) {
-                m[0] = block.template operator()<3, 2>(L::KR, pw, pw);
+                m[0] = block.template operator()<5, 2>(L::KR, pw, pw);
             } else if (pw == 3) {
-                m[0] = block.template operator()<3, 2>(L::KR, 1, 0);
+                m[0] = block.template operator()<5, 2>(L::KR, 1, 0);
                 if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
             } else if constexpr (!SUM) {
                 m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
@@ -1097,14 +1175,14 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         const auto &bc = b[kk & 1][ct];
-                        if (i < 3)
+                        if (i < MK)
                             kS[I][ct] =
-                                mfma(ka_op[I].p[part_a(3, i)], bc.p[part_b(3, i)], kS[I][ct]);
+                                mfma(ka_op[I].p[part_a(MK, i)], bc.p[part_b(MK, i)], kS[I][ct]);
                         o[I][ct] = mfma(qa_op[I].p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
                     }
             }
             __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 2 : 2 + NQ, 0);  // LDS reads
-            interleave<SUM ? 3 * CT : (3 + MQ) * CT, SUM ? 5 : 3>();
+            interleave<SUM ? 3 * CT : (MK + MQ) * CT, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time, X the inverse's diagonal blocks times beta:
@@ -1228,7 +1306,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             if (len_all > 0) {
                 // what the last chunk owes (nothing reads the totals now)
                 if (pw == 0 && lane0 < K / 4)
-                    *reinterpret_cast<f4 *>(lds + L::TOT + 16 * lane0) = exp2(owed);
+                    *reinterpret_cast<f4 *>(lds + L::TOT + 16 * lane0) = exp2(owed_i);
                 __syncthreads();
             }
             return;
@@ -1264,7 +1342,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         }
         if (len_all > 0) {
             if (pw == 0 && lane0 < K / 4)
-                *reinterpret_cast<f4 *>(lds + L::TOT + 16 * lane0) = exp2(owed);
+                *reinterpret_cast<f4 *>(lds + L::TOT + 16 * lane0) = exp2(owed_i);
             __syncthreads();
         }
     }
@@ -1306,9 +1384,10 @@ hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t st
     // all, which 32 to a wavefront would leave to two of four wavefronts (1,024
     // walks of 512 tokens, K = 128, V = 64, 266 -> 247 us; K = V = 64 195 and 197).
     auto with_out = [&]<int K, int OUT>() {
-        // FP32 rows on their way leave a wavefront that does both without
-        // registers (spills; 1,024 walks of 512 tokens 420 -> 542 us)
-        constexpr bool kRoles = EI::kBytes == 4 && K == 128;
+        // FP32 rows on their way, or a third part of queries, P and S', leave a
+        // wavefront that does both without registers (it spills; FP32 in and
+        // out, 1,024 walks of 512 tokens 420 -> 542 us)
+        constexpr bool kRoles = K == 128 && (EI::kBytes == 4 || OUT == 0);
         if (pass == PrePass::narrow) return go.template operator()<K, OUT, false, true, 1>();
         if (pass == PrePass::roles) return go.template operator()<K, OUT, false, true, 2>();
         return p.V <= 64 ? go.template operator()<K, OUT, false, kRoles, 1>()
