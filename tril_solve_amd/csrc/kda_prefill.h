@@ -15,13 +15,15 @@
 // accumulators, each FP32 factor taken as a sum of bfloat16 parts
 // (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)):
 //   6 products (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; about 2^-24 of
-//     each term) for what the state is summed from, (k e^{G_32 - G})^T U and
-//     the inverse times the right-hand side, and for everything an FP32
-//     output is summed from;
-//   5 (without lo hi; 2^-19) for L, and for (k e^G) S beside an FP32 output;
-//   3 (hi hi, hi mid, mid hi; about 2^-17) for (k e^G) S else, a correction
-//     that costs the state 1e-7, and for what a 16-bit output is summed from.
-// (State against 64 bits: 3e-7 to 8e-7; with 3 products for L 5e-7 to 1.2e-6.)
+//     each term) for all that the state is summed from and all that an FP32
+//     output is summed from (with K = 128 and an FP32 output, whose operands
+//     leave no room for a third part of k e^{G - m}, L and (k e^G) S in 5,
+//     without lo hi; 2^-19);
+//   3 (hi hi, hi mid, mid hi; about 2^-17) for what a 16-bit output is summed
+//     from.
+// (State against 64 bits: 2e-7 to 5e-7. L and (k e^G) S in 3 products, too, took
+// 309 instead of 390 us on 16 x 512 tokens, but where decays are slow, the state
+// large against what a chunk adds, that cost it up to 2e-6.)
 // Against FP32 matrix instructions (16 x 16 x 32 in eight of 32 cycles) that
 // is 3 to 6 of 16 cycles. Sums, the state and the decays stay FP32.
 //
@@ -314,11 +316,13 @@ struct PreLds {
     static constexpr int RS = 2 * K, TS = 2 * kPreC;
     static constexpr int kPatch = 20;  // floats between rows of a block of L
     static constexpr int R32 = kPreC * RS;
-    static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of queries, P and S'
+    static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of queries and P
+    // parts of the keys times e^{G - m} (a third would not fit with NQ = 3)
+    static constexpr int NK = K == 128 && OUT == 0 ? 2 : 3;
     // N chunks' operands, each:
     // keys and queries times e^{G - m} (steep: e^G), keys times e^{m - G}
     // (steep: e^{G_32 - G})
-    static constexpr int KR = 0, QR = KR + 2 * R32, KL = QR + NQ * R32;
+    static constexpr int KR = 0, QR = KR + NK * R32, KL = QR + NQ * R32;
     static constexpr int kOperands = KL + 3 * R32;
     // a steep chunk's first half: keys, queries, decays FP32, then L / beta and P
     static constexpr int SK = 0, SQ = SK + kPreC * K * 4, SA = SQ + kPreC * K * 4;
@@ -536,7 +540,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     constexpr int GRP = 4 * kWave / K, TPL = 8 / GRP;
     constexpr int NQ = L::NQ;
     constexpr int MQ = OUT == 0 ? 6 : 3;  // products for P, P U and (q e^G) S
-    constexpr int MK = OUT == 0 ? 5 : 3;  // for (k e^G) S
+    constexpr int NK = L::NK, MK = NK == 3 ? 6 : 5;  // for L and (k e^G) S
     constexpr int OE = OUT == 0 ? 4 : 2;  // bytes of an output element
     __shared__ __align__(16) char lds[L::kBytes];
 
@@ -739,7 +743,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         // the factor of token i of this lane's: keys, queries and their inverse
         auto put_token = [&](int i, f4 e) {
             const f4 k = now.k[i].all();
-            put_row.template operator()<2>(L::KR, tok + i, k * e);
+            put_row.template operator()<NK>(L::KR, tok + i, k * e);
             if constexpr (!SUM)
                 put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
             put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
@@ -862,9 +866,9 @@ void kda_prefill_kernel(DeltaProblem p) {
                 return c[0] + c[1];
             };
             if (pw < 2) {
-                m[0] = block.template operator()<5, 2>(L::KR, pw, pw);
+                m[0] = block.template operator()<MK, NK>(L::KR, pw, pw);
             } else if (pw == 3) {
-                m[0] = block.template operator()<5, 2>(L::KR, 1, 0);
+                m[0] = block.template operator()<MK, NK>(L::KR, 1, 0);
                 if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
             } else if constexpr (!SUM) {
                 m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
@@ -1006,7 +1010,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int i = 0; i < TPL; ++i) {
                 before += g2[i];
                 const f4 e = exp2(before);
-                put_row.template operator()<2>(L::KR, tok + i, now.k[i].all() * e);
+                put_row.template operator()<NK>(L::KR, tok + i, now.k[i].all() * e);
                 if constexpr (!SUM)
                     put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
             }
@@ -1126,12 +1130,13 @@ void kda_prefill_kernel(DeltaProblem p) {
         f4 kS[2][CT], o[2][CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) kS[0][ct] = kS[1][ct] = o[0][ct] = o[1][ct] = z;
-        Operand<2> ka_op[2];
-        Operand<NQ> qa_op[2], b[2][CT];
+        Operand<NK> ka_op[2];
+        Operand<NQ> qa_op[2];
+        Operand<3> b[2][CT];
         f4 em[2];
         auto read_rows = [&](int j) {  // k-step j / 2, row tile j % 2
             const int at = 16 * (j & 1) * L::RS;
-            ka_op[j & 1] = row_operand.template operator()<2>(L::KR + at, j >> 1);
+            ka_op[j & 1] = row_operand.template operator()<NK>(L::KR + at, j >> 1);
             if constexpr (!SUM)
                 qa_op[j & 1] = row_operand.template operator()<NQ>(L::QR + at, j >> 1);
         };
@@ -1144,7 +1149,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         auto split_state = [&](int kk, int ct) {  // S' (also of a steep chunk, where it is S)
 #pragma unroll
             for (int t = 0; t < 2; ++t) S[2 * kk + t][ct] *= em[t];
-            b[kk & 1][ct] = join(split4<NQ>(S[2 * kk][ct]), split4<NQ>(S[2 * kk + 1][ct]));
+            b[kk & 1][ct] = join(split4<3>(S[2 * kk][ct]), split4<3>(S[2 * kk + 1][ct]));
         };
         if (apart) {
 #pragma unroll
@@ -1168,21 +1173,23 @@ void kda_prefill_kernel(DeltaProblem p) {
             if (kk + 1 < K / 32 && I < CT) split_state(kk + 1, I);
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
             if constexpr (SUM) {
-                mul_columns<3, CT>(ka_op[I], b[kk & 1], kS[I]);
+                mul_columns<MK, CT>(ka_op[I], b[kk & 1], kS[I]);
             } else {
 #pragma unroll
-                for (int i = 0; i < MQ; ++i)
+                for (int i = 0; i < 6; ++i)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         const auto &bc = b[kk & 1][ct];
                         if (i < MK)
                             kS[I][ct] =
                                 mfma(ka_op[I].p[part_a(MK, i)], bc.p[part_b(MK, i)], kS[I][ct]);
-                        o[I][ct] = mfma(qa_op[I].p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
+                        if (i < MQ)
+                            o[I][ct] =
+                                mfma(qa_op[I].p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
                     }
             }
-            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 2 : 2 + NQ, 0);  // LDS reads
-            interleave<SUM ? 3 * CT : (MK + MQ) * CT, SUM ? 5 : 3>();
+            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? NK : NK + NQ, 0);  // LDS reads
+            interleave<SUM ? MK * CT : (MK + MQ) * CT, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time, X the inverse's diagonal blocks times beta:
