@@ -1162,6 +1162,10 @@ void kda_prefill_kernel(DeltaProblem p) {
                 for (int ct = 0; ct < CT; ++ct) S[rt][ct] *= e;
             }
         }
+        // (no room for the next operands beside 32 columns and the preparation's
+        // registers, 16 x 512 tokens 400 -> 383 us, or with three wavefronts to a
+        // SIMD)
+        constexpr bool kNext = K == 64 || (!SUM && (ROLES || CT == 1));
         read_em(0);
         read_rows(0);
 #pragma unroll
@@ -1171,7 +1175,8 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
         for (int j = 0; j < K / 16; ++j) {
             const int kk = j >> 1, I = j & 1;
-            if (j + 1 < K / 16) read_rows(j + 1);
+            if (kNext && j + 1 < K / 16) read_rows(j + 1);
+            if (!kNext && j > 0) read_rows(j);
             if (kk + 1 < K / 32 && I < CT) split_state(kk + 1, I);
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
             if constexpr (SUM) {
