@@ -22,7 +22,7 @@
 //   3 (hi hi, hi mid, mid hi; about 2^-17) for what a 16-bit output is summed
 //     from.
 // (State against 64 bits: 2e-7 to 5e-7. L and (k e^G) S in 3 products, too, took
-// 305 instead of 376 us on 16 x 512 tokens, but where decays are slow, the state
+// 305 instead of 354 us on 16 x 512 tokens, but where decays are slow, the state
 // large against what a chunk adds, that cost it up to 2e-6.)
 // Against FP32 matrix instructions (16 x 16 x 32 in eight of 32 cycles) that
 // is 3 to 6 of 16 cycles. Sums, the state and the decays stay FP32.
@@ -62,8 +62,8 @@
 // What bounds it: instruction issue and, with all units at work, power (1.6 to
 // 1.8 of 2.4 GHz). A wavefront's chunk is about 300 matrix instructions and
 // 1,400 vector instructions, 16 and 4 cycles each, most of them the splits into
-// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 376 us: 2.3 TB/s
-// of the 5.1 that a copy reaches, 0.8 of 2.5 PFLOP/s of the products as run.
+// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 354 us: 2.5 TB/s
+// of the 5.1 that a copy reaches, 0.9 of 2.5 PFLOP/s of the products as run.
 // (Figures at rules and forms were taken with three products for L and
 // (k e^G) S; both sides have grown since.)
 #pragma once
