@@ -592,6 +592,26 @@ def test_prefill_cut_streams_and_graphs(kt):
         _delta_run(kt, "prefill", c)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("K", [64, 128])
+def test_prefill_state_of_slow_and_steep_heads(kt, K, dtype):
+    """One decay per head from 0.004 to 3.5 nats a token: a state that is large
+    against what a chunk adds, and exponents of many powers of two. Each head's
+    state to 2e-6 of its norm: products of parts kept to 2^-19 of a term (K =
+    128 with an FP32 output; else 2^-24) leave 1e-6 of a slow head's state."""
+    rates = np.array([0.004, 0.02, 0.1, 0.4, 1.0, 2.0, 3.5])
+    for lengths in ([256], [640]):  # whole, and cut into segments
+        c = _delta_inputs(lengths, 7, 7, K, 64, dtype, 180 + K, gate="head")
+        rng = np.random.default_rng(181)
+        c["g"] = (-rates * np.logaddexp(0.0, rng.standard_normal(c["g"].shape))).astype(np.float32)
+        _, S = _delta_run(kt, "prefill", c, slot=None, init=None)
+        _, want, _ = ref.delta_rule(c["q64"], c["k64"], c["v64"], c["g"], c["beta"], lengths,
+                                    c["state"], None, None, K ** -0.5)
+        off = S.cpu().numpy().astype(np.float64)[0] - want[0]
+        for h in range(7):
+            assert np.linalg.norm(off[h]) <= 2e-6 * np.linalg.norm(want[0, h]), (lengths, h)
+
+
 @pytest.mark.parametrize("requests,H", [(1, 257), (3, 100), (200, 2)])
 def test_prefill_many_workgroups(kt, requests, H):
     """More workgroups than compute units: wavefronts that prepare and walk."""
