@@ -21,7 +21,8 @@
 //     without lo hi; 2^-19);
 //   3 (hi hi, hi mid, mid hi; about 2^-17) for what a 16-bit output is summed
 //     from.
-// (State against 64 bits: 2e-7 to 5e-7. L and (k e^G) S in 3 products, too, took
+// (State against 64 bits: 1e-7 to 4e-7. The correction L_10 U_0 in 3 products,
+// too, cost it up to 7e-6 where keys have a common direction. L and (k e^G) S in 3 products, too, took
 // 305 instead of 354 us on 16 x 512 tokens, but where decays are slow, the state
 // large against what a chunk adds, that cost it up to 2e-6.)
 // Against FP32 matrix instructions (16 x 16 x 32 in eight of 32 cycles) that
@@ -969,7 +970,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         } else {
 #pragma unroll
             for (int s = 0; s < 4; s += 2) {
-                put_pair.template operator()<2>(L::TM, true, 4 * g4 + s, n16, -m[0][s],
+                put_pair.template operator()<3>(L::TM, true, 4 * g4 + s, n16, -m[0][s],
                                                 -m[0][s + 1]);
                 if constexpr (!SUM)
                     put_pair.template operator()<NQ>(L::PM, true, 4 * g4 + s, n16, m[1][s],
@@ -1225,7 +1226,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             mul_columns<6, CT>(x0, r, x);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) h0[ct] = split4<3>(x[ct]);
-            mul_columns<3, CT>(half_of(x1, 0), h0, R[1]);
+            mul_columns<6, CT>(half_of(x1, 0), h0, R[1]);
             if constexpr (!SUM) mul_columns<MQ, CT>(p0, h0, o[0]);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
