@@ -416,9 +416,8 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  * KDA_ERR_UNSUPPORTED. State, decays and sums are FP32. The chunked form's
  * products take each FP32 factor as two or three bfloat16 parts: what the
  * state and an FP32 output are summed from is kept to about 2^-24 of each
- * term (2^-19 in two corrections with K = 128 and an FP32 output), what a
- * 16-bit output is summed from to about 2^-17 (state within 1e-6 of exact
- * arithmetic).
+ * term (within 1e-6 of the norm of exact arithmetic's, 512 tokens), what a
+ * 16-bit output is summed from to about 2^-17.
  *
  * workspace: with one of at least kda_prefill_workspace_size bytes,
  * kda_prefill_* cuts long prompts on few heads into segments of whole chunks

@@ -101,3 +101,17 @@ def test_state_of_alike_keys(kt, K, dtype, out_dtype, keys, rate):
     for cut in (False, True):
         _, S = _run(kt, c, out_dtype, cut)
         assert _off(S, want) <= STATE, (cut, _off(S, want))
+
+
+@pytest.mark.parametrize("keys,rate", [("isotropic", 0.004), ("silu", 0.05),
+                                       ("channel means", 0.004), ("common", "mixed")])
+@pytest.mark.parametrize("K,dtype", [(128, "f32"), (128, "bf16"), (64, "f32"), (64, "f16")])
+def test_fp32_outputs_of_alike_keys(kt, K, dtype, keys, rate):
+    """An FP32 output is summed from the state and from the chunk's U in the
+    same products: state and output to the same share of their norms."""
+    c = _inputs([512], 2, K, 128, dtype, keys, rate, 210 + K)
+    want_out, want, _ = _exact(c)
+    for cut in (False, True):
+        out, S = _run(kt, c, "f32", cut)
+        assert _off(S, want) <= STATE, (cut, _off(S, want))
+        assert _off(out, want_out) <= STATE, (cut, _off(out, want_out))

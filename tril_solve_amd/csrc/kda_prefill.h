@@ -16,9 +16,7 @@
 // (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)):
 //   6 products (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; about 2^-24 of
 //     each term) for all that the state is summed from and all that an FP32
-//     output is summed from (with K = 128 and an FP32 output, whose operands
-//     leave no room for a third part of k e^{G - m}, L and (k e^G) S in 5,
-//     without lo hi; 2^-19);
+//     output is summed from;
 //   3 (hi hi, hi mid, mid hi; about 2^-17) for what a 16-bit output is summed
 //     from.
 // (State against 64 bits: 1e-7 to 4e-7. The correction L_10 U_0 in 3 products,
@@ -148,8 +146,7 @@ __device__ __forceinline__ f4 mfma(w2 a, w2 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a),
                                                      __builtin_bit_cast(s4, b), c, 0, 0, 0);
 }
-// c + a b in M = 3, 5 or 6 products, the smallest first (5: b in three parts, a
-// in two); several such sums are
+// c + a b in M = 3 or 6 products, the smallest first; several such sums are
 // formed product by product, since a product that waits for the one before it
 // takes 21 cycles instead of 16. part_a, part_b: the parts of product i.
 constexpr int part_a(int M, int i) {
@@ -320,12 +317,15 @@ struct PreLds {
     static constexpr int kPatch = 20;  // floats between rows of a block of L
     static constexpr int R32 = kPreC * RS;
     static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of queries and P
-    // parts of the keys times e^{G - m} (a third would not fit with NQ = 3)
-    static constexpr int NK = K == 128 && OUT == 0 ? 2 : 3;
+    // Three parts of the queries do not fit beside those of the keys with K =
+    // 128: they lie there in FP32, in the room of two parts, and are split by
+    // the wavefronts that read them (8 x 512 tokens, 64 heads, f32: 267 us; 240
+    // with the keys in two parts instead, which left 1e-6 of the state).
+    static constexpr bool kSplitLate = K == 128 && NQ == 3;
     // N chunks' operands, each:
     // keys and queries times e^{G - m} (steep: e^G), keys times e^{m - G}
     // (steep: e^{G_32 - G})
-    static constexpr int KR = 0, QR = KR + NK * R32, KL = QR + NQ * R32;
+    static constexpr int KR = 0, QR = KR + 3 * R32, KL = QR + (kSplitLate ? 2 : NQ) * R32;
     static constexpr int kOperands = KL + 3 * R32;
     // a steep chunk's first half: keys, queries, decays FP32, then L / beta and P
     static constexpr int SK = 0, SQ = SK + kPreC * K * 4, SA = SQ + kPreC * K * 4;
@@ -357,6 +357,16 @@ struct PreLds {
         return (high * 4 + low) << 4;
     }
     static __device__ __forceinline__ int swz_tok(int row) { return ((row >> 2) & 3) << 4; }
+    // 16 rows of an operand reduced over channels as loaded: the parts of the
+    // queries, or the two halves of this lane's eight FP32 queries.
+    typedef Operand<kSplitLate ? 2 : NQ> RawQueries;
+    static __device__ __forceinline__ Operand<NQ> queries(const RawQueries &r) {
+        if constexpr (kSplitLate)
+            return join(split4<3>(__builtin_bit_cast(f4, r.p[0])),
+                        split4<3>(__builtin_bit_cast(f4, r.p[1])));
+        else
+            return r;
+    }
 };
 
 // x = (I + L)^-1, one lane per column of a 16 x 16 block in every 16-lane row:
@@ -543,7 +553,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     constexpr int GRP = 4 * kWave / K, TPL = 8 / GRP;
     constexpr int NQ = L::NQ;
     constexpr int MQ = OUT == 0 ? 6 : 3;  // products for P, P U and (q e^G) S
-    constexpr int NK = L::NK, MK = NK == 3 ? 6 : 5;  // for L and (k e^G) S
+    constexpr int kRawQ = L::kSplitLate ? 2 : NQ;  // pieces of a queries' operand in LDS
     constexpr int OE = OUT == 0 ? 4 : 2;  // bytes of an output element
     __shared__ __align__(16) char lds[L::kBytes];
 
@@ -709,6 +719,13 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
             for (int i = 0; i < N; ++i) *reinterpret_cast<w2 *>(d + i * L::R32) = hx.p[i];
         };
+        auto put_query = [&](int row, f4 x) {
+            if constexpr (L::kSplitLate)  // channels 8 i + 4 e .. + 3 to the half e
+                *reinterpret_cast<f4 *>(op + L::QR + (ch >> 2 & 1) * L::R32 + row * L::RS +
+                                        ((2 * (ch & ~7)) ^ L::swz_row(row))) = x;
+            else
+                put_row.template operator()<NQ>(L::QR, row, x);
+        };
         // entries (row, c) and (row + 1, c), row even, of an operand reduced
         // over tokens; low: rows 16..31
         auto put_pair = [&]<int N>(int at, bool low, int row, int c, float x, float y) {
@@ -746,9 +763,8 @@ void kda_prefill_kernel(DeltaProblem p) {
         // the factor of token i of this lane's: keys, queries and their inverse
         auto put_token = [&](int i, f4 e) {
             const f4 k = now.k[i].all();
-            put_row.template operator()<NK>(L::KR, tok + i, k * e);
-            if constexpr (!SUM)
-                put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
+            put_row.template operator()<3>(L::KR, tok + i, k * e);
+            if constexpr (!SUM) put_query(tok + i, now.q[i].all() * (e * p.scale));
             put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
         };
         // from the chunk's middle to this lane's first token, of the wavefronts'
@@ -848,15 +864,17 @@ void kda_prefill_kernel(DeltaProblem p) {
         // blocks below
         f4 m[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
         if (!far) {
-            // rows 16 bi .. of `left` against rows 16 bj .. of the keys
-            auto block = [&]<int M, int N>(int left, int bi, int bj) -> f4 {
-                constexpr int NR = M == 5 ? 3 : N;
-                Operand<N> l[K / 32];
-                Operand<NR> r[K / 32];
+            // rows 16 bi .. of the keys or queries against rows 16 bj .. of the keys
+            auto block = [&]<int M, int N, bool Q>(int bi, int bj) -> f4 {
+                Operand<N> l[K / 32], r[K / 32];
 #pragma unroll
                 for (int kk = 0; kk < K / 32; ++kk) {
-                    l[kk] = row_operand.template operator()<N>(left + 16 * bi * L::RS, kk);
-                    r[kk] = row_operand.template operator()<NR>(L::KL + 16 * bj * L::RS, kk);
+                    if constexpr (Q)
+                        l[kk] = L::queries(row_operand.template operator()<kRawQ>(
+                            L::QR + 16 * bi * L::RS, kk));
+                    else
+                        l[kk] = row_operand.template operator()<N>(L::KR + 16 * bi * L::RS, kk);
+                    r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
                 }
                 f4 c[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
@@ -869,13 +887,13 @@ void kda_prefill_kernel(DeltaProblem p) {
                 return c[0] + c[1];
             };
             if (pw < 2) {
-                m[0] = block.template operator()<MK, NK>(L::KR, pw, pw);
+                m[0] = block.template operator()<6, 3, false>(pw, pw);
             } else if (pw == 3) {
-                m[0] = block.template operator()<MK, NK>(L::KR, 1, 0);
-                if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 0);
+                m[0] = block.template operator()<6, 3, false>(1, 0);
+                if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ, true>(1, 0);
             } else if constexpr (!SUM) {
-                m[0] = block.template operator()<MQ, NQ>(L::QR, 0, 0);
-                m[1] = block.template operator()<MQ, NQ>(L::QR, 1, 1);
+                m[0] = block.template operator()<MQ, NQ, true>(0, 0);
+                m[1] = block.template operator()<MQ, NQ, true>(1, 1);
             }
         } else {
             // running products of the decays from token j on
@@ -1013,9 +1031,8 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int i = 0; i < TPL; ++i) {
                 before += g2[i];
                 const f4 e = exp2(before);
-                put_row.template operator()<NK>(L::KR, tok + i, now.k[i].all() * e);
-                if constexpr (!SUM)
-                    put_row.template operator()<NQ>(L::QR, tok + i, now.q[i].all() * (e * p.scale));
+                put_row.template operator()<3>(L::KR, tok + i, now.k[i].all() * e);
+                if constexpr (!SUM) put_query(tok + i, now.q[i].all() * (e * p.scale));
             }
 #pragma unroll
             for (int i = TPL - 1; i >= 0; --i) {
@@ -1133,15 +1150,15 @@ void kda_prefill_kernel(DeltaProblem p) {
         f4 kS[2][CT], o[2][CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) kS[0][ct] = kS[1][ct] = o[0][ct] = o[1][ct] = z;
-        Operand<NK> ka_op[2];
-        Operand<NQ> qa_op[2];
+        Operand<3> ka_op[2];
+        typename L::RawQueries qa_op[2];
         Operand<3> b[2][CT];
         f4 em[2];
         auto read_rows = [&](int j) {  // k-step j / 2, row tile j % 2
             const int at = 16 * (j & 1) * L::RS;
-            ka_op[j & 1] = row_operand.template operator()<NK>(L::KR + at, j >> 1);
+            ka_op[j & 1] = row_operand.template operator()<3>(L::KR + at, j >> 1);
             if constexpr (!SUM)
-                qa_op[j & 1] = row_operand.template operator()<NQ>(L::QR + at, j >> 1);
+                qa_op[j & 1] = row_operand.template operator()<kRawQ>(L::QR + at, j >> 1);
         };
         auto read_em = [&](int kk) {
 #pragma unroll
@@ -1181,23 +1198,21 @@ void kda_prefill_kernel(DeltaProblem p) {
             if (kk + 1 < K / 32 && I < CT) split_state(kk + 1, I);
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
             if constexpr (SUM) {
-                mul_columns<MK, CT>(ka_op[I], b[kk & 1], kS[I]);
+                mul_columns<6, CT>(ka_op[I], b[kk & 1], kS[I]);
             } else {
+                const Operand<NQ> qa = L::queries(qa_op[I]);
 #pragma unroll
                 for (int i = 0; i < 6; ++i)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         const auto &bc = b[kk & 1][ct];
-                        if (i < MK)
-                            kS[I][ct] =
-                                mfma(ka_op[I].p[part_a(MK, i)], bc.p[part_b(MK, i)], kS[I][ct]);
+                        kS[I][ct] = mfma(ka_op[I].p[part_a(6, i)], bc.p[part_b(6, i)], kS[I][ct]);
                         if (i < MQ)
-                            o[I][ct] =
-                                mfma(qa_op[I].p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
+                            o[I][ct] = mfma(qa.p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
                     }
             }
-            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? NK : NK + NQ, 0);  // LDS reads
-            interleave<SUM ? MK * CT : (MK + MQ) * CT, SUM ? 5 : 3>();
+            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 3 : 3 + kRawQ, 0);  // LDS reads
+            interleave<SUM ? 6 * CT : (6 + MQ) * CT, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time, X the inverse's diagonal blocks times beta:
