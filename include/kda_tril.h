@@ -414,10 +414,9 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  *   state  [num_slots, H, K, V].
  * K 64 or 128, V a multiple of 32 up to 256, num_seqs x H < 2^23, else
  * KDA_ERR_UNSUPPORTED. State, decays and sums are FP32. The chunked form's
- * products take each FP32 factor as two or three bfloat16 parts: what the
- * state and an FP32 output are summed from is kept to about 2^-24 of each
- * term (within 1e-6 of the norm of exact arithmetic's, 512 tokens), what a
- * 16-bit output is summed from to about 2^-17.
+ * products take each FP32 factor as three bfloat16 parts and are kept to about
+ * 2^-24 of each term: state and FP32 outputs within 1e-6 of the norm of exact
+ * arithmetic's (512 tokens), 16-bit outputs those rounded once.
  *
  * workspace: with one of at least kda_prefill_workspace_size bytes,
  * kda_prefill_* cuts long prompts on few heads into segments of whole chunks

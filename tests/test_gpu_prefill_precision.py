@@ -10,7 +10,14 @@ factors, six products of the update and, through U, those of k S and of the
 inverse): sqrt(10) x 1.7e-8 = 5.5e-8 of its norm; 16 chunks without decay,
 roundings of random sign, 4 x 5.5e-8 = 2.2e-7; keys with a common direction make
 the inverse of I + L larger than that of unrelated ones by up to 3, which enters
-what a chunk adds. Together below 7e-7.
+what a chunk adds. Together below 7e-7. FP32 outputs are summed
+from the state and U likewise.
+
+Tolerance of 16-bit outputs against the exact ones rounded once: an error e
+moves a value over a rounding's border with probability at most 2 |e| / step,
+and then by a step of at most eps |x| (bf16: eps = 2^-7, f16: 2^-10). With e of
+norm 5e-7 (half of the FP32 outputs' bound; without the decays' extremes) the
+difference has a norm of at most sqrt(2 x 5e-7 x eps): 8.9e-5 and 3.2e-5.
 """
 import numpy as np
 import pytest
@@ -115,3 +122,16 @@ def test_fp32_outputs_of_alike_keys(kt, K, dtype, keys, rate):
         out, S = _run(kt, c, "f32", cut)
         assert _off(S, want) <= STATE, (cut, _off(S, want))
         assert _off(out, want_out) <= STATE, (cut, _off(out, want_out))
+
+
+@pytest.mark.parametrize("keys,rate", [("isotropic", 0.05), ("silu", 0.004),
+                                       ("channel means", 0.05), ("common", "mixed")])
+@pytest.mark.parametrize("lengths,H", [([512], 2), ([40] * 5, 64)])
+@pytest.mark.parametrize("K,dtype", [(128, "bf16"), (128, "f16"), (64, "bf16"), (64, "f16")])
+def test_16_bit_outputs_are_rounded_once(kt, K, dtype, lengths, H, keys, rate):
+    """One request, and more walks than compute units."""
+    c = _inputs(lengths, H, K, 128, dtype, keys, rate, 220 + K)
+    want = torch.from_numpy(_exact(c)[0]).to(gh.out_torch_dtype(dtype)).double().numpy()
+    out, _ = _run(kt, c, dtype, False)
+    eps = torch.finfo(gh.out_torch_dtype(dtype)).eps
+    assert _off(out, want) <= np.sqrt(2 * 5e-7 * eps), _off(out, want)

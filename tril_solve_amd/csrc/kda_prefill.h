@@ -12,19 +12,18 @@
 //
 // A workgroup per request, value head and 128 (or 64) value columns walks the
 // request's chunks. Every product runs on the bfloat16 matrix cores with FP32
-// accumulators, each FP32 factor taken as a sum of bfloat16 parts
-// (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)):
-//   6 products (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; about 2^-24 of
-//     each term) for all that the state is summed from and all that an FP32
-//     output is summed from;
-//   3 (hi hi, hi mid, mid hi; about 2^-17) for what a 16-bit output is summed
-//     from.
-// (State against 64 bits: 1e-7 to 4e-7. The correction L_10 U_0 in 3 products,
-// too, cost it up to 7e-6 where keys have a common direction. L and (k e^G) S in 3 products, too, took
-// 305 instead of 354 us on 16 x 512 tokens, but where decays are slow, the state
-// large against what a chunk adds, that cost it up to 2e-6.)
-// Against FP32 matrix instructions (16 x 16 x 32 in eight of 32 cycles) that
-// is 3 to 6 of 16 cycles. Sums, the state and the decays stay FP32.
+// accumulators, each FP32 factor taken as a sum of three bfloat16 parts
+// (hi = bf16(x), mid = bf16(x - hi), lo = bf16(x - hi - mid)), in six products
+// (hi hi, hi mid, mid hi, mid mid, hi lo, lo hi; about 2^-24 of each term). That
+// is 6 of 16 cycles against FP32 matrix instructions' eight of 32 (16 x 16 x 32).
+// Sums, the state and the decays stay FP32. State and FP32 outputs are 1e-7 to
+// 4e-7 of their norm from 64 bits, and a 16-bit output differs from the rounded
+// exact one as often as FP32 arithmetic does (bf16: 2e-5 to 5e-5 of the norm).
+// Fewer products were faster, but lost bits: three in L and (k e^G) S 2e-6 of the
+// state where decays are slow, three in the correction L_10 U_0 7e-6 where keys
+// have a common direction; three in P and what 16-bit outputs are summed from
+// (16 x 512 tokens 398 us instead of 462 on one card) four times as many
+// outputs rounded to the other neighbour.
 //
 //   * Each wavefront owns 32 (or 16) value columns of the state in registers
 //     (accumulator layout). Two accumulator tiles b = 0, 1 are the B operand of
@@ -87,52 +86,47 @@ __device__ __forceinline__ constexpr int operand_pos(int x) {
     return 8 * ((x & 15) >> 2) + 4 * (x >> 4) + (x & 3);
 }
 
-// The first N bfloat16 parts of two floats, packed in pairs.
-template <int N>
-__device__ __forceinline__ void split2(float a, float b, uint32_t (&part)[N]) {
+constexpr int kParts = 3;  // bfloat16 parts of an FP32 factor
+// The parts of two floats, packed in pairs.
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&part)[kParts]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < kParts; ++i) {
         uint32_t w = Elem<BF16>::pack(a, b);
         asm("" : "+v"(w));  // else a's own conversion is made a second time
         part[i] = w;
-        if (i + 1 < N) {
+        if (i + 1 < kParts) {
             a -= __builtin_bit_cast(float, w << 16);
             b -= __builtin_bit_cast(float, w & 0xFFFF0000u);
         }
     }
 }
-// An operand half: four values (one accumulator tile), N parts.
-template <int N>
+// The parts of an operand half: four values (one accumulator tile).
 struct Half {
-    w2 p[N];
+    w2 p[kParts];
 };
-template <int N>
-__device__ __forceinline__ Half<N> split4(f4 x) {
-    uint32_t a[N], b[N];
-    split2<N>(x[0], x[1], a);
-    split2<N>(x[2], x[3], b);
-    Half<N> h;
+__device__ __forceinline__ Half split4(f4 x) {
+    uint32_t a[kParts], b[kParts];
+    split2(x[0], x[1], a);
+    split2(x[2], x[3], b);
+    Half h;
 #pragma unroll
-    for (int i = 0; i < N; ++i) h.p[i] = w2{a[i], b[i]};
+    for (int i = 0; i < kParts; ++i) h.p[i] = w2{a[i], b[i]};
     return h;
 }
-// An operand: eight values, N parts.
-template <int N>
+// The parts of an operand: eight values.
 struct Operand {
-    w4 p[N];
+    w4 p[kParts];
 };
-template <int N>
-__device__ __forceinline__ Operand<N> join(const Half<N> &a, const Half<N> &b) {
-    Operand<N> o;
+__device__ __forceinline__ Operand join(const Half &a, const Half &b) {
+    Operand o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.p[i] = w4{a.p[i][0], a.p[i][1], b.p[i][0], b.p[i][1]};
+    for (int i = 0; i < kParts; ++i) o.p[i] = w4{a.p[i][0], a.p[i][1], b.p[i][0], b.p[i][1]};
     return o;
 }
-template <int N>
-__device__ __forceinline__ Half<N> half_of(const Operand<N> &o, int which) {
-    Half<N> h;
+__device__ __forceinline__ Half half_of(const Operand &o, int which) {
+    Half h;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < kParts; ++i)
         h.p[i] = which ? w2{o.p[i][2], o.p[i][3]} : w2{o.p[i][0], o.p[i][1]};
     return h;
 }
@@ -146,24 +140,23 @@ __device__ __forceinline__ f4 mfma(w2 a, w2 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a),
                                                      __builtin_bit_cast(s4, b), c, 0, 0, 0);
 }
-// c + a b in M = 3 or 6 products, the smallest first; several such sums are
-// formed product by product, since a product that waits for the one before it
-// takes 21 cycles instead of 16. part_a, part_b: the parts of product i.
-constexpr int part_a(int M, int i) {
+// c + a b in six products, the smallest first; several such sums are formed
+// product by product, since a product that waits for the one before it takes 21
+// cycles instead of 16. part_a, part_b: the parts of product i.
+constexpr int part_a(int i) {
     constexpr int a[] = {2, 0, 1, 1, 0, 0};
-    return a[6 - M + i];
+    return a[i];
 }
-constexpr int part_b(int M, int i) {
+constexpr int part_b(int i) {
     constexpr int b[] = {0, 2, 1, 0, 1, 0};
-    return b[6 - M + i];
+    return b[i];
 }
-template <int M, int CT, class A, class B>
+template <int CT, class A, class B>
 __device__ __forceinline__ void mul_columns(const A &a, const B (&b)[CT], f4 (&c)[CT]) {
 #pragma unroll
-    for (int i = 0; i < M; ++i)
+    for (int i = 0; i < 6; ++i)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-            c[ct] = mfma(a.p[part_a(M, i)], b[ct].p[part_b(M, i)], c[ct]);
+        for (int ct = 0; ct < CT; ++ct) c[ct] = mfma(a.p[part_a(i)], b[ct].p[part_b(i)], c[ct]);
 }
 
 // Shapes the schedule of the code around it: N times one matrix instruction
@@ -310,23 +303,22 @@ __device__ __forceinline__ void gather_groups(f4 x, f4 (&out)[G]) {
 // of a row are exchanged by an exclusive or with the row number so that the 16
 // rows of one operand read, and the 4 rows of 4 adjacent pieces of a transposed
 // one, fall in different banks without padding.
-// OUT: kda_dtype of the output; N: chunks whose operands are held at once.
-template <int K, int OUT, int N>
+// N: chunks whose operands are held at once.
+template <int K, int N>
 struct PreLds {
     static constexpr int RS = 2 * K, TS = 2 * kPreC;
     static constexpr int kPatch = 20;  // floats between rows of a block of L
     static constexpr int R32 = kPreC * RS;
-    static constexpr int NQ = OUT == 0 ? 3 : 2;  // parts of queries and P
     // Three parts of the queries do not fit beside those of the keys with K =
     // 128: they lie there in FP32, in the room of two parts, and are split by
-    // the wavefronts that read them (8 x 512 tokens, 64 heads, f32: 267 us; 240
-    // with the keys in two parts instead, which left 1e-6 of the state).
-    static constexpr bool kSplitLate = K == 128 && NQ == 3;
+    // the wavefronts that read them.
+    static constexpr bool kSplitLate = K == 128;
+    static constexpr int kRawQ = kSplitLate ? 2 : kParts;  // pieces of a queries' operand
     // N chunks' operands, each:
     // keys and queries times e^{G - m} (steep: e^G), keys times e^{m - G}
     // (steep: e^{G_32 - G})
-    static constexpr int KR = 0, QR = KR + 3 * R32, KL = QR + (kSplitLate ? 2 : NQ) * R32;
-    static constexpr int kOperands = KL + 3 * R32;
+    static constexpr int KR = 0, QR = KR + kParts * R32, KL = QR + kRawQ * R32;
+    static constexpr int kOperands = KL + kParts * R32;
     // a steep chunk's first half: keys, queries, decays FP32, then L / beta and P
     static constexpr int SK = 0, SQ = SK + kPreC * K * 4, SA = SQ + kPreC * K * 4;
     static constexpr int SM = SA + kPreC * K * 4, SP = SM + kPreC * kPreC * 4;
@@ -336,8 +328,8 @@ struct PreLds {
     static constexpr int LOW = 16 * TS / 2, T32 = LOW + 16 * TS;
     // diagonal blocks of the inverse and -L_10; P
     static constexpr int TM = kOperands > kSteepBytes ? kOperands : kSteepBytes;
-    static constexpr int PM = TM + 3 * T32;
-    static constexpr int kBuffer = PM + NQ * T32;
+    static constexpr int PM = TM + kParts * T32;
+    static constexpr int kBuffer = PM + kParts * T32;
     static_assert(kBuffer % 256 == 0);
     // per channel: what S' is of the state in registers (steep: 1), what that
     // state owes (see `apart`), and for a steep chunk e^{G_32}; N chunks'
@@ -357,16 +349,18 @@ struct PreLds {
         return (high * 4 + low) << 4;
     }
     static __device__ __forceinline__ int swz_tok(int row) { return ((row >> 2) & 3) << 4; }
-    // 16 rows of an operand reduced over channels as loaded: the parts of the
-    // queries, or the two halves of this lane's eight FP32 queries.
-    typedef Operand<kSplitLate ? 2 : NQ> RawQueries;
-    static __device__ __forceinline__ Operand<NQ> queries(const RawQueries &r) {
-        if constexpr (kSplitLate)
-            return join(split4<3>(__builtin_bit_cast(f4, r.p[0])),
-                        split4<3>(__builtin_bit_cast(f4, r.p[1])));
-        else
-            return r;
-    }
+    // 16 rows of the queries' operand as loaded: its parts, or the two halves of
+    // this lane's eight FP32 values.
+    struct Queries {
+        w4 p[kRawQ];
+        __device__ __forceinline__ Operand parts() const {
+            if constexpr (kSplitLate)
+                return join(split4(__builtin_bit_cast(f4, p[0])),
+                            split4(__builtin_bit_cast(f4, p[1])));
+            else
+                return Operand{p[0], p[1], p[kRawQ - 1]};
+        }
+    };
 };
 
 // x = (I + L)^-1, one lane per column of a 16 x 16 block in every 16-lane row:
@@ -544,16 +538,13 @@ template <class EI, int K, int OUT, bool SUM, bool ROLES, int CT>
 __global__
 __launch_bounds__((PreShape<SUM, ROLES, CT>::kThreads), (PreShape<SUM, ROLES, CT>::kPerSimd))
 void kda_prefill_kernel(DeltaProblem p) {
-    typedef PreLds<K, OUT, ROLES ? 2 : 1> L;
+    typedef PreLds<K, ROLES ? 2 : 1> L;
     typedef PreShape<SUM, ROLES, CT> Shape;
     constexpr int CW = Shape::kCols;
     constexpr int NT = K / 16;  // state row tiles
     // A wavefront prepares 8 tokens: K / 4 lanes of 4 channels to a token, in
     // GRP groups of lanes with TPL tokens each.
     constexpr int GRP = 4 * kWave / K, TPL = 8 / GRP;
-    constexpr int NQ = L::NQ;
-    constexpr int MQ = OUT == 0 ? 6 : 3;  // products for P, P U and (q e^G) S
-    constexpr int kRawQ = L::kSplitLate ? 2 : NQ;  // pieces of a queries' operand in LDS
     constexpr int OE = OUT == 0 ? 4 : 2;  // bytes of an output element
     __shared__ __align__(16) char lds[L::kBytes];
 
@@ -713,29 +704,29 @@ void kda_prefill_kernel(DeltaProblem p) {
         const float *tots = reinterpret_cast<const float *>(lds + L::TOT + buf * L::kTot);
         const float *beta = reinterpret_cast<const float *>(lds + L::BETA) + buf * kPreC;
 
-        auto put_row = [&]<int N>(int at, int row, f4 x) {
+        auto put_row = [&](int at, int row, f4 x) {
             char *d = op + at + row * L::RS + ((2 * ch) ^ L::swz_row(row));
-            const Half<N> hx = split4<N>(x);
+            const Half hx = split4(x);
 #pragma unroll
-            for (int i = 0; i < N; ++i) *reinterpret_cast<w2 *>(d + i * L::R32) = hx.p[i];
+            for (int i = 0; i < kParts; ++i) *reinterpret_cast<w2 *>(d + i * L::R32) = hx.p[i];
         };
         auto put_query = [&](int row, f4 x) {
             if constexpr (L::kSplitLate)  // channels 8 i + 4 e .. + 3 to the half e
                 *reinterpret_cast<f4 *>(op + L::QR + (ch >> 2 & 1) * L::R32 + row * L::RS +
                                         ((2 * (ch & ~7)) ^ L::swz_row(row))) = x;
             else
-                put_row.template operator()<NQ>(L::QR, row, x);
+                put_row(L::QR, row, x);
         };
         // entries (row, c) and (row + 1, c), row even, of an operand reduced
         // over tokens; low: rows 16..31
-        auto put_pair = [&]<int N>(int at, bool low, int row, int c, float x, float y) {
+        auto put_pair = [&](int at, bool low, int row, int c, float x, float y) {
             char *d = op + at + (low ? L::LOW + row * L::TS +
                                            ((2 * operand_pos(c)) ^ L::swz_tok(row))
                                      : row * (L::TS / 2) + 2 * c);
-            uint32_t part[N];
-            split2<N>(x, y, part);
+            uint32_t part[kParts];
+            split2(x, y, part);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < kParts; ++i) {
                 *reinterpret_cast<uint16_t *>(d + i * L::T32) = (uint16_t)part[i];
                 *reinterpret_cast<uint16_t *>(d + i * L::T32 + (low ? L::TS : L::TS / 2)) =
                     (uint16_t)(part[i] >> 16);
@@ -763,9 +754,9 @@ void kda_prefill_kernel(DeltaProblem p) {
         // the factor of token i of this lane's: keys, queries and their inverse
         auto put_token = [&](int i, f4 e) {
             const f4 k = now.k[i].all();
-            put_row.template operator()<3>(L::KR, tok + i, k * e);
+            put_row(L::KR, tok + i, k * e);
             if constexpr (!SUM) put_query(tok + i, now.q[i].all() * (e * p.scale));
-            put_row.template operator()<3>(L::KL, tok + i, k * rcp(e));
+            put_row(L::KL, tok + i, k * rcp(e));
         };
         // from the chunk's middle to this lane's first token, of the wavefronts'
         // totals and this one's groups
@@ -852,10 +843,10 @@ void kda_prefill_kernel(DeltaProblem p) {
 
         const int rpos = n16 * L::RS + ((g4 << 4) ^ L::swz_row(n16));
         // 16 rows of an operand reduced over channels, k-step kk
-        auto row_operand = [&]<int N>(int at, int kk) -> Operand<N> {
-            Operand<N> o;
+        auto row_operand = [&]<class O>(int at, int kk) -> O {
+            O o;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < (int)(sizeof(O) / sizeof(w4)); ++i)
                 o.p[i] = *reinterpret_cast<const w4 *>(op + at + i * L::R32 + (rpos ^ (64 * kk)));
             return o;
         };
@@ -865,35 +856,42 @@ void kda_prefill_kernel(DeltaProblem p) {
         f4 m[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
         if (!far) {
             // rows 16 bi .. of the keys or queries against rows 16 bj .. of the keys
-            auto block = [&]<int M, int N, bool Q>(int bi, int bj) -> f4 {
-                Operand<N> l[K / 32], r[K / 32];
-#pragma unroll
-                for (int kk = 0; kk < K / 32; ++kk) {
-                    if constexpr (Q)
-                        l[kk] = L::queries(row_operand.template operator()<kRawQ>(
-                            L::QR + 16 * bi * L::RS, kk));
-                    else
-                        l[kk] = row_operand.template operator()<N>(L::KR + 16 * bi * L::RS, kk);
-                    r[kk] = row_operand.template operator()<N>(L::KL + 16 * bj * L::RS, kk);
-                }
+            auto block = [&]<bool Q>(int bi, int bj) -> f4 {
                 f4 c[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-                for (int kk = 0; kk < K / 32; kk += 2)
+                for (int kk = 0; kk < K / 32; kk += 2) {
+                    Operand l[2], r[2];
 #pragma unroll
-                    for (int i = 0; i < M; ++i)
+                    for (int e = 0; e < 2; ++e) {
+                        if constexpr (Q)
+                            l[e] = row_operand
+                                       .template operator()<typename L::Queries>(
+                                           L::QR + 16 * bi * L::RS, kk + e)
+                                       .parts();
+                        else
+                            l[e] = row_operand.template operator()<Operand>(
+                                L::KR + 16 * bi * L::RS, kk + e);
+                        r[e] = row_operand.template operator()<Operand>(L::KL + 16 * bj * L::RS,
+                                                                        kk + e);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 6; ++i)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            c[e] = mfma(l[kk + e].p[part_a(M, i)], r[kk + e].p[part_b(M, i)], c[e]);
+                            c[e] = mfma(l[e].p[part_a(i)], r[e].p[part_b(i)], c[e]);
+                    // (all of them read ahead spill where the state is held, too)
+                    if constexpr (!ROLES) __builtin_amdgcn_sched_barrier(0);
+                }
                 return c[0] + c[1];
             };
             if (pw < 2) {
-                m[0] = block.template operator()<6, 3, false>(pw, pw);
+                m[0] = block.template operator()<false>(pw, pw);
             } else if (pw == 3) {
-                m[0] = block.template operator()<6, 3, false>(1, 0);
-                if constexpr (!SUM) m[1] = block.template operator()<MQ, NQ, true>(1, 0);
+                m[0] = block.template operator()<false>(1, 0);
+                if constexpr (!SUM) m[1] = block.template operator()<true>(1, 0);
             } else if constexpr (!SUM) {
-                m[0] = block.template operator()<MQ, NQ, true>(0, 0);
-                m[1] = block.template operator()<MQ, NQ, true>(1, 1);
+                m[0] = block.template operator()<true>(0, 0);
+                m[1] = block.template operator()<true>(1, 1);
             }
         } else {
             // running products of the decays from token j on
@@ -972,7 +970,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             }
 #pragma unroll
             for (int s = 0; s < 4; s += 2)
-                put_pair.template operator()<3>(L::TM, pw == 1, 4 * g4 + s, 16 * pw + n16, y[s],
+                put_pair(L::TM, pw == 1, 4 * g4 + s, 16 * pw + n16, y[s],
                                                 y[s + 1]);
         } else if (pw == 2) {
             if constexpr (!SUM)
@@ -981,17 +979,17 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
                     for (int s = 0; s < 4; s += 2) {
                         const int r = 4 * g4 + s;
-                        put_pair.template operator()<NQ>(L::PM, b == 1, r, 16 * b + n16,
+                        put_pair(L::PM, b == 1, r, 16 * b + n16,
                                                          n16 <= r ? m[b][s] : 0.0f,
                                                          n16 <= r + 1 ? m[b][s + 1] : 0.0f);
                     }
         } else {
 #pragma unroll
             for (int s = 0; s < 4; s += 2) {
-                put_pair.template operator()<3>(L::TM, true, 4 * g4 + s, n16, -m[0][s],
+                put_pair(L::TM, true, 4 * g4 + s, n16, -m[0][s],
                                                 -m[0][s + 1]);
                 if constexpr (!SUM)
-                    put_pair.template operator()<NQ>(L::PM, true, 4 * g4 + s, n16, m[1][s],
+                    put_pair(L::PM, true, 4 * g4 + s, n16, m[1][s],
                                                      m[1][s + 1]);
             }
         }
@@ -1031,12 +1029,12 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int i = 0; i < TPL; ++i) {
                 before += g2[i];
                 const f4 e = exp2(before);
-                put_row.template operator()<3>(L::KR, tok + i, now.k[i].all() * e);
+                put_row(L::KR, tok + i, now.k[i].all() * e);
                 if constexpr (!SUM) put_query(tok + i, now.q[i].all() * (e * p.scale));
             }
 #pragma unroll
             for (int i = TPL - 1; i >= 0; --i) {
-                put_row.template operator()<3>(L::KL, tok + i, now.k[i].all() * exp2(after));
+                put_row(L::KL, tok + i, now.k[i].all() * exp2(after));
                 after += g2[i];
             }
         }
@@ -1119,26 +1117,26 @@ void kda_prefill_kernel(DeltaProblem p) {
         const int rpos = n16 * L::RS + ((g4 << 4) ^ L::swz_row(n16));
         const char *op = lds + buf * L::kBuffer, *fac = lds + L::FACTORS + buf * L::kFactors;
         // 16 rows of an operand reduced over channels, k-step kk
-        auto row_operand = [&]<int N>(int at, int kk) -> Operand<N> {
-            Operand<N> o;
+        auto row_operand = [&]<class O>(int at, int kk) -> O {
+            O o;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < (int)(sizeof(O) / sizeof(w4)); ++i)
                 o.p[i] = *reinterpret_cast<const w4 *>(op + at + i * L::R32 + (rpos ^ (64 * kk)));
             return o;
         };
         // a lower triangle's rows 0..15, and 16..31
-        auto top_operand = [&]<int N>(int at) -> Half<N> {
-            Half<N> o;
+        auto top_operand = [&](int at) {
+            Half o;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < kParts; ++i)
                 o.p[i] = *reinterpret_cast<const w2 *>(op + at + i * L::T32 + n16 * (L::TS / 2) +
                                                        8 * g4);
             return o;
         };
-        auto low_operand = [&]<int N>(int at) -> Operand<N> {
-            Operand<N> o;
+        auto low_operand = [&](int at) {
+            Operand o;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < kParts; ++i)
                 o.p[i] = *reinterpret_cast<const w4 *>(op + at + i * L::T32 + L::LOW +
                                                        n16 * L::TS + ((g4 << 4) ^ L::swz_tok(n16)));
             return o;
@@ -1150,15 +1148,15 @@ void kda_prefill_kernel(DeltaProblem p) {
         f4 kS[2][CT], o[2][CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) kS[0][ct] = kS[1][ct] = o[0][ct] = o[1][ct] = z;
-        Operand<3> ka_op[2];
-        typename L::RawQueries qa_op[2];
-        Operand<3> b[2][CT];
+        Operand ka_op[2];
+        typename L::Queries qa_op[2];
+        Operand b[2][CT];
         f4 em[2];
         auto read_rows = [&](int j) {  // k-step j / 2, row tile j % 2
             const int at = 16 * (j & 1) * L::RS;
-            ka_op[j & 1] = row_operand.template operator()<3>(L::KR + at, j >> 1);
+            ka_op[j & 1] = row_operand.template operator()<Operand>(L::KR + at, j >> 1);
             if constexpr (!SUM)
-                qa_op[j & 1] = row_operand.template operator()<kRawQ>(L::QR + at, j >> 1);
+                qa_op[j & 1] = row_operand.template operator()<typename L::Queries>(L::QR + at, j >> 1);
         };
         auto read_em = [&](int kk) {
 #pragma unroll
@@ -1169,7 +1167,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         auto split_state = [&](int kk, int ct) {  // S' (also of a steep chunk, where it is S)
 #pragma unroll
             for (int t = 0; t < 2; ++t) S[2 * kk + t][ct] *= em[t];
-            b[kk & 1][ct] = join(split4<3>(S[2 * kk][ct]), split4<3>(S[2 * kk + 1][ct]));
+            b[kk & 1][ct] = join(split4(S[2 * kk][ct]), split4(S[2 * kk + 1][ct]));
         };
         if (apart) {
 #pragma unroll
@@ -1198,21 +1196,20 @@ void kda_prefill_kernel(DeltaProblem p) {
             if (kk + 1 < K / 32 && I < CT) split_state(kk + 1, I);
             if (I == 1 && kk + 2 < K / 32) read_em(kk + 2);
             if constexpr (SUM) {
-                mul_columns<6, CT>(ka_op[I], b[kk & 1], kS[I]);
+                mul_columns<CT>(ka_op[I], b[kk & 1], kS[I]);
             } else {
-                const Operand<NQ> qa = L::queries(qa_op[I]);
+                const Operand qa = qa_op[I].parts();
 #pragma unroll
                 for (int i = 0; i < 6; ++i)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         const auto &bc = b[kk & 1][ct];
-                        kS[I][ct] = mfma(ka_op[I].p[part_a(6, i)], bc.p[part_b(6, i)], kS[I][ct]);
-                        if (i < MQ)
-                            o[I][ct] = mfma(qa.p[part_a(MQ, i)], bc.p[part_b(MQ, i)], o[I][ct]);
+                        kS[I][ct] = mfma(ka_op[I].p[part_a(i)], bc.p[part_b(i)], kS[I][ct]);
+                        o[I][ct] = mfma(qa.p[part_a(i)], bc.p[part_b(i)], o[I][ct]);
                     }
             }
-            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 3 : 3 + kRawQ, 0);  // LDS reads
-            interleave<SUM ? 6 * CT : (6 + MQ) * CT, SUM ? 5 : 3>();
+            __builtin_amdgcn_sched_group_barrier(0x100, SUM ? 3 : 3 + L::kRawQ, 0);  // LDS reads
+            interleave<SUM ? 6 * CT : 12 * CT, SUM ? 5 : 3>();
             __builtin_amdgcn_sched_barrier(0);
         }
         // U, 16 rows at a time, X the inverse's diagonal blocks times beta:
@@ -1225,33 +1222,33 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) R[I][ct][s] = vraw[I][s].at(ct) - kS[I][ct][s];
         if (ROLES && t0 + kPreC < len_all) load_values(t0 + kPreC);
-        Operand<3> u[CT];
+        Operand u[CT];
         {
-            const auto x0 = top_operand.template operator()<3>(L::TM);
-            const auto x1 = low_operand.template operator()<3>(L::TM);
-            const auto p0 = top_operand.template operator()<NQ>(L::PM);
-            const auto p1 = low_operand.template operator()<NQ>(L::PM);
-            Half<3> r[CT], h0[CT];
+            const auto x0 = top_operand(L::TM);
+            const auto x1 = low_operand(L::TM);
+            const auto p0 = top_operand(L::PM);
+            const auto p1 = low_operand(L::PM);
+            Half r[CT], h0[CT];
             f4 x[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                r[ct] = split4<3>(R[0][ct]);
+                r[ct] = split4(R[0][ct]);
                 x[ct] = z;
             }
-            mul_columns<6, CT>(x0, r, x);
+            mul_columns<CT>(x0, r, x);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) h0[ct] = split4<3>(x[ct]);
-            mul_columns<6, CT>(half_of(x1, 0), h0, R[1]);
-            if constexpr (!SUM) mul_columns<MQ, CT>(p0, h0, o[0]);
+            for (int ct = 0; ct < CT; ++ct) h0[ct] = split4(x[ct]);
+            mul_columns<CT>(half_of(x1, 0), h0, R[1]);
+            if constexpr (!SUM) mul_columns<CT>(p0, h0, o[0]);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                r[ct] = split4<3>(R[1][ct]);
+                r[ct] = split4(R[1][ct]);
                 x[ct] = z;
             }
-            mul_columns<6, CT>(half_of(x1, 1), r, x);
+            mul_columns<CT>(half_of(x1, 1), r, x);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) u[ct] = join(h0[ct], split4<3>(x[ct]));
-            if constexpr (!SUM) mul_columns<MQ, CT>(p1, u, o[1]);
+            for (int ct = 0; ct < CT; ++ct) u[ct] = join(h0[ct], split4(x[ct]));
+            if constexpr (!SUM) mul_columns<CT>(p1, u, o[1]);
         }
         if constexpr (!SUM) {
             const Rsrc ro = rows_of(ob + (long)t0 * os, os, p.V * OE, len);
@@ -1264,7 +1261,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         }
         // the state: S' + (k e^{m - G})^T U, which owes e^{G_32 - m}; of a steep
         // chunk e^{G_32} S + (k e^{G_32 - G})^T U
-        Operand<3> kt[2];
+        Operand kt[2];
         // rows of tile rt are channels, reduced over tokens: 4 x 16 blocks of
         // the keys' rows, transposed by the read (lane 4 r + c of 16 gives the
         // address of 4 channels of token r, lane j gets channel j's 4 tokens).
@@ -1301,7 +1298,7 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
         for (int rt = 0; rt < NT; ++rt) {
             if (rt + 1 < NT) read_state(rt + 1);
-            mul_columns<6, CT>(kt[rt & 1], u, S[rt]);
+            mul_columns<CT>(kt[rt & 1], u, S[rt]);
             __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
             interleave<6 * CT, 1>();
             __builtin_amdgcn_sched_barrier(0);
@@ -1414,17 +1411,17 @@ hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t st
     // all, which 32 to a wavefront would leave to two of four wavefronts (1,024
     // walks of 512 tokens, K = 128, V = 64, 266 -> 247 us; K = V = 64 195 and 197).
     auto with_out = [&]<int K, int OUT>() {
-        // FP32 rows on their way, or a third part of queries, P and S', leave a
-        // wavefront that does both without registers (it spills; FP32 in and
-        // out, 1,024 walks of 512 tokens 420 -> 542 us)
-        constexpr bool kRoles = K == 128 && (EI::kBytes == 4 || OUT == 0);
+        // FP32 rows on their way leave a wavefront that does both without
+        // registers: it spills (f32, 40 requests of 1 to 2,000 tokens, 16 heads
+        // 761 -> 835 us; 64 of 64 tokens, 64 heads 374 and 334)
+        constexpr bool kRoles = K == 128 && EI::kBytes == 4;
         if (pass == PrePass::narrow) return go.template operator()<K, OUT, false, true, 1>();
         if (pass == PrePass::roles) return go.template operator()<K, OUT, false, true, 2>();
         return p.V <= 64 ? go.template operator()<K, OUT, false, kRoles, 1>()
                          : go.template operator()<K, OUT, false, kRoles, 2>();
     };
     auto with_k = [&]<int K>() {
-        // (OUT of the sums: two parts for the corrections, as for 16-bit outputs)
+        // (the sums have no outputs: OUT does not matter)
         return pass == PrePass::sums ? go.template operator()<K, 1, true, true, 2>()
                : p.out_dt == 0       ? with_out.template operator()<K, 0>()
                : p.out_dt == 1       ? with_out.template operator()<K, 1>()
