@@ -207,8 +207,11 @@ __global__ __launch_bounds__(kConvThreads) void kda_conv_prefill_kernel(ConvProb
     }
     // the request that row t0 lies in, and the next one to start
     int t = t0, cur_bos = 0, cur_end = 0;  // rows [cur_bos, cur_end) of the current request
-    int next = p.req.cu ? requests_before(p.req.cu, N, t0, lane)
-                        : (t0 + p.req.seq_len - 1) / max(p.req.seq_len, 1);
+    int next = 0;  // (dense requests of no tokens all start at row 0)
+    if (p.req.cu)
+        next = requests_before(p.req.cu, N, t0, lane);
+    else if (p.req.seq_len > 0)
+        next = (t0 + p.req.seq_len - 1) / p.req.seq_len;
     next = __builtin_amdgcn_readfirstlane(next);
     if (next > 0 && end_of(next - 1) > t0) {  // inside request next - 1
         cur_bos = start_of(next - 1);
