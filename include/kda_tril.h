@@ -418,6 +418,11 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  * 2^-24 of each term: state and FP32 outputs within 1e-6 of the norm of exact
  * arithmetic's (512 tokens), 16-bit outputs those rounded once.
  *
+ * A value that is not finite (but for a gate of -inf) reaches the outputs of its
+ * own token and, but for q, of the later ones of its request and head, and their
+ * state; from v only those of its column. kda_recurrent_* leaves NaN or infinities
+ * there, kda_prefill_* NaN.
+ *
  * workspace: with one of at least kda_prefill_workspace_size bytes,
  * kda_prefill_* cuts long prompts on few heads into segments of whole chunks
  * that run side by side (the results agree to rounding with those of one

@@ -63,3 +63,84 @@ def test_dense_delta_rule_of_no_tokens(kt, form):
     assert out.shape == (B, 0, H, V)
     pool[order[1:B]] = 0.0
     assert np.array_equal(S.cpu().numpy(), pool)
+
+
+# A value that is not finite reaches the outputs of its own token and of later
+# ones of its request and head (from v: of its column), and nothing else. The
+# outputs before it are the exact ones to 4e-6 of the largest products' size: 128
+# terms and a few roundings a token in FP32, 2^-24 (sqrt(128) + 4 x 40).
+
+_FORMS = {"recurrent": dict(requests=1, H=2), "narrow": dict(requests=1, H=2),
+          "roles": dict(requests=4, H=48), "whole": dict(requests=6, H=48),
+          "cut": dict(requests=1, H=2, cut=True)}
+
+
+def _problem(requests, H, K, V, dtype, T, seed):
+    rng = np.random.default_rng(seed)
+    n = requests * T
+    unit = lambda: (lambda x: x / np.linalg.norm(x, axis=-1, keepdims=True))(  # noqa: E731
+        rng.standard_normal((n, H, K)))
+    t = gh.out_torch_dtype(dtype)
+    low = lambda x: torch.from_numpy(x).to(t).double().numpy()  # noqa: E731
+    return dict(q=low(unit()), k=low(unit()), v=low(rng.standard_normal((n, H, V))),
+                g=(-0.1 * rng.random((n, H, K))).astype(np.float32).astype(np.float64),
+                beta=rng.uniform(0.2, 0.9, (n, H)).astype(np.float32).astype(np.float64),
+                state=0.2 * rng.standard_normal((requests, H, K, V)))
+
+
+def _delta(kt, form, c, requests, T, dtype, cut=False, **_):
+    t = gh.out_torch_dtype(dtype)
+    q, k, v = (torch.from_numpy(c[x]).to(t).to(DEV) for x in "qkv")
+    g, beta, S = (_dev(c[x].astype(np.float32)) for x in ("g", "beta", "state"))
+    cu = _dev((T * np.arange(requests + 1)).astype(np.int32))
+    out = torch.empty_like(v)
+    if form == "recurrent":
+        kt.kda_recurrent(q, k, v, g, beta, out, cu, state=S)
+    else:
+        n = kt.kda_prefill_workspace_size(v.shape[0], requests, v.shape[1], k.shape[2],
+                                          v.shape[2]) if cut else 0
+        assert bool(n) == cut
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV) if cut else None
+        kt.kda_prefill(q, k, v, g, beta, out, cu, state=S, workspace=ws)
+    return gh.to_numpy_f64(out), S.cpu().numpy()
+
+
+@pytest.mark.parametrize("what,value", [("v", np.nan), ("v", np.inf), ("v", -np.inf),
+                                        ("k", np.nan), ("k", np.inf), ("beta", np.nan),
+                                        ("g", np.nan), ("g", np.inf), ("q", np.nan)])
+@pytest.mark.parametrize("K,dtype", [(128, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("form", list(_FORMS))
+def test_values_that_are_not_finite(kt, form, K, dtype, what, value):
+    f = _FORMS[form]
+    T, V, h = 530 if f.get("cut") else 70, 128, 1
+    r = f["requests"] - 1  # the last request
+    for at in ((40, 500, 517) if f.get("cut") else (0, 5, 21, 40)):
+        print(f"\n[not finite] {form} {what} {value} token {at}", flush=True)
+        c = _problem(f["requests"], f["H"], K, V, dtype, T, 50 + K)
+        clean, S_clean = _delta(kt, form, c, T=T, dtype=dtype, **f)
+        row = r * T + at
+        if what == "beta":
+            c[what][row, h] = value
+        else:
+            c[what][row, h, 3] = value
+        out, S = _delta(kt, form, c, T=T, dtype=dtype, **f)
+        hit = np.zeros(out.shape, bool)  # what has to be not finite
+        hit[row:row + 1 if what == "q" else (r + 1) * T, h, 3 if what == "v" else slice(None)] = True
+        assert not np.isfinite(out[hit]).any()
+        hit_S = np.zeros(S.shape, bool)
+        if what != "q":
+            hit_S[r, h, :, 3 if what == "v" else slice(None)] = True
+        assert not np.isfinite(S[hit_S]).any()
+        # all else: the same bits, but for the request and head whose decays,
+        # keys or write strengths changed, to the exact outputs
+        own = np.zeros(out.shape, bool)
+        own[r * T:(r + 1) * T, h] = what in ("k", "beta", "g")
+        assert np.array_equal(out[~hit & ~own], clean[~hit & ~own])
+        assert np.array_equal(S[~hit_S], S_clean[~hit_S])
+        if what in ("k", "beta", "g") and at > 0:
+            s = slice(r * T, row)
+            part = lambda x: c[x][s, h:h + 1]  # noqa: E731
+            want, _, N = ref.delta_rule(part("q"), part("k"), part("v"), part("g"), part("beta"),
+                                        [at], c["state"][r:r + 1, h:h + 1], None, None, K ** -0.5)
+            half = torch.finfo(gh.out_torch_dtype(dtype)).eps / 2
+            assert (np.abs(out[s, h:h + 1] - want) <= 4e-6 * N + half * np.abs(want)).all()

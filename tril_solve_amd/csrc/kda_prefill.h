@@ -276,6 +276,13 @@ __device__ __forceinline__ f4 rcp(f4 x) {
     return f4{__builtin_amdgcn_rcpf(x[0]), __builtin_amdgcn_rcpf(x[1]),
               __builtin_amdgcn_rcpf(x[2]), __builtin_amdgcn_rcpf(x[3])};
 }
+__device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
+// The largest magnitude, or NaN where there is one.
+__device__ __forceinline__ float largest(float a, f4 x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a = __builtin_elementwise_maximum(a, __builtin_fabsf(x[e]));
+    return a;
+}
 // out[g] = x of the lane at the same place in group g, G groups of 64 / G lanes.
 template <int G>
 __device__ __forceinline__ void gather_groups(f4 x, f4 (&out)[G]) {
@@ -322,7 +329,8 @@ struct PreLds {
     // a steep chunk's first half: keys, queries, decays FP32, then L / beta and P
     static constexpr int SK = 0, SQ = SK + kPreC * K * 4, SA = SQ + kPreC * K * 4;
     static constexpr int SM = SA + kPreC * K * 4, SP = SM + kPreC * kPreC * 4;
-    static constexpr int kSteepBytes = SP + kPreC * kPreC * 4;
+    // (and each wavefront's first token that is not finite)
+    static constexpr int STOP = SP + kPreC * kPreC * 4, kSteepBytes = STOP + kPreWaves * 4;
     // a lower triangle of 32 x 32: the block of rows 0..15 (16 tokens), then
     // rows 16..31 (32 tokens)
     static constexpr int LOW = 16 * TS / 2, T32 = LOW + 16 * TS;
@@ -531,12 +539,14 @@ struct PreShape {
     static constexpr int kCols = SUM ? 8 : 4;  // wavefronts with columns
     static constexpr int kWidth = kCols * 16 * CT;  // columns of a workgroup
     static constexpr int kThreads = kWave * (ROLES ? kCols + kPreWaves : kCols);
-    static constexpr int kPerSimd = SUM ? 3 : 2;  // wavefronts, by their registers
+    // wavefronts, by their registers (three of whole K = 64: 16 x 512 tokens, 64
+    // heads, V = 64, 205 -> 197 us)
+    static constexpr int per_simd(int K) { return SUM || (K == 64 && !ROLES && CT == 1) ? 3 : 2; }
     static_assert(ROLES || kCols == kPreWaves);
 };
 template <class EI, int K, int OUT, bool SUM, bool ROLES, int CT>
 __global__
-__launch_bounds__((PreShape<SUM, ROLES, CT>::kThreads), (PreShape<SUM, ROLES, CT>::kPerSimd))
+__launch_bounds__((PreShape<SUM, ROLES, CT>::kThreads), (PreShape<SUM, ROLES, CT>::per_simd(K)))
 void kda_prefill_kernel(DeltaProblem p) {
     typedef PreLds<K, ROLES ? 2 : 1> L;
     typedef PreShape<SUM, ROLES, CT> Shape;
@@ -670,6 +680,12 @@ void kda_prefill_kernel(DeltaProblem p) {
                 for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(now.g[i][e], kLog2E, x[e]);
                 er[i] = x;
             }
+            // a key or write strength that is not finite shows in the totals
+            // (and the chunk takes the steep path, which looks for its token)
+            float most = pw == 3 ? now.beta : 0.0f;
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) most = largest(most, now.k[i].all());
+            x[0] = __builtin_fmaf(most, 0.0f, x[0]);
             gather_groups<GRP>(x, sums);
             f4 all = sums[0];
 #pragma unroll
@@ -692,8 +708,9 @@ void kda_prefill_kernel(DeltaProblem p) {
             __syncthreads();
     };
     // What the chunk at t0 puts into buffer `buf`, from its loaded rows and the
-    // wavefronts' totals; far, apart: see there.
-    auto prepare = [&](int buf, bool &far, bool &apart) {
+    // wavefronts' totals; far, apart: see there; stop: the first token with a
+    // key, decay or write strength that is not finite.
+    auto prepare = [&](int buf, bool &far, bool &apart, int &stop) {
         // the lane made opaque: the many addresses derived from it are formed
         // where they are used instead of being kept (and spilled) across chunks
         const int lane = opaque_lane(lane0);
@@ -749,6 +766,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         }
         far = __ballot(steep) != 0;  // the same in every wavefront
         apart = far | (__ballot(deep) != 0);
+        stop = kPreC;
         // m and G_32 - m in fixed point (the first wavefront's)
         i4 first_i = {0, 0, 0, 0}, second_i = first_i;
         // the factor of token i of this lane's: keys, queries and their inverse
@@ -827,6 +845,19 @@ void kda_prefill_kernel(DeltaProblem p) {
                     *reinterpret_cast<f4 *>(op + L::SQ + at) = now.q[i].all() * p.scale;
                 *reinterpret_cast<f4 *>(op + L::SA + at) = exp2(now.g[i] * kLog2E);
             }
+            int mine = pw == 3 && lane < kPreC && !finite(now.beta) ? lane : kPreC;
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                const f4 k = now.k[i].all();
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    bad |= !finite(k[e]) | !(now.g[i][e] < __builtin_inff());
+                mine = min(mine, bad ? tok + i : kPreC);
+            }
+#pragma unroll
+            for (int d = 1; d < kWave; d *= 2) mine = min(mine, __shfl_xor(mine, d));
+            reinterpret_cast<int *>(op + L::STOP)[pw] = mine;
         }
         if (pw == 0 && grp == 0) {
             const f4 one = {1.0f, 1.0f, 1.0f, 1.0f};
@@ -835,8 +866,8 @@ void kda_prefill_kernel(DeltaProblem p) {
             *reinterpret_cast<f4 *>(fac + L::EG + 4 * ch) = exp2(owed_i);
             *reinterpret_cast<f4 *>(fac + L::EF + 4 * ch) = exp2(first + second);
         }
-        if (ROLES && pw == 0 && lane0 == 0)
-            reinterpret_cast<int *>(lds + L::FLAGS)[buf] = (far ? 1 : 0) | (apart ? 2 : 0);
+        if (ROLES && pw == 0 && lane0 == 0 && !far)  // (else below)
+            reinterpret_cast<int *>(lds + L::FLAGS)[buf] = (apart ? 2 : 0) | kPreC << 2;
         owed = far ? f4{0.0f, 0.0f, 0.0f, 0.0f} : second;
         owed_i = far ? i4{0, 0, 0, 0} : second_i;
         meet_all();
@@ -900,6 +931,13 @@ void kda_prefill_kernel(DeltaProblem p) {
             const float *sa = reinterpret_cast<const float *>(op + L::SA);
             float *sm = reinterpret_cast<float *>(op + L::SM);
             float *sp = reinterpret_cast<float *>(op + L::SP);
+            const int *stops = reinterpret_cast<const int *>(op + L::STOP);
+            stop = __builtin_amdgcn_readfirstlane(
+                min(min(stops[0], stops[1]), min(stops[2], stops[3])));
+            if (pw == 3 && lane >= stop && lane < kPreC)
+                reinterpret_cast<float *>(lds + L::BETA)[buf * kPreC + lane] = 0.0f;
+            if (ROLES && pw == 0 && lane == 0)
+                reinterpret_cast<int *>(lds + L::FLAGS)[buf] = 3 | stop << 2;
 #pragma unroll 1
             for (int j = pw; j < kPreC; j += kPreWaves) {
                 constexpr int CPL = K / kWave;  // channels per lane, 64 apart
@@ -928,13 +966,16 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int top = (4 * g4 + s) * kPreC + n16, low = top + 16 * kPreC;
-                if (pw < 2) m[0][s] = sm[pw == 0 ? top : low + 16];
+                // (L stops there, as if the tokens from there on were none)
+                if (pw < 2) {
+                    m[0][s] = 16 * pw + 4 * g4 + s < stop ? sm[pw == 0 ? top : low + 16] : 0.0f;
+                }
                 if (pw == 2) {
                     m[0][s] = sp[top];
                     m[1][s] = sp[low + 16];
                 }
                 if (pw == 3) {
-                    m[0][s] = sm[low];
+                    m[0][s] = 16 + 4 * g4 + s < stop ? sm[low] : 0.0f;
                     m[1][s] = sp[low];
                 }
             }
@@ -1110,7 +1151,7 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) vraw[I][s].load(rv, at + (16 * I + s) * vs);
     };
-    auto use = [&](int t0, int buf, bool far, bool apart) {
+    auto use = [&](int t0, int buf, bool far, bool apart, int stop) {
         const int len = min(kPreC, len_all - t0);
         const int lane = opaque_lane(lane0);
         const int g4 = lane >> 4, n16 = lane & 15;
@@ -1222,6 +1263,37 @@ void kda_prefill_kernel(DeltaProblem p) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) R[I][ct][s] = vraw[I][s].at(ct) - kS[I][ct][s];
         if (ROLES && t0 + kPreC < len_all) load_values(t0 + kPreC);
+        // A value that is not finite may only reach its column's outputs from its
+        // token on, but the products with zeros above the diagonals would take it
+        // to earlier ones: the column is then without tokens from there on, and
+        // its outputs from there on and its state are NaN.
+        int first[CT];
+        bool broken = stop < kPreC;
+        if constexpr (!SUM) {
+            float most = 0.0f;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) most = largest(largest(most, R[0][ct]), R[1][ct]);
+            broken |= __ballot(!finite(most)) != 0;
+            if (broken) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    first[ct] = stop;
+#pragma unroll
+                    for (int I = 0; I < 2; ++I)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (!finite(R[I][ct][s]))
+                                first[ct] = min(first[ct], 16 * I + 4 * g4 + s);
+                    first[ct] = min(first[ct], __shfl_xor(first[ct], 16));
+                    first[ct] = min(first[ct], __shfl_xor(first[ct], 32));
+#pragma unroll
+                    for (int I = 0; I < 2; ++I)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (16 * I + 4 * g4 + s >= first[ct]) R[I][ct][s] = 0.0f;
+                }
+            }
+        }
         Operand u[CT];
         {
             const auto x0 = top_operand(L::TM);
@@ -1251,6 +1323,14 @@ void kda_prefill_kernel(DeltaProblem p) {
             if constexpr (!SUM) mul_columns<CT>(p1, u, o[1]);
         }
         if constexpr (!SUM) {
+            if (broken)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int I = 0; I < 2; ++I)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (16 * I + 4 * g4 + s >= first[ct]) o[I][ct][s] = __builtin_nanf("");
             const Rsrc ro = rows_of(ob + (long)t0 * os, os, p.V * OE, len);
             const uint32_t at = 4 * g4 * os + col * OE;
 #pragma unroll
@@ -1303,6 +1383,14 @@ void kda_prefill_kernel(DeltaProblem p) {
             interleave<6 * CT, 1>();
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (broken)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                if (SUM || first[ct] < kPreC)
+#pragma unroll
+                    for (int rt = 0; rt < NT; ++rt)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) S[rt][ct][s] = __builtin_nanf("");
     };
 
     // ======== the walk over the chunks
@@ -1322,8 +1410,9 @@ void kda_prefill_kernel(DeltaProblem p) {
             for (int t0 = 0, buf = 0; t0 < len_all; t0 += kPreC, buf ^= 1) {
                 const bool more = t0 + kPreC < len_all;
                 bool far, apart;
+                int stop;
                 if (more) load_rows(t0 + kPreC, next);
-                prepare(buf, far, apart);
+                prepare(buf, far, apart, stop);
                 if (more) {
                     now = next;
                     sum_decays(buf ^ 1);
@@ -1347,7 +1436,7 @@ void kda_prefill_kernel(DeltaProblem p) {
         for (int t0 = 0, buf = 0; t0 < len_all; t0 += kPreC, buf ^= 1) {
             const int flags = __builtin_amdgcn_readfirstlane(
                 reinterpret_cast<const int *>(lds + L::FLAGS)[buf]);
-            if (cols) use(t0, buf, flags & 1, flags & 2);
+            if (cols) use(t0, buf, flags & 1, flags & 2, flags >> 2);
             __syncthreads();
         }
     } else {
@@ -1355,17 +1444,18 @@ void kda_prefill_kernel(DeltaProblem p) {
         if (len_all > 0) load_rows(0, now);
         for (int t0 = 0; t0 < len_all; t0 += kPreC) {
             bool far, apart;
+            int stop;
             // The other workgroup of the compute unit gives way to a walk (8 x 2,048
             // tokens: 628 -> 598 us; K = 64, with three workgroups: 163 -> 170 us).
             if (K == 128) __builtin_amdgcn_s_setprio(0);
             sum_decays(0);
             __syncthreads();  // totals; nothing reads the chunk before any more
-            prepare(0, far, apart);
+            prepare(0, far, apart, stop);
             if (cols) load_values(t0);
             __syncthreads();
             if (K == 128) __builtin_amdgcn_s_setprio(2);
             if (t0 + kPreC < len_all) load_rows(t0 + kPreC, now);
-            if (cols) use(t0, 0, far, apart);
+            if (cols) use(t0, 0, far, apart, stop);
         }
         if (len_all > 0) {
             if (pw == 0 && lane0 < K / 4)
