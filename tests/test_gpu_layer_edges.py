@@ -144,3 +144,20 @@ def test_values_that_are_not_finite(kt, form, K, dtype, what, value):
                                         [at], c["state"][r:r + 1, h:h + 1], None, None, K ** -0.5)
             half = torch.finfo(gh.out_torch_dtype(dtype)).eps / 2
             assert (np.abs(out[s, h:h + 1] - want) <= 4e-6 * N + half * np.abs(want)).all()
+
+
+def test_pools_without_slots_are_refused(kt):
+    """They have no address in torch, and would pass for no pool at all: the
+    requests' new state would be lost. No request needs none."""
+    q, x = torch.ones((4, 2, 64), device=DEV), torch.ones((4, 2), device=DEV)
+    cu = _dev(np.array([0, 4], np.int32))
+    none = _dev(np.array([0], np.int32))
+    S, win = torch.empty((0, 2, 64, 64), device=DEV), torch.empty((0, 3, 2, 3, 64), device=DEV)
+    for fn in (kt.prefill, kt.recurrent):
+        with pytest.raises(ValueError, match="slots"):
+            fn(q, q, q, q, x, cu, state=S)
+        assert fn(q[:0], q[:0], q[:0], q[:0], x[:0], none, state=S).shape == (0, 2, 64)
+    qkv, cw = torch.ones((4, 3, 2, 64), device=DEV), torch.ones((3, 4, 2, 64), device=DEV)
+    with pytest.raises(ValueError, match="slots"):
+        kt.conv_prefill(qkv, cw, cu, conv_state=win)
+    assert kt.conv_prefill(qkv[:0], cw, none, conv_state=win)[0].shape == (0, 2, 64)

@@ -172,6 +172,8 @@ def kda_conv_prefill(qkv, conv_w, q, k, v, cu_seqlens=None, conv_state=None, slo
         if windows[1:] != (3, H, W - 1, d):
             _bad("conv_state must be [slots, 3, H, W - 1, d]")
         slots = windows[0]
+        if slots == 0 and n > 0:  # (torch gives it no address: it would pass for no pool)
+            _bad("conv_state has no slots")
     fn = _lib.kda_conv_prefill_dense if cu_seqlens is None else _lib.kda_conv_prefill_packed
     _check(fn(qkv.data_ptr(), _code(qkv), conv_w.data_ptr(), q.data_ptr(), k.data_ptr(),
               v.data_ptr(), *req, H, d, W, _addr(conv_state), _addr(slot), _addr(init), slots,
@@ -215,6 +217,8 @@ def _delta_args(q, k, v, g, beta, out, cu_seqlens, state, slot, init, scale, str
         if states[1:] != (H, K, V):
             _bad("state must be [slots, H, K, V]")
         slots = states[0]
+        if slots == 0 and n > 0:
+            _bad("state has no slots")
     if scale is None:
         scale = K ** -0.5
     return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), _code(q), g.data_ptr(), beta.data_ptr(),
