@@ -104,6 +104,11 @@ kda_status check_delta(DeltaProblem &p, const DeltaArgs &a, const int32_t *cu, i
     if (num_seqs > kMaxPairs / a.H) return KDA_ERR_UNSUPPORTED;
     st = check_pool(p.pool, a.state, a.slot, a.init, a.num_slots, num_seqs);
     if (st != KDA_OK) return st;
+    const Span pool = {a.state, p.pool.base ? (size_t)a.num_slots * a.H * a.K * a.V * 4 : 0};
+    const Span lists[] = {{cu, (size_t)(num_seqs + 1) * 4},
+                          {a.slot, (size_t)num_seqs * 4},
+                          {a.init, (size_t)num_seqs * 4}};
+    if (overlaps_any(pool, lists)) return KDA_ERR_INVALID_ARG;
     if (tokens > 0) {
         if (!a.q || !a.k || !a.v || !a.g || !a.beta || !a.out) return KDA_ERR_INVALID_ARG;
         if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.g, 16) ||
@@ -112,10 +117,8 @@ kda_status check_delta(DeltaProblem &p, const DeltaArgs &a, const int32_t *cu, i
         const size_t T = (size_t)tokens, e = dtype_bytes(a.in_dtype);
         const Span in[] = {{a.q, T * a.Hk * a.K * e},       {a.k, T * a.Hk * a.K * e},
                            {a.v, T * a.H * a.V * e},        {a.g, T * a.H * a.gate_dim * 4},
-                           {a.beta, T * (size_t)a.H * 4},   {cu, (size_t)(num_seqs + 1) * 4},
-                           {a.slot, (size_t)num_seqs * 4},  {a.init, (size_t)num_seqs * 4}};
+                           {a.beta, T * (size_t)a.H * 4},   lists[0], lists[1], lists[2]};
         const Span out = {a.out, T * a.H * a.V * dtype_bytes(a.out_dtype)};
-        const Span pool = {a.state, p.pool.base ? (size_t)a.num_slots * a.H * a.K * a.V * 4 : 0};
         if (overlaps_any(out, in) || overlap(out, pool) || overlaps_any(pool, in))
             return KDA_ERR_INVALID_ARG;
     }
@@ -204,18 +207,18 @@ kda_status conv(const void *qkv, kda_dtype dtype, const float *conv_w, void *q, 
     if (st != KDA_OK) return st;
     if (num_seqs == 0 || (tokens == 0 && conv_state == nullptr)) return KDA_OK;
     if (!conv_w || !aligned(conv_w, 16)) return KDA_ERR_INVALID_ARG;
+    const Span pool = {conv_state, p.pool.base ? (size_t)num_slots * 3 * H * (W - 1) * d * 4 : 0};
+    const Span kept[] = {{conv_w, (size_t)3 * W * H * d * 4},
+                         {cu, (size_t)(num_seqs + 1) * 4},
+                         {slot, (size_t)num_seqs * 4},
+                         {init, (size_t)num_seqs * 4}};
+    if (overlaps_any(pool, kept)) return KDA_ERR_INVALID_ARG;
     if (tokens > 0) {
         if (!qkv || !q || !k || !v) return KDA_ERR_INVALID_ARG;
         if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
             return KDA_ERR_INVALID_ARG;
         const size_t each = (size_t)tokens * H * d * dtype_bytes(dtype);
-        const Span in[] = {{qkv, 3 * each},
-                           {conv_w, (size_t)3 * W * H * d * 4},
-                           {cu, (size_t)(num_seqs + 1) * 4},
-                           {slot, (size_t)num_seqs * 4},
-                           {init, (size_t)num_seqs * 4}};
-        const Span pool = {conv_state,
-                           conv_state ? (size_t)num_slots * 3 * H * (W - 1) * d * 4 : 0};
+        const Span in[] = {{qkv, 3 * each}, kept[0], kept[1], kept[2], kept[3]};
         const Span out[] = {{q, each}, {k, each}, {v, each}};
         for (const Span &o : out)
             if (overlaps_any(o, in) || overlap(o, pool)) return KDA_ERR_INVALID_ARG;
