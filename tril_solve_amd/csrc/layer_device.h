@@ -13,17 +13,12 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 typedef uint32_t w2 __attribute__((ext_vector_type(2)));
 typedef uint32_t w4 __attribute__((ext_vector_type(4)));
 
-// N consecutive elements widened to float (exact) and back (round to nearest
-// even); p is aligned to the N elements (16 bytes at most).
+// Elements widened to float (exact) and pairs packed back (round to nearest even).
 template <class E>
 struct Elem;
 template <>
 struct Elem<F32> {
     static __device__ __forceinline__ float one(const float *p) { return *p; }
-    static __device__ __forceinline__ f2 two(const float *p) {
-        return *reinterpret_cast<const f2 *>(p);
-    }
-    static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 };
 template <>
 struct Elem<BF16> {
@@ -34,13 +29,6 @@ struct Elem<BF16> {
         return __builtin_bit_cast(uint32_t, v);
     }
     static __device__ __forceinline__ float one(const uint16_t *p) { return widen(*p); }
-    static __device__ __forceinline__ f2 two(const uint16_t *p) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-        return f2{__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xFFFF0000u)};
-    }
-    static __device__ __forceinline__ void put(uint16_t *p, float v) {
-        *p = __builtin_bit_cast(uint16_t, (__bf16)v);
-    }
 };
 template <>
 struct Elem<F16> {
@@ -53,13 +41,6 @@ struct Elem<F16> {
         return __builtin_bit_cast(uint32_t, v);
     }
     static __device__ __forceinline__ float one(const uint16_t *p) { return widen(*p); }
-    static __device__ __forceinline__ f2 two(const uint16_t *p) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-        return f2{widen(w & 0xFFFFu), widen(w >> 16)};
-    }
-    static __device__ __forceinline__ void put(uint16_t *p, float v) {
-        *p = __builtin_bit_cast(uint16_t, (_Float16)v);
-    }
 };
 
 // Eight consecutive elements (16 or 32 bytes, 16-byte aligned).
