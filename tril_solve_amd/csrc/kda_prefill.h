@@ -586,7 +586,7 @@ void kda_prefill_kernel(DeltaProblem p) {
     const int col = (cols ? map ? col0 - p.V : col0 : 0) + CT * (lane0 & 15);
 
     // Token tensors from the request's first row and this head on, and the
-    // bytes between their rows (fewer than 2^21).
+    // bytes between their rows (at most 2^22: 32 rows' offsets fit 32 bits).
     const long first_k = (row_first * p.Hk + hk) * K;
     const long first_v = (row_first * p.H + h) * p.V;
     const int gd = p.gate_stride;
@@ -1447,13 +1447,13 @@ void kda_prefill_kernel(DeltaProblem p) {
             int stop;
             // The other workgroup of the compute unit gives way to a walk (8 x 2,048
             // tokens: 628 -> 598 us; K = 64, with three workgroups: 163 -> 170 us).
-            if (K == 128) __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_s_setprio(0);
             sum_decays(0);
             __syncthreads();  // totals; nothing reads the chunk before any more
             prepare(0, far, apart, stop);
             if (cols) load_values(t0);
             __syncthreads();
-            if (K == 128) __builtin_amdgcn_s_setprio(2);
+            __builtin_amdgcn_s_setprio(2);
             if (t0 + kPreC < len_all) load_rows(t0 + kPreC, now);
             if (cols) use(t0, 0, far, apart, stop);
         }
