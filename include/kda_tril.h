@@ -341,8 +341,9 @@ kda_status kda_tril_inv_packed_noalloc(const void *A, kda_dtype a_dtype, void *X
  *
  * Types: token tensors of in_dtype (out of out_dtype), decays, write
  * strengths, taps, norm weights and pools FP32. All pointers 16-byte aligned
- * but int32 arrays, beta and norm_w (4 bytes). Outputs must not overlap
- * inputs or pools. As above, nothing is allocated, copied or synchronised.
+ * but int32 arrays, beta and norm_w (4 bytes; the chunk_indices that
+ * kda_chunk_map writes 8). Outputs and pools must not overlap inputs or each
+ * other. As above, nothing is allocated, copied or synchronised.
  */
 
 /*
@@ -428,8 +429,8 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  * that run side by side (the results agree to rounding with those of one
  * piece). The size is 0 where that would not pay: for more than 64 (request,
  * head, 128 value columns) triples or 64 requests, or fewer than 512 tokens
- * per request on average (1,280 with more than 32 triples). With a smaller one, or none (NULL, 0), each request
- * runs in one piece. 16-byte aligned, overlapping no other argument; its
+ * per request on average (1,280 with more than 32 triples). With a smaller one,
+ * or none (NULL, 0), each request runs in one piece. 16-byte aligned, overlapping no other argument; its
  * contents need not be kept; concurrent calls (and captured graphs that may
  * replay at once) need different ones.
  */

@@ -10,8 +10,8 @@
 // 16-byte access of 16-bit elements) and walks `seg` tokens of the packed
 // batch with the last W - 1 inputs in registers, so a segment reads W - 1
 // rows besides its own. The norms are DPP sums over the d / 8 lanes of a head.
-// 16 x 512 tokens, 64 heads of 128, W = 4, bf16: 150 us, 5.4 TB/s of its 805 MB
-// (a copy reaches 5.1); 64 tokens: 6.5 us, a launch and two dependent loads.
+// 16 x 512 tokens, 64 heads of 128, W = 4, bf16: 148 us, 5.4 TB/s of its 805 MB
+// (a tuned copy reaches 6.4); 64 tokens: 6.5 us, a launch and two dependent loads.
 //
 // The window of a request is read and written by the wavefront whose segment
 // holds the request's first token, in that order and each channel by one

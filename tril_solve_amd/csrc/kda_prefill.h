@@ -51,19 +51,18 @@
 //     middle lose between them (state 1.6e-6 off, then 4e-7).
 //
 // Two forms. With many workgroups, four wavefronts prepare a chunk and then
-// walk their columns through it, two workgroups to a compute unit (74 KB of
+// walk their columns through it, two workgroups to a compute unit (79 KB of
 // LDS each). With at most 256, wavefronts of either kind work side by side, one
-// chunk apart, on twice the LDS: 64 walks of 2,048 tokens 363 -> 271 us, 32
-// of 16,384 tokens 2.86 -> 2.09 ms; but 1,024 walks of 512 tokens, four rounds
-// of workgroups whose beginnings and ends nothing covers, 313 -> 335 us.
+// chunk apart, on twice the LDS: 64 walks of 2,048 tokens 567 -> 416 us, 32
+// of 16,384 tokens 4.47 -> 3.23 ms; but 1,024 walks of 512 tokens, four rounds
+// of workgroups whose beginnings and ends nothing covers, 453 -> 465 us.
 //
 // What bounds it: instruction issue and, with all units at work, power (1.6 to
-// 1.8 of 2.4 GHz). A wavefront's chunk is about 300 matrix instructions and
-// 1,400 vector instructions, 16 and 4 cycles each, most of them the splits into
-// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 354 us: 2.5 TB/s
-// of the 5.1 that a copy reaches, 0.9 of 2.5 PFLOP/s of the products as run.
-// (Figures at rules and forms were taken with three products for L and
-// (k e^G) S; both sides have grown since.)
+// 1.8 of 2.4 GHz). A wavefront's chunk is 384 matrix instructions and 2,020
+// vector instructions, 16 and 4 cycles each, most of them the splits into
+// parts; 16 x 512 tokens of 64 heads, K = V = 128, bf16, take 432 to 470 us on
+// three cards: 2.0 TB/s of the 6.4 that a tuned copy reaches, 0.95 of 2.5 PFLOP/s of
+// the products as run.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -1220,8 +1219,8 @@ void kda_prefill_kernel(DeltaProblem p) {
             }
         }
         // (no room for the next operands beside 32 columns and the preparation's
-        // registers, 16 x 512 tokens 400 -> 383 us, or with three wavefronts to a
-        // SIMD)
+        // registers, 16 x 512 tokens 552 -> 470 us, or with three wavefronts to a
+        // SIMD; elsewhere 1 to 2% faster)
         constexpr bool kNext = K == 64 || (!SUM && (ROLES || CT == 1));
         read_em(0);
         read_rows(0);
@@ -1396,8 +1395,8 @@ void kda_prefill_kernel(DeltaProblem p) {
     // ======== the walk over the chunks
     if constexpr (ROLES) {
         if (prepares) {
-            // (16,384 tokens on 32 workgroups: 2.19 -> 2.09 ms; with eight other
-            // wavefronts they would wait: 681 -> 720 us cut)
+            // (16,384 tokens, 32 heads, cut: 900 -> 890 us; in the sums, too, where
+            // eight other wavefronts would wait: 914 us)
             if (!SUM) __builtin_amdgcn_s_setprio(2);
             Rows next;
             next.beta = 0.0f;
@@ -1446,7 +1445,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             bool far, apart;
             int stop;
             // The other workgroup of the compute unit gives way to a walk (8 x 2,048
-            // tokens: 628 -> 598 us; K = 64, with three workgroups: 163 -> 170 us).
+            // tokens, 64 heads: 922 -> 865 us; 16 x 512, K = 64: 282 -> 267 us).
             __builtin_amdgcn_s_setprio(0);
             sum_decays(0);
             __syncthreads();  // totals; nothing reads the chunk before any more
@@ -1496,10 +1495,10 @@ hipError_t launch_prefill_of(const DeltaProblem &p, PrePass pass, hipStream_t st
         return hipGetLastError();
     };
     // Columns of 16 to a wavefront halve its part of a chunk: while that still
-    // takes at most a workgroup per compute unit (64 walks of 64 tokens 15.8 ->
-    // 12.8 us, 128 walks of 300 tokens 51 -> 44 us), and for up to 64 columns in
+    // takes at most a workgroup per compute unit (64 walks of 64 tokens 21.2 ->
+    // 17.5 us, 128 walks of 300 tokens 76 -> 64 us), and for up to 64 columns in
     // all, which 32 to a wavefront would leave to two of four wavefronts (1,024
-    // walks of 512 tokens, K = 128, V = 64, 266 -> 247 us; K = V = 64 195 and 197).
+    // walks of 512 tokens, K = 128, V = 64, 358 -> 330 us; K = V = 64 236 -> 193).
     auto with_out = [&]<int K, int OUT>() {
         // FP32 rows on their way leave a wavefront that does both without
         // registers: it spills (f32, 40 requests of 1 to 2,000 tokens, 16 heads

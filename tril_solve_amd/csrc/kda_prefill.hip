@@ -95,23 +95,28 @@ hipError_t launch_pass(const DeltaProblem &p, int in_dt, PrePass pass, hipStream
 
 }  // namespace
 
+// MI355X's compute units. The rules below and the workspace query, which runs
+// without a device, have to agree.
+constexpr int64_t kUnits = 256;
+
 // A request's walk over its chunks is serial, so a few (request, head, 128
-// columns) workgroups leave most of the 256 compute units idle; a cut prompt
-// takes the chunks of its segments at once, for about twice the work: 32 walks
-// of 16,384 tokens 1,880 -> 660-780 us, of 768 tokens 89 -> 76 us, 64 walks of
-// 2,048 tokens 224 -> 199 us; but 8 walks of 512 tokens 58 and 58, 64 walks of
-// 1,024 tokens 117 -> 120 us, 96 walks of 4,096 tokens 534 -> 555 us.
+// columns) workgroups leave most compute units idle; a cut prompt takes the
+// chunks of its segments at once, for about twice the work: 32 walks of 16,384
+// tokens 2,440 -> 870 us, of 768 tokens 121 -> 91 us, of 512 tokens 82 -> 72 us, 64
+// walks of 2,048 tokens 312 -> 253 us, of 1,280 tokens 198 -> 169 us; but of 1,024
+// tokens 160 and 154 us, 96 walks of 2,048 tokens 313 -> 376 us.
 int32_t prefill_segments(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t V) {
     const int64_t walks = num_seqs * H * column_blocks<2>(V);
     const int64_t chunks = total_tokens / kPreC;
     if (num_seqs < 1 || num_seqs > kMaxCutRequests || walks > 64 ||
         chunks < (walks > 32 ? 40 : 16) * num_seqs)
         return 0;
-    const int64_t parts = 256 * num_seqs / walks;  // a workgroup per compute unit
+    const int64_t parts = kUnits * num_seqs / walks;  // a workgroup per compute unit
     int64_t seg = (chunks + parts - 1) / parts;
-    // A chunk more per segment takes 7 us of both passes, a segment more 2.3 us
-    // of the walk over them: at least four chunks, and about the square root of
-    // a third of a request's.
+    // A chunk more per segment takes 11 us of both passes, a segment more 2 us of
+    // the walk over them: at least four chunks, and about the square root of a
+    // third of a request's (one request of 512 chunks, 2 heads: 9 chunks a segment
+    // 235 us, 13 242 us, 18 274 us, 26 342 us).
     while (seg < 4 || 3 * seg * seg * num_seqs < chunks) ++seg;
     return (int32_t)(kPreC * seg);
 }
@@ -129,12 +134,12 @@ hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream) 
         if (e != hipSuccess) return e;
     }
     // Up to a workgroup per compute unit (of the segments, p.segs - num_seqs at
-    // least exist): 256 walks of 512 tokens 82 us with roles and 102 without,
-    // 320 walks 148 and 139, 1,024 walks 350 and 329 (K = 128, bf16).
+    // least exist): 256 walks of 512 tokens 127 us with roles and 152 without,
+    // 320 walks 221 and 190, 1,024 walks 465 and 453 (K = 128, bf16).
     const int64_t parts = p.seg != 0 ? p.segs - p.req.num_seqs : p.req.num_seqs;
     const int64_t walks = parts * p.H;
-    const PrePass pass = walks * column_blocks<1>(p.V) <= 256   ? PrePass::narrow
-                         : walks * column_blocks<2>(p.V) <= 256 ? PrePass::roles
+    const PrePass pass = walks * column_blocks<1>(p.V) <= kUnits   ? PrePass::narrow
+                         : walks * column_blocks<2>(p.V) <= kUnits ? PrePass::roles
                                                                 : PrePass::whole;
     return launch_pass(p, in_dt, pass, stream);
 }
