@@ -430,9 +430,9 @@ kda_status kda_conv_prefill_dense(const void *qkv, kda_dtype dtype, const float 
  * piece). The size is 0 where that would not pay: for more than 64 (request,
  * head, 128 value columns) triples or 64 requests, or fewer than 512 tokens
  * per request on average (1,280 with more than 32 triples). With a smaller one,
- * or none (NULL, 0), each request runs in one piece. 16-byte aligned, overlapping no other argument; its
- * contents need not be kept; concurrent calls (and captured graphs that may
- * replay at once) need different ones.
+ * or none (NULL, 0), each request runs in one piece. 16-byte aligned,
+ * overlapping no other argument; its contents need not be kept; concurrent calls
+ * (and captured graphs that may replay at once) need different ones.
  */
 kda_status kda_prefill_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H, int32_t K,
                                       int32_t V, size_t *bytes);

@@ -106,7 +106,8 @@ def _delta(kt, form, c, requests, T, dtype, cut=False, **_):
 
 
 @pytest.mark.parametrize("what,value", [("v", np.nan), ("v", np.inf), ("v", -np.inf),
-                                        ("k", np.nan), ("k", np.inf), ("beta", np.nan),
+                                        ("k", np.nan), ("k", np.inf), ("k", -np.inf),
+                                        ("beta", np.nan), ("beta", np.inf), ("beta", -np.inf),
                                         ("g", np.nan), ("g", np.inf), ("q", np.nan)])
 @pytest.mark.parametrize("K,dtype", [(128, "bf16"), (64, "f32")])
 @pytest.mark.parametrize("form", list(_FORMS))
@@ -125,7 +126,8 @@ def test_values_that_are_not_finite(kt, form, K, dtype, what, value):
             c[what][row, h, 3] = value
         out, S = _delta(kt, form, c, T=T, dtype=dtype, **f)
         hit = np.zeros(out.shape, bool)  # what has to be not finite
-        hit[row:row + 1 if what == "q" else (r + 1) * T, h, 3 if what == "v" else slice(None)] = True
+        last = row + 1 if what == "q" else (r + 1) * T
+        hit[row:last, h, 3 if what == "v" else slice(None)] = True
         assert not np.isfinite(out[hit]).any()
         hit_S = np.zeros(S.shape, bool)
         if what != "q":
@@ -161,3 +163,31 @@ def test_pools_without_slots_are_refused(kt):
     with pytest.raises(ValueError, match="slots"):
         kt.conv_prefill(qkv, cw, cu, conv_state=win)
     assert kt.conv_prefill(qkv[:0], cw, none, conv_state=win)[0].shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("steep", [False, True])
+@pytest.mark.parametrize("form", list(_FORMS))
+def test_several_values_that_are_not_finite(kt, form, steep):
+    """Two values in one chunk, a key between and after them, decays that reset
+    channels beside: each column is left exact up to its first one."""
+    f = _FORMS[form]
+    T, K, V, h, dtype = 530 if f.get("cut") else 70, 64, 96, 0, "f32"
+    c = _problem(f["requests"], f["H"], K, V, dtype, T, 9)
+    if steep:
+        c["g"] *= 100.0
+        c["g"][::7, :, ::5] = -np.inf
+    b = T - 40 if f.get("cut") else 32  # first token of a chunk (cut: somewhere in the last)
+    c["v"][b + 9, h, 7], c["v"][b + 20, h, 3], c["v"][b + 1, h, 95] = np.inf, np.nan, -np.inf
+    c["k"][b + 14, h, 0], c["k"][b + 25, h, 5] = np.nan, np.inf
+    out, S = _delta(kt, form, c, T=T, dtype=dtype, **f)
+    stop = np.full(V, b + 14)
+    stop[7], stop[95] = b + 9, b + 1
+    part = lambda x: c[x][:b + 14, h:h + 1]  # noqa: E731
+    clean = np.where(np.isfinite(part("v")), part("v"), 0.0)
+    want, _, N = ref.delta_rule(part("q"), part("k"), clean, part("g"), part("beta"), [b + 14],
+                                c["state"][:1, h:h + 1], None, None, K ** -0.5)
+    for col in range(V):
+        n = stop[col]
+        assert not np.isfinite(out[n:T, h, col]).any()
+        assert (np.abs(out[:n, h, col] - want[:n, 0, col]) <= 4e-6 * N).all()
+    assert not np.isfinite(S[0, h]).any() and np.isfinite(S[0, 1:]).all()

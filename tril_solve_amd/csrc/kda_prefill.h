@@ -681,7 +681,7 @@ void kda_prefill_kernel(DeltaProblem p) {
             }
             // a key or write strength that is not finite shows in the totals
             // (and the chunk takes the steep path, which looks for its token)
-            float most = pw == 3 ? now.beta : 0.0f;
+            float most = pw == 3 ? __builtin_fabsf(now.beta) : 0.0f;
 #pragma unroll
             for (int i = 0; i < TPL; ++i) most = largest(most, now.k[i].all());
             x[0] = __builtin_fmaf(most, 0.0f, x[0]);
@@ -1196,7 +1196,8 @@ void kda_prefill_kernel(DeltaProblem p) {
             const int at = 16 * (j & 1) * L::RS;
             ka_op[j & 1] = row_operand.template operator()<Operand>(L::KR + at, j >> 1);
             if constexpr (!SUM)
-                qa_op[j & 1] = row_operand.template operator()<typename L::Queries>(L::QR + at, j >> 1);
+                qa_op[j & 1] =
+                    row_operand.template operator()<typename L::Queries>(L::QR + at, j >> 1);
         };
         auto read_em = [&](int kk) {
 #pragma unroll
