@@ -476,6 +476,137 @@ kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, cons
                           void *out, kda_dtype out_dtype, int64_t rows, int32_t H,
                           int32_t head_dim, float eps_norm, hipStream_t stream);
 
+/*
+ * The layer's backward pass: the gradients of kda_prefill_*, kda_conv_prefill_*
+ * and kda_gated_norm, and activation checkpoints in 8 bits, which the latter
+ * two take in the place of their inputs. All gradients are written, none is
+ * added to; they have the same bits on every call. Requests, rows outside every
+ * request (neither read nor written), padding entries (their rows' gradients are
+ * 0 and no pool is touched) and alignment are as in the forward calls, with
+ * pointers to codes 8-byte aligned, to scales 4.
+ *
+ * Pools: `state` / `conv_state` as the forward call found it (it updates its
+ * pool in place, so a caller that continues requests keeps a copy), only read;
+ * `dstate` / `dconv_state`, of the same shape and slots, holds the gradient of
+ * every request's new state before the call and of its old one after it (zeros
+ * where init is 0). So the parts of a long sequence run forwards through one
+ * pool and backwards through the other. Either may be NULL: requests start from
+ * zeros, or nothing is known of the new state's gradient (0) and the old one's
+ * is not kept. slot, init and num_slots belong to both; with slot given, entries
+ * outside the pools are padding whenever there is a pool.
+ *
+ * workspace: at least the bytes that the call's workspace query asks for
+ * (KDA_ERR_WORKSPACE otherwise), 16-byte aligned, overlapping no other argument;
+ * its contents need not be kept; concurrent calls (and captured graphs that may
+ * replay at once) need different ones.
+ */
+
+/*
+ * Gradients of kda_prefill_* (and of kda_recurrent_*, the same function), from
+ * its inputs and the gradient of its output:
+ *   dout        [T, H, V] of out_dtype.
+ *   dq, dk      [T, Hk, K], dv [T, H, V] of in_dtype (of shared key heads: the
+ *               sum over the heads that read them).
+ *   dg          FP32, g's shape; dbeta FP32 [T, H].
+ * The same limits on K, V, Hk and gate_dim; at most 2^24 - 1 chunk slots x heads,
+ * chunk slots = total_tokens / 64 + num_seqs, else KDA_ERR_UNSUPPORTED. All
+ * arithmetic is FP32. Any decay is taken exactly, from e^0 to e^-inf (whose
+ * gate's gradient is 0).
+ *
+ * The states are computed again, one for every 64 tokens, and lie in the
+ * workspace with what else passes between the launches: 402 KB for each chunk
+ * slot and head with K = V = 128.
+ *
+ * A value that is not finite reaches the gradients of its request and head (and
+ * of those that share its key head), as NaN or infinities; no other request's.
+ */
+kda_status kda_prefill_backward_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H,
+                                               int32_t Hk, int32_t K, int32_t V, size_t *bytes);
+
+kda_status kda_prefill_backward_packed(
+    const void *dout, kda_dtype out_dtype, const void *q, const void *k, const void *v,
+    kda_dtype in_dtype, const float *g, const float *beta, void *dq, void *dk, void *dv, float *dg,
+    float *dbeta, const int32_t *cu_seqlens, int64_t num_seqs, int64_t total_tokens, int32_t H,
+    int32_t Hk, int32_t K, int32_t V, int32_t gate_dim, const float *state, float *dstate,
+    const int32_t *slot, const int32_t *init, int64_t num_slots, float scale, void *workspace,
+    size_t workspace_bytes, hipStream_t stream);
+
+kda_status kda_prefill_backward_dense(
+    const void *dout, kda_dtype out_dtype, const void *q, const void *k, const void *v,
+    kda_dtype in_dtype, const float *g, const float *beta, void *dq, void *dk, void *dv, float *dg,
+    float *dbeta, int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
+    int32_t gate_dim, const float *state, float *dstate, const int32_t *slot, const int32_t *init,
+    int64_t num_slots, float scale, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of kda_conv_prefill_*: dq, dk, dv [T, H, d] (of its outputs) and
+ * dqkv [T, 3, H, d] of dtype, dconv_w [3, W, H, d] FP32 (zeros for a call of no
+ * tokens). qkv is [T, 3, H, d] of dtype, or, where qkv_scale [T, 3, H] is given,
+ * the int8 codes of a checkpoint of it.
+ */
+kda_status kda_conv_backward_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H,
+                                            int32_t head_dim, int32_t conv_width, size_t *bytes);
+
+kda_status kda_conv_backward_packed(const void *dq, const void *dk, const void *dv,
+                                    kda_dtype dtype, const void *qkv, const float *qkv_scale,
+                                    const float *conv_w, void *dqkv, float *dconv_w,
+                                    const int32_t *cu_seqlens, int64_t num_seqs,
+                                    int64_t total_tokens, int32_t H, int32_t head_dim,
+                                    int32_t conv_width, const float *conv_state,
+                                    float *dconv_state, const int32_t *slot, const int32_t *init,
+                                    int64_t num_slots, float eps_l2, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+kda_status kda_conv_backward_dense(const void *dq, const void *dk, const void *dv, kda_dtype dtype,
+                                   const void *qkv, const float *qkv_scale, const float *conv_w,
+                                   void *dqkv, float *dconv_w, int64_t B, int64_t T, int32_t H,
+                                   int32_t head_dim, int32_t conv_width, const float *conv_state,
+                                   float *dconv_state, const int32_t *slot, const int32_t *init,
+                                   int64_t num_slots, float eps_l2, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of kda_gated_norm: dout (of its output), d_o and dz [rows, H, d] of
+ * dtype, dnorm_w [d] FP32 (zeros for a call of no rows). o and z are of dtype, or,
+ * where o_scale and z_scale [rows, H] are given (both or neither), the int8 codes
+ * of checkpoints of them.
+ */
+kda_status kda_gated_norm_backward_workspace_size(int64_t rows, int32_t H, int32_t head_dim,
+                                                  size_t *bytes);
+
+kda_status kda_gated_norm_backward(const void *dout, const void *o, const void *z, kda_dtype dtype,
+                                   const float *o_scale, const float *z_scale, const float *norm_w,
+                                   void *d_o, void *dz, float *dnorm_w, int64_t rows, int32_t H,
+                                   int32_t head_dim, float eps_norm, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits. Every vector of d channels is kept as int8
+ * codes and one FP32 scale:
+ *   scale = max |x| / 127,   code = x / scale to the nearest integer, halves to even
+ * (each value off by at most half a step, max |x| / 254). Vectors whose largest
+ * magnitude is below 2^-110 are kept as zeros; one that holds a value that is not
+ * finite gets a scale of NaN and reads back as NaN.
+ *   x       [rows, H, d] of dtype (of kda_conv_prefill's qkv: rows x 3, H).
+ *   codes   [rows, H, d] int8;  scale [rows, H] FP32.
+ * kda_checkpoint writes codes and scale, kda_checkpoint_load writes
+ * out = code x scale. kda_gated_norm_checkpoint is kda_gated_norm (the same bits)
+ * that also writes the checkpoints of o and z.
+ * head_dim 64 or 128, else KDA_ERR_UNSUPPORTED; rows x H < 2^28.
+ */
+kda_status kda_checkpoint(const void *x, kda_dtype dtype, int8_t *codes, float *scale,
+                          int64_t rows, int32_t H, int32_t head_dim, hipStream_t stream);
+
+kda_status kda_checkpoint_load(const int8_t *codes, const float *scale, void *out,
+                               kda_dtype out_dtype, int64_t rows, int32_t H, int32_t head_dim,
+                               hipStream_t stream);
+
+kda_status kda_gated_norm_checkpoint(const void *o, const void *z, kda_dtype in_dtype,
+                                     const float *norm_w, void *out, kda_dtype out_dtype,
+                                     int8_t *o_codes, float *o_scale, int8_t *z_codes,
+                                     float *z_scale, int64_t rows, int32_t H, int32_t head_dim,
+                                     float eps_norm, hipStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status s);
 

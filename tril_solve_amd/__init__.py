@@ -415,4 +415,12 @@ from .layer import (chunk_map, conv_prefill, gated_norm, kda_chunk_map,  # noqa:
                     kda_conv_prefill, kda_gated_norm, kda_prefill, kda_prefill_workspace_size,
                     kda_recurrent, prefill, prepare_prefill, prepare_recurrent, recurrent)
 
-EXPORTED += _layer.EXPORTED
+from . import backward as _backward  # noqa: E402
+from .backward import (checkpoint, checkpoint_load, conv_prefill_backward,  # noqa: E402,F401
+                       gated_norm_backward, gated_norm_checkpoint, kda_checkpoint,
+                       kda_checkpoint_load, kda_conv_backward, kda_conv_backward_workspace_size,
+                       kda_gated_norm_backward, kda_gated_norm_backward_workspace_size,
+                       kda_gated_norm_checkpoint, kda_prefill_backward,
+                       kda_prefill_backward_workspace_size, prefill_backward)
+
+EXPORTED += _layer.EXPORTED + _backward.EXPORTED

@@ -21,7 +21,9 @@ OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cpp", "plan.cpp", "launch_common.cpp", "tril_fused.hip", "tril_split.hip",
            "tril_small.hip", "tril_kkt.hip", "kda_decode.hip", "layer_api.cpp", "kda_map.hip",
            "kda_conv.hip", "kda_prefill.hip", "kda_prefill_f32.hip", "kda_prefill_bf16.hip",
-           "kda_prefill_f16.hip", "kda_recurrent.hip", "kda_norm.hip"]
+           "kda_prefill_f16.hip", "kda_recurrent.hip", "kda_norm.hip", "grad_api.cpp",
+           "kda_delta_grad_f32.hip", "kda_delta_grad_bf16.hip", "kda_delta_grad_f16.hip",
+           "kda_conv_grad.hip", "kda_norm_grad.hip", "kda_checkpoint.hip"]
 PROBE_SOURCES = ["bench_probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

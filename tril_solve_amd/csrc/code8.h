@@ -1,0 +1,79 @@
+// Vectors of d channels held in 8 bits: int8 codes and one FP32 scale, the
+// largest magnitude being 127 steps. Eight channels to a lane.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "layer_device.h"
+
+namespace kda {
+
+struct I8 {
+    typedef int8_t T;
+    static constexpr int kBytes = 1;
+};
+template <>
+struct Raw8<I8> {
+    w2 w;
+    __device__ __forceinline__ void load(const int8_t *p) { w = *reinterpret_cast<const w2 *>(p); }
+    __device__ __forceinline__ void load_stream(const int8_t *p) {
+        w = __builtin_nontemporal_load(reinterpret_cast<const w2 *>(p));
+    }
+    __device__ __forceinline__ void widen(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(w[i >> 2] >> 8 * (i & 3));
+    }
+    static __device__ __forceinline__ void store(int8_t *p, const int (&c)[8]) {
+        w2 o = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i >> 2] |= (uint32_t)(c[i] & 0xFF) << 8 * (i & 3);
+        *reinterpret_cast<w2 *>(p) = o;
+    }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float lane_max(float v) {
+    return __builtin_elementwise_maximum(
+        v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF,
+                                                              0xF, true)));
+}
+// The largest of L = 8 or 16 adjacent lanes, NaN where there is one.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    v = lane_max<0x141>(lane_max<0x4E>(lane_max<0xB1>(v)));
+    return L == 16 ? lane_max<0x140>(v) : v;
+}
+
+// Largest magnitudes below this are stored as zeros: their steps would leave
+// FP32's normal range.
+constexpr float kLeast8 = 0x1p-110f;
+
+// Codes of x and the vector's scale: the integer nearest x / scale, halves to
+// even, found exactly. x / scale is first taken by the reciprocal, off by less
+// than 2^-14, so the integer next to it is at most one off, where the quotient
+// is near a half; the remainder x - c scale of that integer is exact in FP32
+// (both are multiples of half the scale's last place, and it is near half
+// the scale) and says which side x is on. A vector that is not finite keeps a
+// scale of NaN and reads back as NaN.
+template <int L>
+__device__ __forceinline__ float encode8(const float (&x)[8], int (&c)[8]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __builtin_elementwise_maximum(top, __builtin_fabsf(x[i]));
+    top = lanes_max<L>(top);
+    const bool fine = top < __builtin_inff(), some = top >= kLeast8;
+    const float scale = top / 127.0f, inv = 127.0f / top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float n = __builtin_rintf(x[i] * inv);
+        const float r = 2.0f * __builtin_fmaf(-n, scale, x[i]);
+        const int odd = (int)n & 1;
+        int step = r > scale ? 1 : r < -scale ? -1 : 0;
+        if (r == scale) step = odd;
+        if (r == -scale) step = -odd;
+        c[i] = fine && some ? (int)n + step : 0;
+    }
+    return !fine ? __builtin_nanf("") : some ? scale : 0.0f;
+}
+
+}  // namespace kda

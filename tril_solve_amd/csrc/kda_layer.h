@@ -83,10 +83,105 @@ struct MapProblem {
     int32_t num_seqs, total_tokens, chunk, max_chunks;
 };
 
+// Gradients of the gated delta rule. Chunks have slots: chunk c of request n,
+// which starts at row b, has slot b / kGradChunk + n + c.
+constexpr int kGradChunk = 64;
+struct DeltaGradProblem {
+    Requests req;
+    Pool pool;           // states before the forward pass, [num_slots, H, K, V]
+    Pool grad;           // gradients of the states, in place (slot, init as in pool)
+    const void *q, *k;   // [T, Hk, K]
+    const void *v;       // [T, H, V]
+    const void *dout;    // [T, H, V]
+    const float *g;      // [T, H, K] or [T, H]
+    const float *beta;   // [T, H]
+    void *dq, *dk;       // [T, Hk, K]
+    void *dv;            // [T, H, V]
+    float *dg, *dbeta;   // [T, H, K] or [T, H]; [T, H]
+    int32_t H, Hk, K, V;
+    int32_t gate_stride;  // elements of g per (token, head): K or 1
+    int32_t slots;        // chunk slots of the workspace
+    float scale;
+    float *work;          // [slots, H] chunks of grad_chunk_floats
+    float *dq_head, *dk_head;  // [T, H, K] where key heads are shared, else null
+};
+inline int64_t grad_slots(int64_t total_tokens, int64_t num_seqs) {
+    return total_tokens / kGradChunk + num_seqs;
+}
+// A and its inverse, five operands of C x K, two of C x V, two states, decays.
+inline int64_t grad_chunk_floats(int32_t K, int32_t V) {
+    return (int64_t)2 * kGradChunk * kGradChunk + 5 * kGradChunk * K + 2 * kGradChunk * V +
+           2 * K * V + K;
+}
+
+struct CheckpointProblem {
+    const void *x;   // [vecs, d] to be stored, or null: to be read back
+    int8_t *codes;   // [vecs, d]
+    float *scale;    // [vecs]
+    void *out;       // [vecs, d], read back
+    int64_t vecs;
+    int32_t d;
+};
+struct NormCheckpointProblem {
+    NormProblem norm;
+    int8_t *o_codes, *z_codes;
+    float *o_scale, *z_scale;
+};
+struct NormGradProblem {
+    const void *dout, *o, *z;         // o, z: codes where o_scale is given
+    const float *o_scale, *z_scale;   // [rows, H] or null
+    const float *norm_w;
+    void *d_o, *dz;
+    float *dnorm_w;
+    float *part;  // [blocks, d]
+    int64_t vecs;
+    int32_t d;
+    float eps_norm;
+};
+// Workgroups of the norm's backward pass, each of which leaves a row of dnorm_w:
+// enough for every compute unit, and few rows to add.
+inline int64_t norm_grad_blocks(int64_t vecs, int32_t d) {
+    const int64_t per = 256 / (d / 8), need = (vecs + per - 1) / per;
+    return need < 2048 ? need : 2048;
+}
+
+struct ConvGradProblem {
+    Requests req;
+    Pool pool;            // windows before the forward pass, [num_slots, 3, H, W - 1, d]
+    Pool grad;            // gradients of the windows, in place
+    const void *dout[3];  // of q, k, v: [T, H, d]
+    const void *qkv;      // [T, 3, H, d], or codes where qkv_scale is given
+    const float *qkv_scale;  // [T, 3, H] or null
+    const float *conv_w;  // [3, W, H, d]
+    void *dqkv;           // [T, 3, H, d]
+    float *dconv_w;       // [3, W, H, d]
+    float *part;          // [rows, 3, W, H, d]
+    float *old;           // [num_seqs, 3, H, W - 1, d]
+    int32_t H, d, W;
+    int32_t seg;          // tokens per wavefront
+    float eps_l2;
+};
+// Rows of dconv_w that the workgroups (four segments each) leave.
+inline int64_t conv_grad_rows(int64_t tokens, int32_t seg) {
+    return (tokens + 4 * (int64_t)seg - 1) / (4 * (int64_t)seg);
+}
+// Tokens per wavefront: 32, fewer for short calls, more where the rows of
+// dconv_w would outgrow the tensors (from 16,384 tokens on 128 rows).
+inline int32_t conv_grad_segment(int64_t tokens) {
+    if (tokens > 16384) return (int32_t)((tokens + 511) / 512);
+    return tokens >= 2048 ? 32 : tokens >= 512 ? 16 : 4;
+}
+
 hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream);
 hipError_t launch_recurrent(const DeltaProblem &p, int in_dt, hipStream_t stream);
 hipError_t launch_conv(const ConvProblem &p, int in_dt, hipStream_t stream);
 hipError_t launch_norm(const NormProblem &p, int in_dt, int out_dt, hipStream_t stream);
+hipError_t launch_delta_grad(const DeltaGradProblem &p, int in_dt, int dout_dt, hipStream_t stream);
+hipError_t launch_conv_grad(const ConvGradProblem &p, int dt, hipStream_t stream);
+hipError_t launch_norm_grad(const NormGradProblem &p, int dt, hipStream_t stream);
+hipError_t launch_checkpoint(const CheckpointProblem &p, int dt, hipStream_t stream);
+hipError_t launch_norm_checkpoint(const NormCheckpointProblem &p, int in_dt, int out_dt,
+                                  hipStream_t stream);
 hipError_t launch_map(const MapProblem &p, hipStream_t stream);
 
 }  // namespace kda
