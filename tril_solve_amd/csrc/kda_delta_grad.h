@@ -55,7 +55,7 @@ struct GradWork {
     int V;
     __device__ __forceinline__ GradWork(const DeltaGradProblem &p, int slot, int h)
         : base(p.work + ((long)slot * p.H + h) *
-                            (2L * kGC * kGC + 5L * kGC * K + 2L * kGC * p.V + 2L * K * p.V + K)),
+                            (2L * kGC * kGC + 5L * kGC * K + 2L * kGC * p.V + 2L * K * p.V + K + kGC)),
           V(p.V) {}
     __device__ __forceinline__ float *A() const { return base; }
     __device__ __forceinline__ float *M() const { return base + kGC * kGC; }       // (I + A B)^-1
@@ -65,7 +65,8 @@ struct GradWork {
     __device__ __forceinline__ float *Kbt() const { return Kb() + kGC * K; }       // [K][C]
     __device__ __forceinline__ float *Qt() const { return Kbt() + kGC * K; }       // q e^G, [K][C]
     __device__ __forceinline__ float *decay() const { return Qt() + kGC * K; }     // e^G, [K]
-    __device__ __forceinline__ float *X() const { return decay() + K; }            // [C][V]
+    __device__ __forceinline__ float *beta() const { return decay() + K; }         // [C]
+    __device__ __forceinline__ float *X() const { return beta() + kGC; }           // [C][V]
     __device__ __forceinline__ float *U() const { return X() + kGC * V; }          // dU, [C][V]
     __device__ __forceinline__ float *S() const { return U() + kGC * V; }          // [K][V]
     __device__ __forceinline__ float *D() const { return S() + K * V; }            // dS, [K][V]
@@ -146,6 +147,36 @@ __device__ __forceinline__ void grad_put<F16>(uint16_t *p, float x) {
 }
 __device__ __forceinline__ const f4 &as4(const float *p) { return *reinterpret_cast<const f4 *>(p); }
 __device__ __forceinline__ f4 &as4(float *p) { return *reinterpret_cast<f4 *>(p); }
+
+// Descriptors: rows row .. row + len - 1 of head h in a tensor [T, heads, width],
+// from the first one's element of that head on; n floats.
+template <class E>
+__device__ __forceinline__ Rsrc grad_rows(const void *base, long row, int h, int heads, int width,
+                                          int len) {
+    const typename E::T *at =
+        static_cast<const typename E::T *>(base) + (row * heads + h) * (long)width;
+    const uint32_t n = ((uint32_t)(len - 1) * heads * width + width) * E::kBytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<typename E::T *>(at), 0, n, kRsrcWord3);
+}
+__device__ __forceinline__ Rsrc grad_floats(float *base, int n) {
+    return __builtin_amdgcn_make_buffer_rsrc(base, 0, 4 * n, kRsrcWord3);
+}
+// Stores of 16 lanes fill a part of a line, which the next one completes: they
+// go through L2 by its usual policy.
+template <class E>
+__device__ __forceinline__ void grad_store1(Rsrc r, uint32_t off, float v);
+template <>
+__device__ __forceinline__ void grad_store1<F32>(Rsrc r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+}
+template <>
+__device__ __forceinline__ void grad_store1<BF16>(Rsrc r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), r, off, 0, 0);
+}
+template <>
+__device__ __forceinline__ void grad_store1<F16>(Rsrc r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (_Float16)v), r, off, 0, 0);
+}
 
 // A gate in powers of two. NaN stays (a comparison with it is false).
 __device__ __forceinline__ float grad_gate(float g) {
@@ -336,6 +367,9 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         oP = mm16(image(imQ, ti - 2, T), b, oP);
     }
 
+    if (threadIdx.x < kGC)
+        ws.beta()[threadIdx.x] = (int)threadIdx.x < ch.len
+                                     ? p.beta[(long)(ch.row + threadIdx.x) * p.H + h] : 0.0f;
     // operands of the walks: k e^{G - G_i} both ways, q e^G by channels
 #pragma unroll
     for (int T = 0; T < NT; ++T) {
@@ -487,27 +521,36 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
 
 // -------------------------------------------------------------------- the walks
 
-// A wavefront's columns of a request and head: CT tiles of 16. blockIdx.y: 0
-// the states forwards, 1 their gradients backwards.
-template <class EO, int K, int CT>
-__global__ __launch_bounds__(CT == 1 ? 64 : 512) void kda_grad_walk_kernel(DeltaGradProblem p,
-                                                                             int per_head) {
-    constexpr int NT = K / 16;
+// Barrier of the workgroup that orders LDS alone: loads and stores of memory stay
+// in flight.
+__device__ __forceinline__ void grad_lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A workgroup's columns of a request and head: CT tiles of 16. Each of its four
+// wavefronts owns a quarter of the state's channels: it adds its part of W S
+// (or of (k e^{G - G_i}) dS), the parts are joined in LDS, and every wavefront
+// updates its channels with the whole U. So one step of the chain is a quarter
+// of the products, one barrier, and another quarter; the operands of the next
+// chunk are on their way meanwhile.
+template <class EO, int K, int CT, bool BACK>
+__device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int h, int part,
+                                          float (*joined)[4][4 * CT][kWave * 4]) {
+    constexpr int NT = K / 64;  // tiles of 16 channels to a wavefront
     const int lane = threadIdx.x & (kWave - 1);
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int x = lane & 15, gq = lane >> 4;
-    const int waves = blockDim.x / kWave;
-    const int part = (int)(blockIdx.x % per_head), rest = (int)(blockIdx.x / per_head);
-    const int h = rest % p.H, n = rest / p.H;
-    const int V = p.V, col = (part * waves + wv) * 16 * CT + x;
+    const int V = p.V, col = part * 16 * CT + x, c0 = 16 * NT * w;
     const int2 rows = request_rows(p.req, n);
-    const bool back = blockIdx.y != 0;
-    const Pool &pool = back ? p.grad : p.pool;
+    const Pool &pool = BACK ? p.grad : p.pool;
     const int at = p.grad.slot != nullptr || pool.base != nullptr ? request_slot(pool, n) : 0;
     if (at < 0) return;  // padding
     const int chunks = (rows.y + kGC - 1) / kGC, slot0 = rows.x / kGC + n;
-    const bool from_pool = pool.base != nullptr && (back || request_continues(pool, n));
+    const bool from_pool = pool.base != nullptr && (BACK || request_continues(pool, n));
     float *state = pool.base + ((long)at * p.H + h) * K * V;
+    const f4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     f4 S[NT][CT];
 #pragma unroll
     for (int T = 0; T < NT; ++T)
@@ -515,87 +558,142 @@ __global__ __launch_bounds__(CT == 1 ? 64 : 512) void kda_grad_walk_kernel(Delta
         for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                S[T][c][s] = from_pool ? state[(16 * T + 4 * gq + s) * V + col + 16 * c] : 0.0f;
+                S[T][c][s] =
+                    from_pool ? state[(c0 + 16 * T + 4 * gq + s) * V + col + 16 * c] : 0.0f;
+
+    f4 lhs[4][NT], rhs[NT][4], qt[NT][4], x0[4][CT], beta[4], decay[NT], o[4][CT];
+    auto load_first = [&](const GradWork<K> &ws) {  // for W S or (k e^{G - G_i}) dS
+        const Rsrc r = grad_floats(BACK ? ws.Kb() : ws.W(), kGC * K);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int T = 0; T < NT; ++T)
+                lhs[i][T] = load4<F32>(r, 4 * ((16 * i + x) * K + c0 + 16 * T + 4 * gq));
+    };
+    auto load_join = [&](const GradWork<K> &ws, int j) {
+        const Rsrc r = grad_floats(BACK ? ws.U() : ws.X(), kGC * V);
+        const Rsrc rb = grad_floats(ws.beta(), kGC);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            beta[i] = load4<F32>(rb, 4 * (16 * i + 4 * gq));
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    x0[i][c][s] = load1<F32>(r, 4 * ((16 * i + 4 * gq + s) * V + col + 16 * c));
+        }
+        if constexpr (BACK) {
+            const Rsrc ro = grad_rows<EO>(p.dout, rows.x + j * kGC, h, p.H, V,
+                                          min(kGC, rows.y - j * kGC));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        o[i][c][s] = load1<EO>(ro, ((uint32_t)(16 * i + 4 * gq + s) * p.H * V +
+                                                    col + 16 * c) * EO::kBytes);
+        }
+    };
+    auto load_last = [&](const GradWork<K> &ws) {
+        const Rsrc r = grad_floats(BACK ? ws.Wt() : ws.Kbt(), kGC * K);
+        const Rsrc rq = grad_floats(ws.Qt(), kGC * K), rd = grad_floats(ws.decay(), K);
+#pragma unroll
+        for (int T = 0; T < NT; ++T) {
+            decay[T] = load4<F32>(rd, 4 * (c0 + 16 * T + 4 * gq));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int e = 4 * ((c0 + 16 * T + x) * kGC + 16 * t + 4 * gq);
+                rhs[T][t] = load4<F32>(r, e);
+                if constexpr (BACK) qt[T][t] = load4<F32>(rq, e);
+            }
+        }
+    };
+    auto chunk_of = [&](int j) { return BACK ? chunks - 1 - j : j; };
+    if (chunks > 0) {
+        const GradWork<K> ws(p, slot0 + chunk_of(0), h);
+        load_first(ws);
+        load_last(ws);
+        load_join(ws, chunk_of(0));
+    }
     for (int j = 0; j < chunks; ++j) {
-        const int c0 = back ? chunks - 1 - j : j;
-        const GradWork<K> ws(p, slot0 + c0, h);
-        const int row0 = rows.x + c0 * kGC, len = min(kGC, rows.y - c0 * kGC);
-        float *kept = back ? ws.D() : ws.S();
-        const float *lhs = back ? ws.Kb() : ws.W();
-        float *io = back ? ws.U() : ws.X();
+        const GradWork<K> ws(p, slot0 + chunk_of(j), h);
+        const int jn = chunk_of(min(j + 1, chunks - 1));
+        const GradWork<K> next(p, slot0 + jn, h);
+        float(*mine)[4 * CT][kWave * 4] = joined[j & 1];
+        f4 acc[4][CT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                acc[i][c] = zero4;
+#pragma unroll
+                for (int T = 0; T < NT; ++T) acc[i][c] = mm16(lhs[i][T], S[T][c], acc[i][c]);
+            }
+        load_first(next);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) as4(&mine[w][i * CT + c][lane * 4]) = acc[i][c];
+        {
+            const Rsrc r = grad_floats(BACK ? ws.D() : ws.S(), K * V);
+#pragma unroll
+            for (int T = 0; T < NT; ++T)
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        grad_store1<F32>(
+                            r, 4 * ((c0 + 16 * T + 4 * gq + s) * V + col + 16 * c), S[T][c][s]);
+        }
+#pragma unroll
+        for (int T = 0; T < NT; ++T)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                S[T][c] *= decay[T];
+                if constexpr (BACK)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        S[T][c] = mm16(qt[T][t], o[t][c] * p.scale, S[T][c]);
+            }
+        grad_lds_barrier();
+        f4 u[4][CT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const f4 sum = (as4(&mine[0][i * CT + c][lane * 4]) +
+                                as4(&mine[1][i * CT + c][lane * 4])) +
+                               (as4(&mine[2][i * CT + c][lane * 4]) +
+                                as4(&mine[3][i * CT + c][lane * 4]));
+                u[i][c] = BACK ? x0[i][c] + sum : x0[i][c] - sum;
+            }
+        {  // wavefront w keeps tile row w
+            const Rsrc r = grad_floats(BACK ? ws.U() : ws.X(), kGC * V);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i == w)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            grad_store1<F32>(r, 4 * ((16 * i + 4 * gq + s) * V + col + 16 * c),
+                                             u[i][c][s]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) u[i][c] = (BACK ? -beta[i] : beta[i]) * u[i][c];
+        load_join(next, jn);
 #pragma unroll
         for (int T = 0; T < NT; ++T)
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    kept[(16 * T + 4 * gq + s) * V + col + 16 * c] = S[T][c][s];
-        // X - W S, or dU + (k e^{G - G_i}) dS
-        f4 u[4][CT];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f4 acc[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) acc[c] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int T = 0; T < NT; ++T) {
-                const f4 a = as4(lhs + (16 * i + x) * K + 16 * T + 4 * gq);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) acc[c] = mm16(a, S[T][c], acc[c]);
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * i + 4 * gq + s;
-                const long row = (long)(row0 + min(r, len - 1)) * p.H + h;
-                const float beta = r < len ? p.beta[row] : 0.0f;
-#pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    float *e = io + r * V + col + 16 * c;
-                    const float y = back ? *e + acc[c][s] : *e - acc[c][s];
-                    *e = y;
-                    u[i][c][s] = back ? -beta * y : beta * y;
-                }
-            }
-        }
-        // e^G S + (k e^{G - G_i})^T U, or e^G dS - W^T B dU + (q e^G)^T O'
-        const float *rhs = back ? ws.Wt() : ws.Kbt();
-#pragma unroll
-        for (int T = 0; T < NT; ++T) {
-            const f4 d = as4(ws.decay() + 16 * T + 4 * gq);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) S[T][c] *= d;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const f4 a = as4(rhs + (16 * T + x) * kGC + 16 * t + 4 * gq);
-#pragma unroll
-                for (int c = 0; c < CT; ++c) S[T][c] = mm16(a, u[t][c], S[T][c]);
-            }
-        }
-        if (back) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int r = 16 * t + 4 * gq + s;
-                    const long row = ((long)(row0 + min(r, len - 1)) * p.H + h) * V + col;
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        const float o = Elem<EO>::one(
-                            static_cast<const typename EO::T *>(p.dout) + row + 16 * c);
-                        u[t][c][s] = r < len ? p.scale * o : 0.0f;
-                    }
-                }
-#pragma unroll
-            for (int T = 0; T < NT; ++T)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const f4 a = as4(ws.Qt() + (16 * T + x) * kGC + 16 * t + 4 * gq);
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) S[T][c] = mm16(a, u[t][c], S[T][c]);
-                }
-        }
+                for (int t = 0; t < 4; ++t) S[T][c] = mm16(rhs[T][t], u[t][c], S[T][c]);
+        load_last(next);
     }
-    if (back && pool.base != nullptr) {
+    if (BACK && pool.base != nullptr) {
         const bool cont = request_continues(pool, n);
 #pragma unroll
         for (int T = 0; T < NT; ++T)
@@ -603,8 +701,25 @@ __global__ __launch_bounds__(CT == 1 ? 64 : 512) void kda_grad_walk_kernel(Delta
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    state[(16 * T + 4 * gq + s) * V + col + 16 * c] = cont ? S[T][c][s] : 0.0f;
+                    state[(c0 + 16 * T + 4 * gq + s) * V + col + 16 * c] =
+                        cont ? S[T][c][s] : 0.0f;
     }
+}
+
+// blockIdx.y: 0 the states forwards, 1 their gradients backwards. The workgroups
+// of a request and head (`parts`) read the same operands: their numbers are 8
+// apart, which puts them on one XCD and its L2.
+template <class EO, int K, int CT>
+__global__ __launch_bounds__(256, 2) void kda_grad_walk_kernel(DeltaGradProblem p, int parts) {
+    __shared__ __align__(16) float joined[2][4][4 * CT][kWave * 4];
+    const long group = blockIdx.x / (8 * parts), in = blockIdx.x % (8 * parts);
+    const long walk = group * 8 + in % 8;
+    if (walk >= (long)p.req.num_seqs * p.H) return;
+    const int part = (int)(in / 8), h = (int)(walk % p.H), n = (int)(walk / p.H);
+    if (blockIdx.y == 0)
+        grad_walk<EO, K, CT, false>(p, n, h, part, joined);
+    else
+        grad_walk<EO, K, CT, true>(p, n, h, part, joined);
 }
 
 // ------------------------------------------------------------ gradients of a chunk
@@ -649,6 +764,9 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
     float *xdu = bs + kGC, *cols = xdu + kGC;
     float *dgs = cols + 2 * kGC;        // [4][C] per wavefront (one gate per head)
     const f4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    // rows of this chunk and head; loads behind the last give 0, stores are dropped
+    const Rsrc rdout = grad_rows<EO>(p.dout, ch.row, h, p.H, V, len);
+    const Rsrc rX = grad_floats(ws.X(), kGC * V), rU = grad_floats(ws.U(), kGC * V);
 
     for (int e = threadIdx.x; e < kGC * kGC / 4; e += 256) {
         const int r = e / (kGC / 4), c = e % (kGC / 4) * 4;
@@ -661,7 +779,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
         const int r = threadIdx.x >> 2;
         float sum = 0.0f;
         for (int c = 4 * (threadIdx.x & 3); c < V; c += 16) {
-            const f4 a = as4(ws.X() + r * V + c), b = as4(ws.U() + r * V + c);
+            const f4 a = load4<F32>(rX, 4 * (r * V + c)), b = load4<F32>(rU, 4 * (r * V + c));
 #pragma unroll
             for (int s = 0; s < 4; ++s) sum = __builtin_fmaf(a[s], b[s], sum);
         }
@@ -671,6 +789,8 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
     __syncthreads();
 
     // Y = M^T (B dU)
+    const Rsrc rdv = grad_rows<E>(p.dv, ch.row, h, p.H, V, len);
+#pragma unroll 1
     for (int n = w; n < V / 16; n += 4) {
         f4 b[4];
 #pragma unroll
@@ -678,7 +798,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int r = 16 * t + 4 * gq + s;
-                b[t][s] = bs[r] * ws.U()[r * V + 16 * n + x];
+                b[t][s] = bs[r] * load1<F32>(rU, 4 * (r * V + 16 * n + x));
             }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -695,18 +815,15 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
             for (int s = 0; s < 4; ++s) {
                 const int r = 16 * i + 4 * gq + s;
                 Ys[r * VR + 16 * n + x] = acc[s];
-                if (r < len)
-                    grad_put<E>(static_cast<T_ *>(p.dv) +
-                                    ((long)(ch.row + r) * p.H + h) * V + 16 * n + x, acc[s]);
+                grad_store1<E>(rdv, (uint32_t)(r * p.H * V + 16 * n + x) * E::kBytes, acc[s]);
             }
         }
     }
     __syncthreads();
 
+    const uint32_t dstep = (uint32_t)p.H * V * EO::kBytes;  // bytes between rows of dout
     auto dout4 = [&](int r, int c) {
-        const long at = ((long)(ch.row + min(r, len - 1)) * p.H + h) * V + c;
-        const f4 o = grad_load4<EO>(static_cast<const typename EO::T *>(p.dout) + at);
-        return r < len ? o * p.scale : f4{0.0f, 0.0f, 0.0f, 0.0f};
+        return load4<EO>(rdout, r * dstep + (uint32_t)c * EO::kBytes) * p.scale;
     };
 
     // E = strict(Y X^T) (even wavefronts) and low(O' X^T) (odd): tile rows 3 and 0
@@ -718,16 +835,19 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
 #pragma unroll
         for (int j = 0; j < 4; ++j) up[j] = zero4;
         dn[0] = dn[1] = zero4;
+#pragma unroll 1
         for (int T = 0; T < V / 16; ++T) {
             const int c = 16 * T + 4 * gq;
+            f4 xv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xv[j] = load4<F32>(rX, 4 * ((16 * j + x) * V + c));
             const f4 a = isP ? dout4(16 * hi + x, c) : as4(&Ys[(16 * hi + x) * VR + c]);
             const f4 b = isP ? dout4(16 * lo + x, c) : as4(&Ys[(16 * lo + x) * VR + c]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j <= hi) {
-                    const f4 xv = as4(ws.X() + (16 * j + x) * V + c);
-                    up[j] = mm16(a, xv, up[j]);
-                    if (j < 2 && j <= lo) dn[j] = mm16(b, xv, dn[j]);
+                    up[j] = mm16(a, xv[j], up[j]);
+                    if (j < 2 && j <= lo) dn[j] = mm16(b, xv[j], dn[j]);
                 }
         }
         float colsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -769,100 +889,127 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
 
     // the rest by key channels: 16 to a wavefront at a time
     const bool per_channel = p.gate_stride == K;
+    const Rsrc rk = grad_rows<E>(p.k, ch.row, hk, p.Hk, K, len);
+    const Rsrc rq = grad_rows<E>(p.q, ch.row, hk, p.Hk, K, len);
+    const Rsrc rg = grad_rows<F32>(p.g, ch.row, h, p.H, p.gate_stride, len);
+    const Rsrc rS = grad_floats(ws.S(), 2 * K * V);  // and dS behind it
+    const uint32_t kstep = (uint32_t)p.Hk * K, gstep = (uint32_t)p.H * p.gate_stride;
     f4 dg_head[4] = {zero4, zero4, zero4, zero4};
+#pragma unroll 1
     for (int n = w; n < NT; n += 4) {
+        // (nothing of the matrices or of the rows' offsets is worth registers
+        // across the channels: they are taken anew)
+        int gq = lane >> 4, x = lane & 15;
+        asm volatile("" : "+v"(gq), "+v"(x) : : "memory");
         const int c = 16 * n + x;
         // O' S^T, Y S^T, U dS^T and the rows of S * dS
         f4 dq[4], dk[4], ke[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) dq[i] = dk[i] = ke[i] = zero4;
         float both = 0.0f;
+#pragma unroll 1
         for (int T = 0; T < V / 16; ++T) {
             const int v = 16 * T + 4 * gq;
-            const f4 s4 = as4(ws.S() + c * V + v), d4 = as4(ws.D() + c * V + v);
+            const f4 s4 = load4<F32>(rS, 4 * (c * V + v));
+            const f4 d4 = load4<F32>(rS, 4 * ((K + c) * V + v));
+            f4 o[4], xx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = load4<EO>(rdout, (16 * i + x) * dstep + (uint32_t)v * EO::kBytes);
+                xx[i] = load4<F32>(rX, 4 * ((16 * i + x) * V + v));
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) both = __builtin_fmaf(s4[s], d4[s], both);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 16 * i + x;
-                dq[i] = mm16(dout4(r, v), s4, dq[i]);
+                dq[i] = mm16(o[i], s4, dq[i]);
                 dk[i] = mm16(as4(&Ys[r * VR + v]), s4, dk[i]);
-                ke[i] = mm16(as4(ws.X() + r * V + v) * bs[r], d4, ke[i]);
+                ke[i] = mm16(xx[i] * bs[r], d4, ke[i]);
             }
         }
         both = add_rows32(add_rows16(both));
+        __builtin_amdgcn_sched_barrier(0);
 
-        f4 k[4], q[4], pre[4], suf[4];
+        f4 k[4], q[4], g[4], pre[4], suf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int r = 16 * t + 4 * gq + s;
-                const long row = ch.row + min(r, len - 1);
-                const long at = (row * p.Hk + hk) * K + c;
-                const float kk = Elem<E>::one(static_cast<const T_ *>(p.k) + at);
-                const float qq = Elem<E>::one(static_cast<const T_ *>(p.q) + at);
-                const float gg = p.g[(row * p.H + h) * p.gate_stride + (per_channel ? c : 0)];
-                k[t][s] = r < len ? kk : 0.0f;
-                q[t][s] = r < len ? qq : 0.0f;
-                pre[t][s] = grad_gate(r < len ? gg : 0.0f);
+                const uint32_t r = 16 * t + 4 * gq + s, at = r * kstep + c;
+                k[t][s] = load1<E>(rk, at * E::kBytes);
+                q[t][s] = load1<E>(rq, at * E::kBytes);
+                g[t][s] = grad_gate(load1<F32>(rg, 4 * (r * gstep + (per_channel ? c : 0))));
             }
-        // In registers, tokens 4 g .. 4 g + 3 of a tile: sums before (through
-        // the token) and behind it, over 2, 4, 8, 16 and more tokens. fac(b): the
-        // factor of level b.
-        f4 fac[4][4];  // levels 1, 2, 4, 8 of each tile
-        float total[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f4 g = pre[t];
-            fac[0][t] = exp2(f4{0.0f, g[1], 0.0f, g[3]});
-            fac[1][t] = exp2(f4{g[1], 0.0f, g[2], g[2] + g[3]});
-            const f4 in = {g[0], g[0] + g[1], g[0] + g[1] + g[2], g[0] + g[1] + g[2] + g[3]};
-            const f4 out = {g[1] + g[2] + g[3], g[2] + g[3], g[3], 0.0f};
-            fac[2][t] = exp2((gq & 1) ? in : out);
-            f4 part[4];  // totals of the four groups of lanes
-            gather_groups<4>(f4{in[3], 0.0f, 0.0f, 0.0f}, part);
-            const float t0 = part[0][0], t1 = part[1][0], t2 = part[2][0], t3 = part[3][0];
-            const float e8 = gq == 3 ? t2 : gq == 0 ? t1 : 0.0f;
-            fac[3][t] = exp2((gq & 2) ? in + e8 : out + e8);
-            const float b16 = gq == 0 ? 0.0f : gq == 1 ? t0 : gq == 2 ? t0 + t1 : t0 + t1 + t2;
-            const float a16 = gq == 3 ? 0.0f : gq == 2 ? t3 : gq == 1 ? t2 + t3 : t1 + t2 + t3;
-            pre[t] = in + b16;
-            suf[t] = out + a16;
-            total[t] = t0 + t1 + t2 + t3;
-        }
-        f4 dg[4];
-        // sums of x over the tokens of a tile from this one on, or before it
-        auto groups = [&](f4 v, float (&part)[4]) {
-            f4 o[4];
-            gather_groups<4>(f4{v[0] + v[1] + v[2] + v[3], 0.0f, 0.0f, 0.0f}, o);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[i] = o[i][0];
+        // In registers, tokens 4 g .. 4 g + 3 of a tile: sums through the token
+        // (in) and behind it (out) over 4, 16 and more tokens.
+        auto in4 = [](f4 v) {
+            const float a = v[0] + v[1], b = a + v[2];
+            return f4{v[0], a, b, b + v[3]};
+        };
+        auto out4 = [](f4 v) {
+            const float a = v[2] + v[3];
+            return f4{v[1] + a, a, v[3], 0.0f};
         };
         auto from4 = [](f4 v) {
-            return f4{v[0] + v[1] + v[2] + v[3], v[1] + v[2] + v[3], v[2] + v[3], v[3]};
+            const float a = v[2] + v[3], b = v[1] + a;
+            return f4{v[0] + b, b, a, v[3]};
         };
-        auto before4 = [](f4 v) { return f4{0.0f, v[0], v[0] + v[1], v[0] + v[1] + v[2]}; };
+        auto before4 = [](f4 v) {
+            const float a = v[0] + v[1];
+            return f4{0.0f, v[0], a, a + v[2]};
+        };
+        // a sum of four tokens, of each group of lanes
+        auto groups = [&](float v, float (&part)[4]) {
+            float a = v, b = v;
+            lane_swap32(a, b);
+            part[0] = part[1] = a;
+            part[2] = part[3] = b;
+            lane_swap16(part[0], part[1]);
+            lane_swap16(part[2], part[3]);
+        };
+        auto earlier = [&](const float (&o)[4]) {
+            const float a = o[0] + o[1];
+            return gq == 0 ? 0.0f : gq == 1 ? o[0] : gq == 2 ? a : a + o[2];
+        };
+        auto later = [&](const float (&o)[4]) {
+            const float a = o[2] + o[3];
+            return gq == 3 ? 0.0f : gq == 2 ? o[3] : gq == 1 ? a : o[1] + a;
+        };
+        float total[4], next8[4];  // next8: of the other group in the token's half of 16
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f4 in = in4(g[t]);
+            float o[4];
+            groups(in[3], o);
+            next8[t] = gq == 3 ? o[2] : gq == 0 ? o[1] : 0.0f;
+            pre[t] = in + earlier(o);
+            suf[t] = out4(g[t]) + later(o);
+            total[t] = (o[0] + o[1]) + (o[2] + o[3]);
+        }
+        f4 dg[4];
         auto from16 = [&](f4 v, float &sum) {
             float o[4];
-            groups(v, o);
-            sum = o[0] + o[1] + o[2] + o[3];
-            return from4(v) + (gq == 3 ? 0.0f : gq == 2 ? o[3] : gq == 1 ? o[2] + o[3]
-                                                              : o[1] + o[2] + o[3]);
+            const f4 in = from4(v);
+            groups(in[0], o);
+            sum = (o[0] + o[1]) + (o[2] + o[3]);
+            return in + later(o);
         };
         auto before16 = [&](f4 v, float &sum) {
             float o[4];
-            groups(v, o);
-            sum = o[0] + o[1] + o[2] + o[3];
-            return before4(v) + (gq == 0 ? 0.0f : gq == 1 ? o[0] : gq == 2 ? o[0] + o[1]
-                                                                : o[0] + o[1] + o[2]);
+            const f4 in = before4(v);
+            groups(in[3] + v[3], o);
+            sum = (o[0] + o[1]) + (o[2] + o[3]);
+            return in + earlier(o);
         };
+        // Forms the sums here: the compiler else moves them behind everything,
+        // and keeps all of their terms till there.
+        auto now = [&](int t) { asm volatile("" : "+v"(dq[t]), "+v"(dk[t]), "+v"(dg[t])); };
         // the states' terms: decays from the chunk's start and to its end
         {
-            const float whole = total[0] + total[1] + total[2] + total[3];
+            const float whole = (total[0] + total[1]) + (total[2] + total[3]);
             const float all = __builtin_amdgcn_exp2f(whole) * both;
             float head = 0.0f, rs[4], es[4];
-            f4 er[4], rr[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const f4 eg = exp2(pre[t] + head);
@@ -871,47 +1018,50 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
                 for (int j = 3; j > t; --j) tail += total[j];
                 const f4 ez = exp2(suf[t] + tail);
                 head += total[t];
-                dq[t] = eg * dq[t];
+                dq[t] = eg * dq[t] * p.scale;
                 const f4 r = -eg * dk[t], e = ez * ke[t];
                 dk[t] = r + e;
-                rr[t] = from16(q[t] * dq[t] + k[t] * r, rs[t]);
-                er[t] = before16(k[t] * e, es[t]);
+                dg[t] = from16(q[t] * dq[t] + k[t] * r, rs[t]);
+                dg[t] += before16(k[t] * e, es[t]);
+                now(t);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 float more = all;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) more += j > t ? rs[j] : j < t ? es[j] : 0.0f;
-                dg[t] = rr[t] + er[t] + more;
+                dg[t] += more;
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         // pairs of tokens, level by level: z holds queries of the upper half
         // and keys of the lower, so one product serves rows and columns
-        auto level = [&](int t, f4 f, bool upper[4], f4 e1, f4 e2) {
+        auto level = [&](int t, f4 f, const bool (&upper)[4], f4 e1, f4 e2) {
             f4 term;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const float kf = k[t][s] * f[s], qf = q[t][s] * f[s];
-                if (upper[s]) {
-                    dq[t][s] = __builtin_fmaf(f[s], e1[s], dq[t][s]);
-                    dk[t][s] = __builtin_fmaf(f[s], e2[s], dk[t][s]);
-                    term[s] = qf * e1[s] + kf * e2[s];
-                } else {
-                    dk[t][s] = __builtin_fmaf(f[s], e1[s] + e2[s], dk[t][s]);
-                    term[s] = kf * (e1[s] + e2[s]);
-                }
+                const float a = f[s] * (upper[s] ? e2[s] : e1[s] + e2[s]);
+                const float b = upper[s] ? f[s] * e1[s] : 0.0f;
+                dq[t][s] += b;
+                dk[t][s] += a;
+                term[s] = __builtin_fmaf(q[t][s], b, k[t][s] * a);
             }
             return term;
         };
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
+            asm volatile("" : "+v"(g[t]));  // its sums are not worth registers till here
             const f4 a = as4(&Am[(16 * t + x) * kMatRow + 16 * t + 4 * gq]);
             const f4 b = as4(&Pm[(16 * t + x) * kMatRow + 16 * t + 4 * gq]);
 #pragma unroll
             for (int l = 0; l < 4; ++l) {
-                f4 am, bm, z, kf;
+                f4 am, bm, z, kf, f;
                 bool upper[4];
-                const f4 f = fac[l][t];
+                if (l == 0) f = f4{0.0f, g[t][1], 0.0f, g[t][3]};
+                if (l == 1) f = f4{g[t][1], 0.0f, g[t][2], g[t][2] + g[t][3]};
+                if (l == 2) f = (gq & 1) ? in4(g[t]) : out4(g[t]);
+                if (l == 3) f = ((gq & 2) ? in4(g[t]) : out4(g[t])) + next8[t];
+                f = exp2(f);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const int d = (4 * gq + s) ^ x;
@@ -935,10 +1085,11 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
                     dg[t] += (gq & 1) ? from4(r) : before4(r);
                 } else {
                     float o[4];
-                    groups(r, o);
-                    dg[t] += (gq & 2) ? from4(r) + (gq == 2 ? o[3] : 0.0f)
-                                      : before4(r) + (gq == 1 ? o[0] : 0.0f);
+                    groups((r[0] + r[1]) + (r[2] + r[3]), o);
+                    const float more = gq == 2 ? o[3] : gq == 1 ? o[0] : 0.0f;
+                    dg[t] += ((gq & 2) ? from4(r) : before4(r)) + more;
                 }
+                now(t);
             }
             // the diagonal of P
 #pragma unroll
@@ -948,39 +1099,48 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
                 dq[t][s] = __builtin_fmaf(d, k[t][s], dq[t][s]);
                 dk[t][s] = __builtin_fmaf(d, q[t][s], dk[t][s]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         auto tiles = [&](const float *m, int i, int j) {
             return as4(m + (16 * i + x) * kMatRow + 16 * j + 4 * gq);
         };
-        {  // level 16
-            f4 f[4], kf[4], z[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f[t] = exp2((t & 1) ? pre[t] : suf[t]);
-                kf[t] = k[t] * f[t];
-                z[t] = (t & 1) ? q[t] * f[t] : kf[t];
+        for (int pair = 0; pair < 4; pair += 2) {  // level 16: tiles 0 and 1, 2 and 3
+            f4 f[2], kf[2], z[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = pair + i;
+                f[i] = exp2(i ? pre[t] : suf[t]);
+                kf[i] = k[t] * f[i];
+                z[i] = i ? q[t] * f[i] : kf[i];
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const f4 e2 = mm16(tiles(Am, t, t ^ 1), kf[t ^ 1], zero4);
-                const f4 e1 = mm16(tiles(Pm, t, t ^ 1), z[t ^ 1], zero4);
-                bool upper[4] = {(t & 1) != 0, (t & 1) != 0, (t & 1) != 0, (t & 1) != 0};
-                const f4 r = level(t, f[t], upper, e1, e2);
+            for (int i = 0; i < 2; ++i) {
+                const int t = pair + i;
+                const f4 e2 = mm16(tiles(Am, t, t ^ 1), kf[1 - i], zero4);
+                const f4 e1 = mm16(tiles(Pm, t, t ^ 1), z[1 - i], zero4);
+                const bool upper[4] = {i == 1, i == 1, i == 1, i == 1};
+                const f4 r = level(t, f[i], upper, e1, e2);
                 float sum;
-                dg[t] += (t & 1) ? from16(r, sum) : before16(r, sum);
+                dg[t] += i ? from16(r, sum) : before16(r, sum);
+                now(t);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         {  // level 32
-            f4 f[4], kf[4], z[4], term[4];
+            f4 kf[4], z[4];
             float sum[4];
-            f[0] = exp2(suf[0] + total[1]);
-            f[1] = exp2(suf[1]);
-            f[2] = exp2(pre[2]);
-            f[3] = exp2(pre[3] + total[2]);
+            auto factor = [&](int t) {
+                return exp2(t == 0   ? suf[0] + total[1]
+                            : t == 1 ? suf[1]
+                            : t == 2 ? pre[2]
+                                     : pre[3] + total[2]);
+            };
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                kf[t] = k[t] * f[t];
-                z[t] = t >= 2 ? q[t] * f[t] : kf[t];
+                const f4 f = factor(t);
+                kf[t] = k[t] * f;
+                z[t] = t >= 2 ? q[t] * f : kf[t];
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -989,34 +1149,36 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
                                    mm16(tiles(Am, t, y), kf[y], zero4));
                 const f4 e1 = mm16(tiles(Pm, t, y + 1), z[y + 1],
                                    mm16(tiles(Pm, t, y), z[y], zero4));
-                bool upper[4] = {t >= 2, t >= 2, t >= 2, t >= 2};
-                const f4 r = level(t, f[t], upper, e1, e2);
-                term[t] = t >= 2 ? from16(r, sum[t]) : before16(r, sum[t]);
+                const bool upper[4] = {t >= 2, t >= 2, t >= 2, t >= 2};
+                const f4 r = level(t, factor(t), upper, e1, e2);
+                dg[t] += t >= 2 ? from16(r, sum[t]) : before16(r, sum[t]);
+                now(t);
             }
-            dg[0] += term[0];
-            dg[1] += term[1] + sum[0];
-            dg[2] += term[2] + sum[3];
-            dg[3] += term[3];
+            dg[1] += sum[0];
+            dg[2] += sum[3];
         }
+        const Rsrc rdq = p.dq_head ? grad_rows<F32>(p.dq_head, ch.row, h, p.H, K, len)
+                                   : grad_rows<E>(p.dq, ch.row, hk, p.Hk, K, len);
+        const Rsrc rdk = p.dq_head ? grad_rows<F32>(p.dk_head, ch.row, h, p.H, K, len)
+                                   : grad_rows<E>(p.dk, ch.row, hk, p.Hk, K, len);
+        const Rsrc rdg = grad_rows<F32>(p.dg, ch.row, h, p.H, p.gate_stride, len);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int r = 16 * t + 4 * gq + s;
-                if (r < len) {
-                    const long row = ch.row + r, at = row * p.H + h;
-                    if (p.dq_head) {
-                        p.dq_head[at * K + c] = dq[t][s];
-                        p.dk_head[at * K + c] = dk[t][s];
-                    } else {
-                        grad_put<E>(static_cast<T_ *>(p.dq) + (row * p.Hk + hk) * K + c, dq[t][s]);
-                        grad_put<E>(static_cast<T_ *>(p.dk) + (row * p.Hk + hk) * K + c, dk[t][s]);
-                    }
-                    if (per_channel) p.dg[at * K + c] = dg[t][s];
+                const uint32_t r = 16 * t + 4 * gq + s;
+                if (p.dq_head) {
+                    grad_store1<F32>(rdq, 4 * (r * p.H * K + c), dq[t][s]);
+                    grad_store1<F32>(rdk, 4 * (r * p.H * K + c), dk[t][s]);
+                } else {
+                    grad_store1<E>(rdq, (r * kstep + c) * E::kBytes, dq[t][s]);
+                    grad_store1<E>(rdk, (r * kstep + c) * E::kBytes, dk[t][s]);
                 }
+                if (per_channel) grad_store1<F32>(rdg, 4 * (r * gstep + c), dg[t][s]);
             }
+        if (!per_channel)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) dg_head[t] += dg[t];
+            for (int t = 0; t < 4; ++t) dg_head[t] += dg[t];
     }
     if (!per_channel) {  // summed over the channels: 16 lanes, then the wavefronts
 #pragma unroll
@@ -1068,15 +1230,15 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
                            p);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    const long walks = (long)p.req.num_seqs * p.H;
-    if (walks * (p.V / 16) > 2048) {
-        const int waves = p.V / 32;
-        hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 2>), dim3((unsigned)walks, 2),
-                           dim3(waves * kWave), 0, stream, p, 1);
+    const long walks = (long)p.req.num_seqs * p.H, groups = (walks + 7) / 8;
+    if (walks * (p.V / 32) >= 1024) {
+        const int parts = p.V / 32;
+        hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 2>), dim3((unsigned)(groups * 8 * parts), 2),
+                           dim3(256), 0, stream, p, parts);
     } else {
-        hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 1>),
-                           dim3((unsigned)(walks * (p.V / 16)), 2), dim3(kWave), 0, stream, p,
-                           p.V / 16);
+        const int parts = p.V / 16;
+        hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 1>), dim3((unsigned)(groups * 8 * parts), 2),
+                           dim3(256), 0, stream, p, parts);
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (p.req.total_tokens > 0) {
