@@ -53,10 +53,12 @@ template <int K>
 struct GradWork {
     float *base;
     int V;
-    __device__ __forceinline__ GradWork(const DeltaGradProblem &p, int slot, int h)
-        : base(p.work + ((long)slot * p.H + h) *
-                            (2L * kGC * kGC + 5L * kGC * K + 2L * kGC * p.V + 2L * K * p.V + K + kGC)),
-          V(p.V) {}
+    // floats of one chunk and head
+    static __device__ __forceinline__ long size(int V) {
+        return 2L * kGC * kGC + 5L * kGC * K + 2L * kGC * V + 2L * K * V + K + kGC;
+    }
+    __device__ __forceinline__ GradWork(float *work, int V, long item)
+        : base(work + item * size(V)), V(V) {}
     __device__ __forceinline__ float *A() const { return base; }
     __device__ __forceinline__ float *M() const { return base + kGC * kGC; }       // (I + A B)^-1
     __device__ __forceinline__ float *W() const { return M() + kGC * kGC; }        // [C][K]
@@ -161,6 +163,22 @@ __device__ __forceinline__ Rsrc grad_rows(const void *base, long row, int h, int
 __device__ __forceinline__ Rsrc grad_floats(float *base, int n) {
     return __builtin_amdgcn_make_buffer_rsrc(base, 0, 4 * n, kRsrcWord3);
 }
+// An element as loaded, and widened where it is used: a load in flight is not waited
+// for before.
+template <class E>
+__device__ __forceinline__ uint32_t grad_raw1(Rsrc r, uint32_t off) {
+    if constexpr (E::kBytes == 4)
+        return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+}
+template <class E>
+__device__ __forceinline__ float grad_widen(uint32_t raw) {
+    if constexpr (E::kBytes == 4)
+        return __builtin_bit_cast(float, raw);
+    else
+        return Elem<E>::widen(raw);
+}
 // Stores of 16 lanes fill a part of a line, which the next one completes: they
 // go through L2 by its usual policy.
 template <class E>
@@ -207,6 +225,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     constexpr int kImages = 6 * NT * 64 * 4, kMats = 2 * kMat + (kMat > kGC * KR ? kMat : kGC * KR);
     __shared__ __align__(16) float lds[kImages > kMats ? kImages : kMats];
     __shared__ __align__(16) float totals[4][K];
+    __shared__ float bs[kGC];
     const int lane = threadIdx.x & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int x = lane & 15, gq = lane >> 4;
@@ -214,35 +233,35 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     const GradChunk ch = grad_chunk(p.req, slot, lane);
     if (ch.len == 0) return;
     if (p.grad.slot != nullptr && request_slot(p.grad, ch.request) < 0) return;
-    const GradWork<K> ws(p, slot, h);
+    const GradWork<K> ws(p.work, p.V, (long)slot * p.H + h);
     const int V = p.V, tok = 16 * w + x;
-    const bool on = tok < ch.len;
-    const long row = ch.row + min(tok, ch.len - 1);
-
     f4 k[NT], q[NT], pre[NT], suf[NT], tot[NT];
-    {
-        const long at = (row * p.Hk + h / (p.H / p.Hk)) * K + 4 * gq;
-        const typename E::T *kp = static_cast<const typename E::T *>(p.k) + at;
-        const typename E::T *qp = static_cast<const typename E::T *>(p.q) + at;
-        const float *gp = p.g + (row * p.H + h) * p.gate_stride;
-        const bool per_channel = p.gate_stride == K;
-        const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    {  // rows behind the last load 0
+        const int hk = h / (p.H / p.Hk);
+        const Rsrc rk = grad_rows<E>(p.k, ch.row, hk, p.Hk, K, ch.len);
+        const Rsrc rq = grad_rows<E>(p.q, ch.row, hk, p.Hk, K, ch.len);
+        const Rsrc rg = grad_rows<F32>(p.g, ch.row, h, p.H, p.gate_stride, ch.len);
+        const uint32_t at = (uint32_t)(tok * p.Hk * K + 4 * gq) * E::kBytes;
+        const uint32_t gat = (uint32_t)tok * p.H * p.gate_stride * 4;
 #pragma unroll
         for (int T = 0; T < NT; ++T) {
-            k[T] = grad_load4<E>(kp + 16 * T);
-            q[T] = grad_load4<E>(qp + 16 * T);
-            f4 gg;
-            if (per_channel) {
-                gg = as4(gp + 16 * T + 4 * gq);
-            } else {
-                const float one = *gp;
-                gg = f4{one, one, one, one};
-            }
-            if (!on) k[T] = q[T] = gg = zero;
+            k[T] = load4<E>(rk, at + 16 * T * E::kBytes);
+            q[T] = load4<E>(rq, at + 16 * T * E::kBytes);
+        }
+        if (p.gate_stride == K) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) gg[s] = grad_gate(gg[s]);
-            pre[T] = tot[T] = gg;
-            suf[T] = zero;
+            for (int T = 0; T < NT; ++T) tot[T] = load4<F32>(rg, gat + 16 * gq + 64 * T);
+        } else {
+            const float one = load1<F32>(rg, gat);
+#pragma unroll
+            for (int T = 0; T < NT; ++T) tot[T] = f4{one, one, one, one};
+        }
+#pragma unroll
+        for (int T = 0; T < NT; ++T) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) tot[T][s] = grad_gate(tot[T][s]);
+            pre[T] = tot[T];
+            suf[T] = f4{0.0f, 0.0f, 0.0f, 0.0f};
         }
     }
 
@@ -320,6 +339,12 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     auto image = [&](float *im, int slot_, int T) -> f4 & {
         return as4(im + ((slot_ * NT + T) * 64 + lane) * 4);
     };
+    if (threadIdx.x < kGC) {
+        const Rsrc rb = grad_rows<F32>(p.beta, ch.row, h, p.H, 1, ch.len);
+        const float one = load1<F32>(rb, threadIdx.x * p.H * 4);
+        bs[threadIdx.x] = one;
+        ws.beta()[threadIdx.x] = one;
+    }
     if (x == 0)
 #pragma unroll
         for (int T = 0; T < NT; ++T) as4(&totals[w][16 * T + 4 * gq]) = tot[T];
@@ -340,22 +365,30 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         }
     }
     __syncthreads();
-    f4 eg[NT], es[NT];  // e^G from the chunk's start through the token, and from it to the end
+    // 1 for wavefronts from 1, 2, 3 on and up to 0, 1, 2 (branches on them would cut
+    // the code into pieces)
+    const float u1 = w >= 1, u2 = w >= 2, u3 = w >= 3, d0 = w < 1, d1 = w < 2, d2 = w < 3;
+    const float a32 = w == 0, b32 = w == 3;
+    f4 kg[NT];  // k e^G
 #pragma unroll
     for (int T = 0; T < NT; ++T) {
         f4 t[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) t[j] = as4(&totals[j][16 * T + 4 * gq]);
-        f4 half = w == 0 ? suf[T] + t[1] : w == 1 ? suf[T] : w == 2 ? pre[T] : pre[T] + t[2];
-        half = exp2(half);
+        const f4 half = exp2((w >= 2 ? pre[T] : suf[T]) + (a32 * t[1] + b32 * t[2]));
         image(imK, w, T) = k[T] * half;
         if (w >= 2) image(imQ, w - 2, T) = q[T] * half;
-        const f4 before = w == 0 ? f4{0.0f, 0.0f, 0.0f, 0.0f} : w == 1 ? t[0]
-                          : w == 2 ? t[0] + t[1] : t[0] + t[1] + t[2];
-        const f4 behind = w == 3 ? f4{0.0f, 0.0f, 0.0f, 0.0f} : w == 2 ? t[3]
-                          : w == 1 ? t[2] + t[3] : t[1] + t[2] + t[3];
-        eg[T] = exp2(pre[T] + before);
-        es[T] = exp2(suf[T] + behind);
+        const f4 before = u1 * t[0] + u2 * t[1] + u3 * t[2];
+        const f4 behind = d2 * t[3] + d1 * t[2] + d0 * t[1];
+        // operands of the walks: k e^{G - G_i} both ways, q e^G by channels
+        const f4 eg = exp2(pre[T] + before), kb = k[T] * exp2(suf[T] + behind), qg = q[T] * eg;
+        kg[T] = k[T] * eg;
+        as4(ws.Kb() + tok * K + 16 * T + 4 * gq) = kb;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            ws.Kbt()[(16 * T + 4 * gq + s) * kGC + tok] = kb[s];
+            ws.Qt()[(16 * T + 4 * gq + s) * kGC + tok] = qg[s];
+        }
         if (w == 0 && x == 0) as4(ws.decay() + 16 * T + 4 * gq) = exp2(t[0] + t[1] + t[2] + t[3]);
     }
     __syncthreads();
@@ -367,27 +400,13 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         oP = mm16(image(imQ, ti - 2, T), b, oP);
     }
 
-    if (threadIdx.x < kGC)
-        ws.beta()[threadIdx.x] = (int)threadIdx.x < ch.len
-                                     ? p.beta[(long)(ch.row + threadIdx.x) * p.H + h] : 0.0f;
-    // operands of the walks: k e^{G - G_i} both ways, q e^G by channels
-#pragma unroll
-    for (int T = 0; T < NT; ++T) {
-        const f4 kb = k[T] * es[T], qg = q[T] * eg[T];
-        as4(ws.Kb() + tok * K + 16 * T + 4 * gq) = kb;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            ws.Kbt()[(16 * T + 4 * gq + s) * kGC + tok] = kb[s];
-            ws.Qt()[(16 * T + 4 * gq + s) * kGC + tok] = qg[s];
-        }
-    }
     __syncthreads();  // the images are read
 
     // the matrices: A to memory, L = A B and P to LDS
     float *Mm = lds, *Pm = lds + kMat, *Lm = lds + 2 * kMat;
     auto put = [&](int bi, int bj, f4 a, bool isA, bool isP) {
         const int col = 16 * bj + x;
-        const float beta = col < ch.len ? p.beta[(long)(ch.row + col) * p.H + h] : 0.0f;
+        const float beta = bs[col];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int r = 16 * bi + 4 * gq + s;
@@ -457,7 +476,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     // k e^G by tokens, in L's place; M to memory
     float *Kg = Lm;
 #pragma unroll
-    for (int T = 0; T < NT; ++T) as4(&Kg[tok * KR + 16 * T + 4 * gq]) = k[T] * eg[T];
+    for (int T = 0; T < NT; ++T) as4(&Kg[tok * KR + 16 * T + 4 * gq]) = kg[T];
     for (int e = threadIdx.x; e < kGC * kGC / 4; e += 256) {
         const int r = e / (kGC / 4), c = e % (kGC / 4) * 4;
         if (c / 16 <= r / 16) as4(ws.M() + r * kGC + c) = as4(&Mm[r * kMatRow + c]);
@@ -483,18 +502,18 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         }
     }
     // X = M V, dU = P^T O', still without the states
+    const Rsrc rv = grad_rows<E>(p.v, ch.row, h, p.H, V, ch.len);
+    const Rsrc ro = grad_rows<EO>(p.dout, ch.row, h, p.H, V, ch.len);
+    const uint32_t vstep = (uint32_t)p.H * V;
     for (int n = w; n < V / 16; n += 4) {
         f4 b[4], o[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int r = 16 * t + 4 * gq + s;
-                const long at = ((long)(ch.row + min(r, ch.len - 1)) * p.H + h) * V + 16 * n + x;
-                const float vv = Elem<E>::one(static_cast<const typename E::T *>(p.v) + at);
-                const float oo = Elem<EO>::one(static_cast<const typename EO::T *>(p.dout) + at);
-                b[t][s] = r < ch.len ? vv : 0.0f;
-                o[t][s] = r < ch.len ? p.scale * oo : 0.0f;
+                const uint32_t at = (16 * t + 4 * gq + s) * vstep + 16 * n + x;
+                b[t][s] = load1<E>(rv, at * E::kBytes);
+                o[t][s] = load1<EO>(ro, at * EO::kBytes) * p.scale;
             }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -530,22 +549,35 @@ __device__ __forceinline__ void grad_lds_barrier() {
 }
 
 // A workgroup's columns of a request and head: CT tiles of 16. Each of its four
-// wavefronts owns a quarter of the state's channels: it adds its part of W S
-// (or of (k e^{G - G_i}) dS), the parts are joined in LDS, and every wavefront
-// updates its channels with the whole U. So one step of the chain is a quarter
-// of the products, one barrier, and another quarter; the operands of the next
-// chunk are on their way meanwhile.
+// wavefronts owns a quarter of the state's channels and adds its part of W S (or
+// of (k e^{G - G_i}) dS); wavefront i joins the parts of tile row i in LDS and
+// makes X (or dU) of it, and every wavefront updates its channels with the whole
+// U. So one step of the chain is a quarter of the products, two exchanges in LDS
+// and another quarter, and the operands of the next chunk are on their way
+// meanwhile.
+template <int CT>
+struct GradWalkLds {
+    float part[4][4 * CT][kWave * 4];  // [wavefront][tile row, column tile]
+    float u[4 * CT][kWave * 4], o[4 * CT][kWave * 4];
+};
 template <class EO, int K, int CT, bool BACK>
 __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int h, int part,
-                                          float (*joined)[4][4 * CT][kWave * 4]) {
+                                          GradWalkLds<CT> &lds) {
     constexpr int NT = K / 64;  // tiles of 16 channels to a wavefront
     const int lane = threadIdx.x & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int x = lane & 15, gq = lane >> 4;
-    const int V = p.V, col = part * 16 * CT + x, c0 = 16 * NT * w;
-    const int2 rows = request_rows(p.req, n);
-    const Pool &pool = BACK ? p.grad : p.pool;
-    const int at = p.grad.slot != nullptr || pool.base != nullptr ? request_slot(pool, n) : 0;
+    // (copies: captured by reference, the arguments would be read from scratch)
+    float *const work = p.work;
+    const void *const dout = p.dout;
+    const float scale = p.scale;
+    const int V = p.V, H = p.H, col = part * 16 * CT + x, c0 = 16 * NT * w;
+    int2 rows = request_rows(p.req, n);
+    rows.x = __builtin_amdgcn_readfirstlane(rows.x);  // (descriptors are made of them)
+    rows.y = __builtin_amdgcn_readfirstlane(rows.y);
+    const Pool pool = BACK ? p.grad : p.pool;
+    const int at = __builtin_amdgcn_readfirstlane(
+        p.grad.slot != nullptr || pool.base != nullptr ? request_slot(pool, n) : 0);
     if (at < 0) return;  // padding
     const int chunks = (rows.y + kGC - 1) / kGC, slot0 = rows.x / kGC + n;
     const bool from_pool = pool.base != nullptr && (BACK || request_continues(pool, n));
@@ -561,7 +593,8 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
                 S[T][c][s] =
                     from_pool ? state[(c0 + 16 * T + 4 * gq + s) * V + col + 16 * c] : 0.0f;
 
-    f4 lhs[4][NT], rhs[NT][4], qt[NT][4], x0[4][CT], beta[4], decay[NT], o[4][CT];
+    f4 lhs[4][NT], rhs[NT][4], qt[NT][4], x0[CT], beta, decay[NT];
+    uint32_t o[CT][4];
     auto load_first = [&](const GradWork<K> &ws) {  // for W S or (k e^{G - G_i}) dS
         const Rsrc r = grad_floats(BACK ? ws.Kb() : ws.W(), kGC * K);
 #pragma unroll
@@ -570,57 +603,69 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
             for (int T = 0; T < NT; ++T)
                 lhs[i][T] = load4<F32>(r, 4 * ((16 * i + x) * K + c0 + 16 * T + 4 * gq));
     };
-    auto load_join = [&](const GradWork<K> &ws, int j) {
+    auto load_join = [&](const GradWork<K> &ws) {
         const Rsrc r = grad_floats(BACK ? ws.U() : ws.X(), kGC * V);
-        const Rsrc rb = grad_floats(ws.beta(), kGC);
+        beta = load4<F32>(grad_floats(ws.beta(), kGC), 4 * (16 * w + 4 * gq));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            beta[i] = load4<F32>(rb, 4 * (16 * i + 4 * gq));
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x0[c][s] = load1<F32>(r, 4 * ((16 * w + 4 * gq + s) * V + col + 16 * c));
+    };
+    auto load_dout = [&](int j) {
+        if constexpr (BACK) {
+            const Rsrc ro = grad_rows<EO>(dout, rows.x + j * kGC, h, H, V,
+                                          min(kGC, rows.y - j * kGC));
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    x0[i][c][s] = load1<F32>(r, 4 * ((16 * i + 4 * gq + s) * V + col + 16 * c));
-        }
-        if constexpr (BACK) {
-            const Rsrc ro = grad_rows<EO>(p.dout, rows.x + j * kGC, h, p.H, V,
-                                          min(kGC, rows.y - j * kGC));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < CT; ++c)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        o[i][c][s] = load1<EO>(ro, ((uint32_t)(16 * i + 4 * gq + s) * p.H * V +
-                                                    col + 16 * c) * EO::kBytes);
+                    o[c][s] = grad_raw1<EO>(ro, ((uint32_t)(16 * w + 4 * gq + s) * H * V + col +
+                                                 16 * c) * EO::kBytes);
         }
     };
-    auto load_last = [&](const GradWork<K> &ws) {
-        const Rsrc r = grad_floats(BACK ? ws.Wt() : ws.Kbt(), kGC * K);
+    auto load_middle = [&](const GradWork<K> &ws) {
         const Rsrc rq = grad_floats(ws.Qt(), kGC * K), rd = grad_floats(ws.decay(), K);
 #pragma unroll
         for (int T = 0; T < NT; ++T) {
             decay[T] = load4<F32>(rd, 4 * (c0 + 16 * T + 4 * gq));
+            if constexpr (BACK)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int e = 4 * ((c0 + 16 * T + x) * kGC + 16 * t + 4 * gq);
-                rhs[T][t] = load4<F32>(r, e);
-                if constexpr (BACK) qt[T][t] = load4<F32>(rq, e);
-            }
+                for (int t = 0; t < 4; ++t)
+                    qt[T][t] =
+                        load4<F32>(rq, 4 * ((c0 + 16 * T + x) * kGC + 16 * t + 4 * gq));
         }
+    };
+    auto load_last = [&](const GradWork<K> &ws) {
+        const Rsrc r = grad_floats(BACK ? ws.Wt() : ws.Kbt(), kGC * K);
+#pragma unroll
+        for (int T = 0; T < NT; ++T)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                rhs[T][t] = load4<F32>(r, 4 * ((c0 + 16 * T + x) * kGC + 16 * t + 4 * gq));
     };
     auto chunk_of = [&](int j) { return BACK ? chunks - 1 - j : j; };
     if (chunks > 0) {
-        const GradWork<K> ws(p, slot0 + chunk_of(0), h);
+        const GradWork<K> ws(work, V, (long)(slot0 + chunk_of(0)) * H + h);
+        load_dout(chunk_of(0));
         load_first(ws);
+        load_join(ws);
+        load_middle(ws);
         load_last(ws);
-        load_join(ws, chunk_of(0));
     }
     for (int j = 0; j < chunks; ++j) {
-        const GradWork<K> ws(p, slot0 + chunk_of(j), h);
+        const GradWork<K> ws(work, V, (long)(slot0 + chunk_of(j)) * H + h);
         const int jn = chunk_of(min(j + 1, chunks - 1));
-        const GradWork<K> next(p, slot0 + jn, h);
-        float(*mine)[4 * CT][kWave * 4] = joined[j & 1];
+        const GradWork<K> next(work, V, (long)(slot0 + jn) * H + h);
+        if constexpr (BACK)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                f4 v;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) v[s] = scale * grad_widen<EO>(o[c][s]);
+                as4(&lds.o[w * CT + c][lane * 4]) = v;
+            }
+        load_dout(jn);
         f4 acc[4][CT];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -634,7 +679,7 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < CT; ++c) as4(&mine[w][i * CT + c][lane * 4]) = acc[i][c];
+            for (int c = 0; c < CT; ++c) as4(&lds.part[w][i * CT + c][lane * 4]) = acc[i][c];
         {
             const Rsrc r = grad_floats(BACK ? ws.D() : ws.S(), K * V);
 #pragma unroll
@@ -646,51 +691,49 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
                         grad_store1<F32>(
                             r, 4 * ((c0 + 16 * T + 4 * gq + s) * V + col + 16 * c), S[T][c][s]);
         }
-#pragma unroll
-        for (int T = 0; T < NT; ++T)
+        grad_lds_barrier();
+        {
+            const Rsrc r = grad_floats(BACK ? ws.U() : ws.X(), kGC * V);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
+                const int e = w * CT + c;
+                const f4 sum =
+                    (as4(&lds.part[0][e][lane * 4]) + as4(&lds.part[1][e][lane * 4])) +
+                    (as4(&lds.part[2][e][lane * 4]) + as4(&lds.part[3][e][lane * 4]));
+                const f4 y = BACK ? x0[c] + sum : x0[c] - sum;
+                as4(&lds.u[e][lane * 4]) = (BACK ? -beta : beta) * y;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    grad_store1<F32>(r, 4 * ((16 * w + 4 * gq + s) * V + col + 16 * c), y[s]);
+            }
+        }
+        load_join(next);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            f4 og[4];
+            if constexpr (BACK)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) og[t] = as4(&lds.o[t * CT + c][lane * 4]);
+#pragma unroll
+            for (int T = 0; T < NT; ++T) {
                 S[T][c] *= decay[T];
                 if constexpr (BACK)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        S[T][c] = mm16(qt[T][t], o[t][c] * p.scale, S[T][c]);
+                    for (int t = 0; t < 4; ++t) S[T][c] = mm16(qt[T][t], og[t], S[T][c]);
             }
-        grad_lds_barrier();
-        f4 u[4][CT];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                const f4 sum = (as4(&mine[0][i * CT + c][lane * 4]) +
-                                as4(&mine[1][i * CT + c][lane * 4])) +
-                               (as4(&mine[2][i * CT + c][lane * 4]) +
-                                as4(&mine[3][i * CT + c][lane * 4]));
-                u[i][c] = BACK ? x0[i][c] + sum : x0[i][c] - sum;
-            }
-        {  // wavefront w keeps tile row w
-            const Rsrc r = grad_floats(BACK ? ws.U() : ws.X(), kGC * V);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i == w)
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            grad_store1<F32>(r, 4 * ((16 * i + 4 * gq + s) * V + col + 16 * c),
-                                             u[i][c][s]);
         }
+        load_middle(next);
+        grad_lds_barrier();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < CT; ++c) {
+            f4 u[4];
 #pragma unroll
-            for (int c = 0; c < CT; ++c) u[i][c] = (BACK ? -beta[i] : beta[i]) * u[i][c];
-        load_join(next, jn);
+            for (int t = 0; t < 4; ++t) u[t] = as4(&lds.u[t * CT + c][lane * 4]);
 #pragma unroll
-        for (int T = 0; T < NT; ++T)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) S[T][c] = mm16(rhs[T][t], u[t][c], S[T][c]);
+                for (int T = 0; T < NT; ++T) S[T][c] = mm16(rhs[T][t], u[t], S[T][c]);
+        }
         load_last(next);
     }
     if (BACK && pool.base != nullptr) {
@@ -711,15 +754,16 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
 // apart, which puts them on one XCD and its L2.
 template <class EO, int K, int CT>
 __global__ __launch_bounds__(256, 2) void kda_grad_walk_kernel(DeltaGradProblem p, int parts) {
-    __shared__ __align__(16) float joined[2][4][4 * CT][kWave * 4];
-    const long group = blockIdx.x / (8 * parts), in = blockIdx.x % (8 * parts);
-    const long walk = group * 8 + in % 8;
-    if (walk >= (long)p.req.num_seqs * p.H) return;
-    const int part = (int)(in / 8), h = (int)(walk % p.H), n = (int)(walk / p.H);
+    __shared__ __align__(16) GradWalkLds<CT> lds;
+    const int group = blockIdx.x / (8u * parts), in = blockIdx.x % (8u * parts);
+    const int walk = group * 8 + in % 8;
+    if (walk >= p.req.num_seqs * p.H) return;
+    const int part = in / 8, h = __builtin_amdgcn_readfirstlane(walk % p.H);
+    const int n = __builtin_amdgcn_readfirstlane(walk / p.H);
     if (blockIdx.y == 0)
-        grad_walk<EO, K, CT, false>(p, n, h, part, joined);
+        grad_walk<EO, K, CT, false>(p, n, h, part, lds);
     else
-        grad_walk<EO, K, CT, true>(p, n, h, part, joined);
+        grad_walk<EO, K, CT, true>(p, n, h, part, lds);
 }
 
 // ------------------------------------------------------------ gradients of a chunk
@@ -756,7 +800,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
         }
         return;
     }
-    const GradWork<K> ws(p, slot, h);
+    const GradWork<K> ws(p.work, p.V, (long)slot * p.H + h);
     constexpr int kMat = kGC * kMatRow;
     float *Am = lds, *Pm = lds + kMat;  // dA and dP, both halves (first M, in Am)
     float *Ys = lds + 2 * kMat;         // [C][V + 4]
@@ -822,10 +866,6 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
     __syncthreads();
 
     const uint32_t dstep = (uint32_t)p.H * V * EO::kBytes;  // bytes between rows of dout
-    auto dout4 = [&](int r, int c) {
-        return load4<EO>(rdout, r * dstep + (uint32_t)c * EO::kBytes) * p.scale;
-    };
-
     // E = strict(Y X^T) (even wavefronts) and low(O' X^T) (odd): tile rows 3 and 0
     // (0, 1) or 2 and 1 (2, 3)
     {
@@ -835,37 +875,60 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
 #pragma unroll
         for (int j = 0; j < 4; ++j) up[j] = zero4;
         dn[0] = dn[1] = zero4;
+        struct Step {
+            f4 xv[4], a, b;
+        };
+        auto load = [&](int T) {  // the next step's operands while this one's are multiplied
+            const int c = 16 * T + 4 * gq;
+            Step v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v.xv[j] = load4<F32>(rX, 4 * ((16 * j + x) * V + c));
+            if (isP) {
+                v.a = load4<EO>(rdout, (16 * hi + x) * dstep + (uint32_t)c * EO::kBytes);
+                v.b = load4<EO>(rdout, (16 * lo + x) * dstep + (uint32_t)c * EO::kBytes);
+            } else {
+                v.a = as4(&Ys[(16 * hi + x) * VR + c]);
+                v.b = as4(&Ys[(16 * lo + x) * VR + c]);
+            }
+            return v;
+        };
+        Step now = load(0);
 #pragma unroll 1
         for (int T = 0; T < V / 16; ++T) {
-            const int c = 16 * T + 4 * gq;
-            f4 xv[4];
+            const Step next = load(min(T + 1, V / 16 - 1));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) xv[j] = load4<F32>(rX, 4 * ((16 * j + x) * V + c));
-            const f4 a = isP ? dout4(16 * hi + x, c) : as4(&Ys[(16 * hi + x) * VR + c]);
-            const f4 b = isP ? dout4(16 * lo + x, c) : as4(&Ys[(16 * lo + x) * VR + c]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j <= hi) {
-                    up[j] = mm16(a, xv[j], up[j]);
-                    if (j < 2 && j <= lo) dn[j] = mm16(b, xv[j], dn[j]);
-                }
+            for (int j = 0; j < 3; ++j) up[j] = mm16(now.a, now.xv[j], up[j]);
+            if (hi == 3) up[3] = mm16(now.a, now.xv[3], up[3]);
+            dn[0] = mm16(now.b, now.xv[0], dn[0]);
+            if (lo == 1) dn[1] = mm16(now.b, now.xv[1], dn[1]);
+            now = next;
         }
+        // both halves of dA or dP; of a tile on the diagonal only what is below it
+        float *mat = isP ? Pm : Am;
         float colsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const Rsrc rA = grad_floats(ws.A(), kGC * kGC);
+        const float factor = isP ? p.scale : -1.0f;
         auto place = [&](int i, int j, f4 v) {
-            const int c = 16 * j + x;
-            const float beta = bs[c];
-            float *mat = isP ? Pm : Am;
+            const int c = 16 * j + x, r0 = 16 * i + 4 * gq;
+            if (!isP) {
+                f4 a;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * i + 4 * gq + s;
-                float e = v[s];
-                if (isP) {
-                    if (r >= c) mat[r * kMatRow + c] = mat[c * kMatRow + r] = e * beta;
-                } else {
-                    e = r > c ? e : 0.0f;
-                    colsum[j] = __builtin_fmaf(r > c ? ws.A()[r * kGC + c] : 0.0f, e, colsum[j]);
-                    if (r > c) mat[r * kMatRow + c] = mat[c * kMatRow + r] = -e * beta;
-                    if (r == c) mat[r * kMatRow + c] = 0.0f;
+                for (int s = 0; s < 4; ++s) a[s] = load1<F32>(rA, 4 * ((r0 + s) * kGC + c));
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    colsum[j] = __builtin_fmaf(r0 + s > c ? a[s] : 0.0f, v[s], colsum[j]);
+            }
+            v *= factor * bs[c];
+            if (i > j) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) mat[(r0 + s) * kMatRow + c] = v[s];
+                as4(&mat[c * kMatRow + r0]) = v;
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int r = r0 + s;
+                    if (r > c) mat[c * kMatRow + r] = v[s];
+                    if (r >= c) mat[r * kMatRow + c] = isP || r > c ? v[s] : 0.0f;
                 }
             }
         };
@@ -907,26 +970,37 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
 #pragma unroll
         for (int i = 0; i < 4; ++i) dq[i] = dk[i] = ke[i] = zero4;
         float both = 0.0f;
+        struct Step {
+            f4 s, d, o[4], x[4];
+        };
+        auto load = [&](int T) {
+            const int v = 16 * T + 4 * gq;
+            Step r;
+            r.s = load4<F32>(rS, 4 * (c * V + v));
+            r.d = load4<F32>(rS, 4 * ((K + c) * V + v));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r.o[i] = load4<EO>(rdout, (16 * i + x) * dstep + (uint32_t)v * EO::kBytes);
+                r.x[i] = load4<F32>(rX, 4 * ((16 * i + x) * V + v));
+            }
+            return r;
+        };
+        float beta[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) beta[i] = bs[16 * i + x];
+        Step at = load(0);
 #pragma unroll 1
         for (int T = 0; T < V / 16; ++T) {
-            const int v = 16 * T + 4 * gq;
-            const f4 s4 = load4<F32>(rS, 4 * (c * V + v));
-            const f4 d4 = load4<F32>(rS, 4 * ((K + c) * V + v));
-            f4 o[4], xx[4];
+            const Step next = load(min(T + 1, V / 16 - 1));
+#pragma unroll
+            for (int s = 0; s < 4; ++s) both = __builtin_fmaf(at.s[s], at.d[s], both);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                o[i] = load4<EO>(rdout, (16 * i + x) * dstep + (uint32_t)v * EO::kBytes);
-                xx[i] = load4<F32>(rX, 4 * ((16 * i + x) * V + v));
+                dq[i] = mm16(at.o[i], at.s, dq[i]);
+                dk[i] = mm16(as4(&Ys[(16 * i + x) * VR + 16 * T + 4 * gq]), at.s, dk[i]);
+                ke[i] = mm16(at.x[i] * beta[i], at.d, ke[i]);
             }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) both = __builtin_fmaf(s4[s], d4[s], both);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * i + x;
-                dq[i] = mm16(o[i], s4, dq[i]);
-                dk[i] = mm16(as4(&Ys[r * VR + v]), s4, dk[i]);
-                ke[i] = mm16(xx[i] * bs[r], d4, ke[i]);
-            }
+            at = next;
         }
         both = add_rows32(add_rows16(both));
         __builtin_amdgcn_sched_barrier(0);
@@ -968,13 +1042,14 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
             lane_swap16(part[0], part[1]);
             lane_swap16(part[2], part[3]);
         };
+        // (by factors of 0 and 1: selections become branches)
+        const float u1 = gq >= 1, u2 = gq >= 2, u3 = gq >= 3, l0 = gq < 1, l1 = gq < 2, l2 = gq < 3;
+        const float is0 = gq == 0, is1 = gq == 1, is2 = gq == 2, is3 = gq == 3;
         auto earlier = [&](const float (&o)[4]) {
-            const float a = o[0] + o[1];
-            return gq == 0 ? 0.0f : gq == 1 ? o[0] : gq == 2 ? a : a + o[2];
+            return __builtin_fmaf(u3, o[2], __builtin_fmaf(u2, o[1], u1 * o[0]));
         };
         auto later = [&](const float (&o)[4]) {
-            const float a = o[2] + o[3];
-            return gq == 3 ? 0.0f : gq == 2 ? o[3] : gq == 1 ? a : o[1] + a;
+            return __builtin_fmaf(l0, o[1], __builtin_fmaf(l1, o[2], l2 * o[3]));
         };
         float total[4], next8[4];  // next8: of the other group in the token's half of 16
 #pragma unroll
@@ -982,7 +1057,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
             const f4 in = in4(g[t]);
             float o[4];
             groups(in[3], o);
-            next8[t] = gq == 3 ? o[2] : gq == 0 ? o[1] : 0.0f;
+            next8[t] = __builtin_fmaf(is3, o[2], is0 * o[1]);
             pre[t] = in + earlier(o);
             suf[t] = out4(g[t]) + later(o);
             total[t] = (o[0] + o[1]) + (o[2] + o[3]);
@@ -1086,7 +1161,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
                 } else {
                     float o[4];
                     groups((r[0] + r[1]) + (r[2] + r[3]), o);
-                    const float more = gq == 2 ? o[3] : gq == 1 ? o[0] : 0.0f;
+                    const float more = __builtin_fmaf(is2, o[3], is1 * o[0]);
                     dg[t] += ((gq & 2) ? from4(r) : before4(r)) + more;
                 }
                 now(t);
@@ -1231,7 +1306,7 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     const long walks = (long)p.req.num_seqs * p.H, groups = (walks + 7) / 8;
-    if (walks * (p.V / 32) >= 1024) {
+    if (walks * (p.V / 32) >= 1024 && !getenv("CT1")) {
         const int parts = p.V / 32;
         hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 2>), dim3((unsigned)(groups * 8 * parts), 2),
                            dim3(256), 0, stream, p, parts);
