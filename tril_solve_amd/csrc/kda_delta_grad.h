@@ -37,6 +37,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "bf16_parts.h"
 #include "layer_device.h"
 #include "tril_launch.h"
 
@@ -194,6 +195,16 @@ __device__ __forceinline__ void grad_store1<BF16>(Rsrc r, uint32_t off, float v)
 template <>
 __device__ __forceinline__ void grad_store1<F16>(Rsrc r, uint32_t off, float v) {
     __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (_Float16)v), r, off, 0, 0);
+}
+
+template <class E>
+__device__ __forceinline__ void grad_store4(Rsrc r, uint32_t off, f4 v) {
+    if constexpr (E::kBytes == 4) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(w4, v), r, off, 0, 0);
+    } else {
+        const w2 o = {Elem<E>::pack(v[0], v[1]), Elem<E>::pack(v[2], v[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(o, r, off, 0, 0);
+    }
 }
 
 // A gate in powers of two. NaN stays (a comparison with it is false).
@@ -768,21 +779,43 @@ __global__ __launch_bounds__(256, 2) void kda_grad_walk_kernel(DeltaGradProblem 
 
 // ------------------------------------------------------------ gradients of a chunk
 
+// LDS of the last kernel (bytes): parts of Y and X of up to 128 value columns
+// (rows 16 bytes apart in their banks), dout if it is bfloat16 (one part), the two
+// matrices (first the inverse in dA's place), and per token beta, X.dU, the column
+// sums of A * E by tile rows and, with one gate per head, dg by wavefronts.
+template <int K>
+struct GradLds {
+    static constexpr int VB = 128, RS = 2 * VB + 16, PART = kGC * RS, kMat = kGC * kMatRow * 4;
+    static constexpr int Y = 0, X = Y + kParts * PART, O = X + kParts * PART, A = O + PART;
+    static constexpr int P = A + kMat, BETA = P + kMat, XDU = BETA + kGC * 4;
+    static constexpr int COLS = XDU + kGC * 4, DG = COLS + 4 * kGC * 4;
+    static constexpr int kBytes = DG + K / 16 * kGC * 4;
+    static_assert(kBytes <= 160 * 1024);
+};
+// Eight adjacent elements of dout as an operand: one part if they are bfloat16.
+template <class EO>
+__device__ __forceinline__ Operand grad_operand(Rsrc r, uint32_t off) {
+    const f4 a = load4<EO>(r, off), b = load4<EO>(r, off + 4 * EO::kBytes);
+    return join(split4(a), split4(b));
+}
+
+// A wavefront to every 16 key channels.
 template <class E, class EO, int K>
-__global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem p) {
-    constexpr int NT = K / 16;
-    extern __shared__ __align__(16) float lds[];
+__global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel(DeltaGradProblem p) {
+    typedef GradLds<K> L;
+    constexpr int NW = K / 16, VB = L::VB;
+    constexpr bool kExact = EO::kBytes == 2 && !__is_same(EO, F16);  // dout is one bfloat16 part
+    __shared__ __align__(16) char lds[L::kBytes];
     const int lane = threadIdx.x & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int x = lane & 15, gq = lane >> 4;
     const int h = (int)(blockIdx.x % p.H), slot = (int)(blockIdx.x / p.H);
     const GradChunk ch = grad_chunk(p.req, slot, lane);
     if (ch.len == 0) return;
-    const int V = p.V, VR = V + 4, len = ch.len;
-    const int hk = h / (p.H / p.Hk);
+    const int V = p.V, len = ch.len, hk = h / (p.H / p.Hk);
     typedef typename E::T T_;
     if (p.grad.slot != nullptr && request_slot(p.grad, ch.request) < 0) {  // padding: zeros
-        for (int r = w; r < len; r += 4) {
+        for (int r = w; r < len; r += NW) {
             const long row = ch.row + r, at = row * p.H + h;
             for (int c = lane; c < V; c += kWave)
                 grad_put<E>(static_cast<T_ *>(p.dv) + at * V + c, 0.0f);
@@ -801,210 +834,252 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
         return;
     }
     const GradWork<K> ws(p.work, p.V, (long)slot * p.H + h);
-    constexpr int kMat = kGC * kMatRow;
-    float *Am = lds, *Pm = lds + kMat;  // dA and dP, both halves (first M, in Am)
-    float *Ys = lds + 2 * kMat;         // [C][V + 4]
-    float *bs = Ys + kGC * VR;          // beta [C], X.dU [C], column sums [2][C]
-    float *xdu = bs + kGC, *cols = xdu + kGC;
-    float *dgs = cols + 2 * kGC;        // [4][C] per wavefront (one gate per head)
+    float *Am = reinterpret_cast<float *>(lds + L::A), *Pm = reinterpret_cast<float *>(lds + L::P);
+    float *bs = reinterpret_cast<float *>(lds + L::BETA);
+    float *xdu = reinterpret_cast<float *>(lds + L::XDU);
+    float *cols = reinterpret_cast<float *>(lds + L::COLS);
+    float *dgs = reinterpret_cast<float *>(lds + L::DG);
     const f4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     // rows of this chunk and head; loads behind the last give 0, stores are dropped
     const Rsrc rdout = grad_rows<EO>(p.dout, ch.row, h, p.H, V, len);
     const Rsrc rX = grad_floats(ws.X(), kGC * V), rU = grad_floats(ws.U(), kGC * V);
-
-    for (int e = threadIdx.x; e < kGC * kGC / 4; e += 256) {
-        const int r = e / (kGC / 4), c = e % (kGC / 4) * 4;
-        if (c / 16 <= r / 16) as4(&Am[r * kMatRow + c]) = as4(ws.M() + r * kGC + c);
-    }
-    if (threadIdx.x < kGC)
-        bs[threadIdx.x] = (int)threadIdx.x < len
-                              ? p.beta[(long)(ch.row + threadIdx.x) * p.H + h] : 0.0f;
-    {  // X.dU: four lanes to a row
-        const int r = threadIdx.x >> 2;
-        float sum = 0.0f;
-        for (int c = 4 * (threadIdx.x & 3); c < V; c += 16) {
-            const f4 a = load4<F32>(rX, 4 * (r * V + c)), b = load4<F32>(rU, 4 * (r * V + c));
-#pragma unroll
-            for (int s = 0; s < 4; ++s) sum = __builtin_fmaf(a[s], b[s], sum);
-        }
-        sum = lane_add<0x4E>(lane_add<0xB1>(sum));
-        if ((threadIdx.x & 3) == 0) xdu[r] = sum;
-    }
-    __syncthreads();
-
-    // Y = M^T (B dU)
+    const Rsrc rS = grad_floats(ws.S(), 2 * K * V);  // and dS behind it
     const Rsrc rdv = grad_rows<E>(p.dv, ch.row, h, p.H, V, len);
-#pragma unroll 1
-    for (int n = w; n < V / 16; n += 4) {
-        f4 b[4];
+    const uint32_t dstep = (uint32_t)p.H * V * EO::kBytes;  // bytes between rows of dout
+    const uint32_t vstep = (uint32_t)p.H * V * E::kBytes;
+    const int c = 16 * w + x;  // this lane's key channel
+
+    // this wavefront's rows of S and dS, 32 columns to a step
+    f4 s4[VB / 32][2], d4[VB / 32][2];
+    auto load_states = [&](int vb) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < VB / 32; ++t)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * t + 4 * gq + s;
-                b[t][s] = bs[r] * load1<F32>(rU, 4 * (r * V + 16 * n + x));
+            for (int e = 0; e < 2; ++e) {
+                const int v = vb + 32 * t + 8 * gq + 4 * e;
+                const bool in = vb + 32 * t < V;
+                s4[t][e] = load4<F32>(rS, in ? 4 * (c * V + v) : kOffMasked);
+                d4[t][e] = load4<F32>(rS, in ? 4 * ((K + c) * V + v) : kOffMasked);
             }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f4 acc = zero4;
-#pragma unroll
-            for (int t = i; t < 4; ++t) {
-                f4 a;
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    a[s] = Am[(16 * t + 4 * gq + s) * kMatRow + 16 * i + x];
-                acc = mm16(a, b[t], acc);
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * i + 4 * gq + s;
-                Ys[r * VR + 16 * n + x] = acc[s];
-                grad_store1<E>(rdv, (uint32_t)(r * p.H * V + 16 * n + x) * E::kBytes, acc[s]);
-            }
-        }
+    };
+    load_states(0);
+    for (int e = threadIdx.x; e < kGC * kGC / 4; e += K * 4) {
+        const int r = e / (kGC / 4), col = e % (kGC / 4) * 4;
+        if (col / 16 <= r / 16) as4(&Am[r * kMatRow + col]) = as4(ws.M() + r * kGC + col);
+    }
+    if (threadIdx.x < kGC) {
+        bs[threadIdx.x] = load1<F32>(grad_floats(ws.beta(), kGC), 4 * threadIdx.x);
+        xdu[threadIdx.x] = 0.0f;
     }
     __syncthreads();
 
-    const uint32_t dstep = (uint32_t)p.H * V * EO::kBytes;  // bytes between rows of dout
-    // E = strict(Y X^T) (even wavefronts) and low(O' X^T) (odd): tile rows 3 and 0
-    // (0, 1) or 2 and 1 (2, 3)
-    {
-        const bool isP = w & 1;
-        const int hi = w < 2 ? 3 : 2, lo = w < 2 ? 0 : 1;
-        f4 up[4], dn[2];
+    // O' S^T, Y S^T, X dS^T, the rows of S * dS, and tile rows of Y X^T and O' X^T:
+    // row w & 3 of one of them, or, with four wavefronts, row w of both
+    constexpr int NJ = 8 / NW;
+    f4 dq[4], dk[4], ke[4], ex[NJ][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) up[j] = zero4;
-        dn[0] = dn[1] = zero4;
-        struct Step {
-            f4 xv[4], a, b;
-        };
-        auto load = [&](int T) {  // the next step's operands while this one's are multiplied
-            const int c = 16 * T + 4 * gq;
-            Step v;
+    for (int i = 0; i < 4; ++i) {
+        dq[i] = dk[i] = ke[i] = zero4;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v.xv[j] = load4<F32>(rX, 4 * ((16 * j + x) * V + c));
-            if (isP) {
-                v.a = load4<EO>(rdout, (16 * hi + x) * dstep + (uint32_t)c * EO::kBytes);
-                v.b = load4<EO>(rdout, (16 * lo + x) * dstep + (uint32_t)c * EO::kBytes);
-            } else {
-                v.a = as4(&Ys[(16 * hi + x) * VR + c]);
-                v.b = as4(&Ys[(16 * lo + x) * VR + c]);
-            }
-            return v;
-        };
-        Step now = load(0);
+        for (int j = 0; j < NJ; ++j) ex[j][i] = zero4;
+    }
+    float both = 0.0f;
+    const int tr = w & 3;
 #pragma unroll 1
-        for (int T = 0; T < V / 16; ++T) {
-            const Step next = load(min(T + 1, V / 16 - 1));
+    for (int vb = 0; vb < V; vb += VB) {
+        const int nv = min(VB, V - vb);
+        if (vb > 0) __syncthreads();
+        {  // X and dout to LDS; X.dU, NW lanes to a row
+            const int r = threadIdx.x / NW;
+            float sum = 0.0f;
+            for (int col = 4 * (threadIdx.x % NW); col < nv; col += 4 * NW) {
+                const f4 a = load4<F32>(rX, 4 * (r * V + vb + col));
+                const f4 b = load4<F32>(rU, 4 * (r * V + vb + col));
 #pragma unroll
-            for (int j = 0; j < 3; ++j) up[j] = mm16(now.a, now.xv[j], up[j]);
-            if (hi == 3) up[3] = mm16(now.a, now.xv[3], up[3]);
-            dn[0] = mm16(now.b, now.xv[0], dn[0]);
-            if (lo == 1) dn[1] = mm16(now.b, now.xv[1], dn[1]);
-            now = next;
-        }
-        // both halves of dA or dP; of a tile on the diagonal only what is below it
-        float *mat = isP ? Pm : Am;
-        float colsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const Rsrc rA = grad_floats(ws.A(), kGC * kGC);
-        const float factor = isP ? p.scale : -1.0f;
-        auto place = [&](int i, int j, f4 v) {
-            const int c = 16 * j + x, r0 = 16 * i + 4 * gq;
-            if (!isP) {
-                f4 a;
+                for (int s = 0; s < 4; ++s) sum = __builtin_fmaf(a[s], b[s], sum);
+                const Half parts = split4(a);
+                char *at = lds + L::X + r * L::RS + 2 * col;
 #pragma unroll
-                for (int s = 0; s < 4; ++s) a[s] = load1<F32>(rA, 4 * ((r0 + s) * kGC + c));
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    colsum[j] = __builtin_fmaf(r0 + s > c ? a[s] : 0.0f, v[s], colsum[j]);
+                for (int i = 0; i < kParts; ++i)
+                    *reinterpret_cast<w2 *>(at + i * L::PART) = parts.p[i];
+                if constexpr (kExact)
+                    *reinterpret_cast<w2 *>(lds + L::O + r * L::RS + 2 * col) =
+                        __builtin_bit_cast(w2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                   rdout, r * dstep + 2 * (vb + col), 0, 0));
             }
-            v *= factor * bs[c];
-            if (i > j) {
+            sum = lane_add<0x4E>(lane_add<0xB1>(sum));
+            if (NW == 8) sum = lane_add<0x141>(sum);
+            if (threadIdx.x % NW == 0) xdu[r] += sum;
+        }
+        // Y = M^T (B dU), its transpose in the accumulators: columns of four
+        for (int n = w; n < nv / 16; n += NW) {
+            f4 b[4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) mat[(r0 + s) * kMatRow + c] = v[s];
-                as4(&mat[c * kMatRow + r0]) = v;
-            } else {
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const int r = r0 + s;
-                    if (r > c) mat[c * kMatRow + r] = v[s];
-                    if (r >= c) mat[r * kMatRow + c] = isP || r > c ? v[s] : 0.0f;
+                    const int r = 16 * t + 4 * gq + s;
+                    b[t][s] = bs[r] * load1<F32>(rU, 4 * (r * V + vb + 16 * n + x));
                 }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f4 acc = zero4;
+#pragma unroll
+                for (int t = i; t < 4; ++t) {
+                    f4 a;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        a[s] = Am[(16 * t + 4 * gq + s) * kMatRow + 16 * i + x];
+                    acc = mm16(b[t], a, acc);
+                }
+                const int r = 16 * i + x, col = 16 * n + 4 * gq;
+                const Half parts = split4(acc);
+                char *at = lds + L::Y + r * L::RS + 2 * col;
+#pragma unroll
+                for (int j = 0; j < kParts; ++j)
+                    *reinterpret_cast<w2 *>(at + j * L::PART) = parts.p[j];
+                grad_store4<E>(rdv, r * vstep + (uint32_t)(vb + col) * E::kBytes, acc);
+            }
+        }
+        __syncthreads();
+        auto rows_of = [&](int base, int i, int t) {  // tile row i, columns 32 t ..
+            const char *at = lds + base + (16 * i + x) * L::RS + 64 * t + 16 * gq;
+            Operand o;
+#pragma unroll
+            for (int j = 0; j < kParts; ++j)
+                o.p[j] = *reinterpret_cast<const w4 *>(at + j * L::PART);
+            return o;
+        };
+        // O' tile rows times b's parts
+        auto dout_mul = [&](int i, int t, const Operand &b, f4 acc) {
+            if constexpr (kExact) {
+                const w4 a = *reinterpret_cast<const w4 *>(lds + L::O + (16 * i + x) * L::RS +
+                                                           64 * t + 16 * gq);
+                return mfma(a, b.p[0], mfma(a, b.p[1], mfma(a, b.p[2], acc)));
+            } else {
+                const Operand a = grad_operand<EO>(
+                    rdout,
+                    (16 * i + x) * dstep + (uint32_t)(vb + 32 * t + 8 * gq) * EO::kBytes);
+#pragma unroll
+                for (int j = 0; j < 6; ++j) acc = mfma(a.p[part_a(j)], b.p[part_b(j)], acc);
+                return acc;
             }
         };
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= hi) place(hi, j, up[j]);
+        for (int t = 0; t < VB / 32; ++t) {
+            if (32 * t >= nv) break;
+            // E, dP
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (j <= lo) place(lo, j, dn[j]);
-        if (!isP)
+            for (int j = 0; j < NJ; ++j) {
+                const bool isP = NW == 8 ? w >= 4 : j == 1;
+                if (isP) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float sum = add_rows32(add_rows16(colsum[j]));
-                if (gq == 0) cols[(w >> 1) * kGC + 16 * j + x] = sum;
+                    for (int i = 0; i < 4; ++i)
+                        if (i <= tr) ex[j][i] = dout_mul(tr, t, rows_of(L::X, i, t), ex[j][i]);
+                } else {
+                    const Operand a = rows_of(L::Y, tr, t);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i <= tr) {
+                            const Operand b = rows_of(L::X, i, t);
+#pragma unroll
+                            for (int m = 0; m < 6; ++m)
+                                ex[j][i] = mfma(a.p[part_a(m)], b.p[part_b(m)], ex[j][i]);
+                        }
+                }
+            }
+            // the states' products
+            const Operand S = join(split4(s4[t][0]), split4(s4[t][1]));
+            const Operand D = join(split4(d4[t][0]), split4(d4[t][1]));
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) both = __builtin_fmaf(s4[t][e][s], d4[t][e][s], both);
+            {
+                Operand a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = rows_of(L::Y, i, t);
+#pragma unroll
+                for (int m = 0; m < 6; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dk[i] = mfma(a[i].p[part_a(m)], S.p[part_b(m)], dk[i]);
+            }
+            {
+                Operand a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = rows_of(L::X, i, t);
+#pragma unroll
+                for (int m = 0; m < 6; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        ke[i] = mfma(a[i].p[part_a(m)], D.p[part_b(m)], ke[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dq[i] = dout_mul(i, t, S, dq[i]);
+        }
+        if (vb + VB < V) load_states(vb + VB);
+    }
+    both = add_rows32(add_rows16(both));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ke[i] *= as4(&bs[16 * i + 4 * gq]);
+    __syncthreads();
+
+    // E and dP: both halves of dA and dP to LDS; of a tile on the diagonal only
+    // what is below it
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        const bool isP = NW == 8 ? w >= 4 : j == 1;
+        float *mat = isP ? Pm : Am;
+        const float factor = isP ? p.scale : -1.0f;
+        const Rsrc rA = grad_floats(ws.A(), kGC * kGC);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i <= tr) {
+                const int col = 16 * i + x, r0 = 16 * tr + 4 * gq;
+                f4 v = ex[j][i];
+                if (!isP) {
+                    float sum = 0.0f;
+                    f4 a;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) a[s] = load1<F32>(rA, 4 * ((r0 + s) * kGC + col));
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        sum = __builtin_fmaf(r0 + s > col ? a[s] : 0.0f, v[s], sum);
+                    sum = add_rows32(add_rows16(sum));
+                    if (gq == 0) cols[tr * kGC + col] = sum;
+                }
+                v *= factor * bs[col];
+                if (i < tr) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) mat[(r0 + s) * kMatRow + col] = v[s];
+                    as4(&mat[col * kMatRow + r0]) = v;
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int r = r0 + s;
+                        if (r > col) mat[col * kMatRow + r] = v[s];
+                        if (r >= col) mat[r * kMatRow + col] = isP || r > col ? v[s] : 0.0f;
+                    }
+                }
             }
     }
     __syncthreads();
-    if ((int)threadIdx.x < len)
-        p.dbeta[(long)(ch.row + threadIdx.x) * p.H + h] =
-            xdu[threadIdx.x] - cols[threadIdx.x] - cols[kGC + threadIdx.x];
+    if ((int)threadIdx.x < len) {
+        const int r = threadIdx.x;
+        float sum = xdu[r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum -= i >= r / 16 ? cols[i * kGC + r] : 0.0f;
+        p.dbeta[(long)(ch.row + r) * p.H + h] = sum;
+    }
 
-    // the rest by key channels: 16 to a wavefront at a time
+    // the rest by key channels, in registers
     const bool per_channel = p.gate_stride == K;
     const Rsrc rk = grad_rows<E>(p.k, ch.row, hk, p.Hk, K, len);
     const Rsrc rq = grad_rows<E>(p.q, ch.row, hk, p.Hk, K, len);
     const Rsrc rg = grad_rows<F32>(p.g, ch.row, h, p.H, p.gate_stride, len);
-    const Rsrc rS = grad_floats(ws.S(), 2 * K * V);  // and dS behind it
     const uint32_t kstep = (uint32_t)p.Hk * K, gstep = (uint32_t)p.H * p.gate_stride;
-    f4 dg_head[4] = {zero4, zero4, zero4, zero4};
-#pragma unroll 1
-    for (int n = w; n < NT; n += 4) {
-        // (nothing of the matrices or of the rows' offsets is worth registers
-        // across the channels: they are taken anew)
-        int gq = lane >> 4, x = lane & 15;
-        asm volatile("" : "+v"(gq), "+v"(x) : : "memory");
-        const int c = 16 * n + x;
-        // O' S^T, Y S^T, U dS^T and the rows of S * dS
-        f4 dq[4], dk[4], ke[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dq[i] = dk[i] = ke[i] = zero4;
-        float both = 0.0f;
-        struct Step {
-            f4 s, d, o[4], x[4];
-        };
-        auto load = [&](int T) {
-            const int v = 16 * T + 4 * gq;
-            Step r;
-            r.s = load4<F32>(rS, 4 * (c * V + v));
-            r.d = load4<F32>(rS, 4 * ((K + c) * V + v));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r.o[i] = load4<EO>(rdout, (16 * i + x) * dstep + (uint32_t)v * EO::kBytes);
-                r.x[i] = load4<F32>(rX, 4 * ((16 * i + x) * V + v));
-            }
-            return r;
-        };
-        float beta[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) beta[i] = bs[16 * i + x];
-        Step at = load(0);
-#pragma unroll 1
-        for (int T = 0; T < V / 16; ++T) {
-            const Step next = load(min(T + 1, V / 16 - 1));
-#pragma unroll
-            for (int s = 0; s < 4; ++s) both = __builtin_fmaf(at.s[s], at.d[s], both);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dq[i] = mm16(at.o[i], at.s, dq[i]);
-                dk[i] = mm16(as4(&Ys[(16 * i + x) * VR + 16 * T + 4 * gq]), at.s, dk[i]);
-                ke[i] = mm16(at.x[i] * beta[i], at.d, ke[i]);
-            }
-            at = next;
-        }
-        both = add_rows32(add_rows16(both));
-        __builtin_amdgcn_sched_barrier(0);
-
+    {
         f4 k[4], q[4], g[4], pre[4], suf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -1251,23 +1326,24 @@ __global__ __launch_bounds__(256, 2) void kda_grad_chunk_kernel(DeltaGradProblem
                 }
                 if (per_channel) grad_store1<F32>(rdg, 4 * (r * gstep + c), dg[t][s]);
             }
-        if (!per_channel)
+        if (!per_channel)  // summed over the channels: 16 lanes, then the wavefronts
 #pragma unroll
-            for (int t = 0; t < 4; ++t) dg_head[t] += dg[t];
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const float sum = sum16(dg[t][s]);
+                    if (x == 0) dgs[w * kGC + 16 * t + 4 * gq + s] = sum;
+                }
     }
-    if (!per_channel) {  // summed over the channels: 16 lanes, then the wavefronts
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float sum = sum16(dg_head[t][s]);
-                if (x == 0) dgs[w * kGC + 16 * t + 4 * gq + s] = sum;
-            }
+    if (!per_channel) {
         __syncthreads();
         const int r = threadIdx.x;
-        if (r < len)
-            p.dg[(long)(ch.row + r) * p.H + h] =
-                (dgs[r] + dgs[kGC + r]) + (dgs[2 * kGC + r] + dgs[3 * kGC + r]);
+        if (r < len) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) sum += dgs[i * kGC + r];
+            p.dg[(long)(ch.row + r) * p.H + h] = sum;
+        }
     }
 }
 
@@ -1293,10 +1369,6 @@ __global__ __launch_bounds__(256) void kda_grad_shared_kernel(DeltaGradProblem p
     }
 }
 
-constexpr size_t grad_chunk_lds(int V) {
-    return sizeof(float) * (2 * kGC * kMatRow + kGC * (V + 4) + 8 * kGC);
-}
-
 template <class E, class EO, int K>
 hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream) {
     const unsigned items = (unsigned)((long)p.slots * p.H);
@@ -1317,15 +1389,8 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (p.req.total_tokens > 0) {
-        const auto fn = kda_grad_chunk_kernel<E, EO, K>;
-        const size_t lds = grad_chunk_lds(p.V);
-        if (lds > 64 * 1024) {
-            const hipError_t e = hipFuncSetAttribute(
-                reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
-                (int)lds);
-            if (e != hipSuccess) return e;
-        }
-        hipLaunchKernelGGL(fn, dim3(items), dim3(256), lds, stream, p);
+        hipLaunchKernelGGL((kda_grad_chunk_kernel<E, EO, K>), dim3(items), dim3(K * 4), 0, stream,
+                           p);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (p.Hk != p.H)
             hipLaunchKernelGGL((kda_grad_shared_kernel<E, K>), dim3((unsigned)(p.slots * p.Hk)),
