@@ -56,7 +56,7 @@ struct GradWork {
     int V;
     // floats of one chunk and head
     static __device__ __forceinline__ long size(int V) {
-        return 2L * kGC * kGC + 5L * kGC * K + 2L * kGC * V + 2L * K * V + K + kGC;
+        return 2L * kGC * kGC + 5L * kGC * K + 2L * kGC * V + 2L * K * V + K + kGC + 4;
     }
     __device__ __forceinline__ GradWork(float *work, int V, long item)
         : base(work + item * size(V)), V(V) {}
@@ -69,7 +69,11 @@ struct GradWork {
     __device__ __forceinline__ float *Qt() const { return Kbt() + kGC * K; }       // q e^G, [K][C]
     __device__ __forceinline__ float *decay() const { return Qt() + kGC * K; }     // e^G, [K]
     __device__ __forceinline__ float *beta() const { return decay() + K; }         // [C]
-    __device__ __forceinline__ float *X() const { return beta() + kGC; }           // [C][V]
+    // the first row, the number of rows (0: no such chunk), whether it is padding
+    __device__ __forceinline__ int32_t *chunk() const {
+        return reinterpret_cast<int32_t *>(beta() + kGC);
+    }
+    __device__ __forceinline__ float *X() const { return beta() + kGC + 4; }       // [C][V]
     __device__ __forceinline__ float *U() const { return X() + kGC * V; }          // dU, [C][V]
     __device__ __forceinline__ float *S() const { return U() + kGC * V; }          // [K][V]
     __device__ __forceinline__ float *D() const { return S() + K * V; }            // dS, [K][V]
@@ -242,9 +246,12 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     const int x = lane & 15, gq = lane >> 4;
     const int h = (int)(blockIdx.x % p.H), slot = (int)(blockIdx.x / p.H);
     const GradChunk ch = grad_chunk(p.req, slot, lane);
-    if (ch.len == 0) return;
-    if (p.grad.slot != nullptr && request_slot(p.grad, ch.request) < 0) return;
     const GradWork<K> ws(p.work, p.V, (long)slot * p.H + h);
+    const bool padding =
+        ch.len > 0 && p.grad.slot != nullptr && request_slot(p.grad, ch.request) < 0;
+    if (threadIdx.x == 0)
+        *reinterpret_cast<int4 *>(ws.chunk()) = make_int4(ch.row, ch.len, padding, 0);
+    if (ch.len == 0 || padding) return;
     const int V = p.V, tok = 16 * w + x;
     f4 k[NT], q[NT], pre[NT], suf[NT], tot[NT];
     {  // rows behind the last load 0
@@ -810,11 +817,46 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int x = lane & 15, gq = lane >> 4;
     const int h = (int)(blockIdx.x % p.H), slot = (int)(blockIdx.x / p.H);
-    const GradChunk ch = grad_chunk(p.req, slot, lane);
-    if (ch.len == 0) return;
-    const int V = p.V, len = ch.len, hk = h / (p.H / p.Hk);
+    const GradWork<K> ws(p.work, p.V, (long)slot * p.H + h);
+    float *Am = reinterpret_cast<float *>(lds + L::A), *Pm = reinterpret_cast<float *>(lds + L::P);
+    float *bs = reinterpret_cast<float *>(lds + L::BETA);
+    float *xdu = reinterpret_cast<float *>(lds + L::XDU);
+    float *cols = reinterpret_cast<float *>(lds + L::COLS);
+    float *dgs = reinterpret_cast<float *>(lds + L::DG);
+    const f4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int V = p.V, hk = h / (p.H / p.Hk);
+    const int c = 16 * w + x;  // this lane's key channel
+    // what does not depend on the chunk is loaded before it is known (of slots
+    // without a chunk, whatever lies there)
+    const Rsrc rX = grad_floats(ws.X(), kGC * V), rU = grad_floats(ws.U(), kGC * V);
+    const Rsrc rS = grad_floats(ws.S(), 2 * K * V);  // and dS behind it
+    const Rsrc rM = grad_floats(ws.M(), kGC * kGC);
+    // this wavefront's rows of S and dS, 32 columns to a step
+    f4 s4[VB / 32][2], d4[VB / 32][2];
+    auto load_rows = [&](f4 (&to)[VB / 32][2], int row, int vb) {
+#pragma unroll
+        for (int t = 0; t < VB / 32; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = vb + 32 * t + 8 * gq + 4 * e;
+                to[t][e] = load4<F32>(rS, vb + 32 * t < V ? 4 * (row * V + v) : kOffMasked);
+            }
+    };
+    const int4 where = *reinterpret_cast<const int4 *>(ws.chunk());
+    f4 minv[1024 / (K * 4)];
+#pragma unroll
+    for (int e = 0; e < 1024 / (K * 4); ++e)
+        minv[e] = load4<F32>(rM, 16 * (threadIdx.x + e * K * 4));
+    const float my_beta =
+        threadIdx.x < kGC ? load1<F32>(grad_floats(ws.beta(), kGC), 4 * threadIdx.x) : 0.0f;
+    load_rows(s4, c, 0);
+    const int len = __builtin_amdgcn_readfirstlane(where.y);
+    if (len == 0) return;
+    struct {
+        int row;
+    } ch = {__builtin_amdgcn_readfirstlane(where.x)};
     typedef typename E::T T_;
-    if (p.grad.slot != nullptr && request_slot(p.grad, ch.request) < 0) {  // padding: zeros
+    if (__builtin_amdgcn_readfirstlane(where.z)) {  // padding: zeros
         for (int r = w; r < len; r += NW) {
             const long row = ch.row + r, at = row * p.H + h;
             for (int c = lane; c < V; c += kWave)
@@ -833,42 +875,18 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
         }
         return;
     }
-    const GradWork<K> ws(p.work, p.V, (long)slot * p.H + h);
-    float *Am = reinterpret_cast<float *>(lds + L::A), *Pm = reinterpret_cast<float *>(lds + L::P);
-    float *bs = reinterpret_cast<float *>(lds + L::BETA);
-    float *xdu = reinterpret_cast<float *>(lds + L::XDU);
-    float *cols = reinterpret_cast<float *>(lds + L::COLS);
-    float *dgs = reinterpret_cast<float *>(lds + L::DG);
-    const f4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     // rows of this chunk and head; loads behind the last give 0, stores are dropped
     const Rsrc rdout = grad_rows<EO>(p.dout, ch.row, h, p.H, V, len);
-    const Rsrc rX = grad_floats(ws.X(), kGC * V), rU = grad_floats(ws.U(), kGC * V);
-    const Rsrc rS = grad_floats(ws.S(), 2 * K * V);  // and dS behind it
     const Rsrc rdv = grad_rows<E>(p.dv, ch.row, h, p.H, V, len);
     const uint32_t dstep = (uint32_t)p.H * V * EO::kBytes;  // bytes between rows of dout
     const uint32_t vstep = (uint32_t)p.H * V * E::kBytes;
-    const int c = 16 * w + x;  // this lane's key channel
-
-    // this wavefront's rows of S and dS, 32 columns to a step
-    f4 s4[VB / 32][2], d4[VB / 32][2];
-    auto load_states = [&](int vb) {
 #pragma unroll
-        for (int t = 0; t < VB / 32; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int v = vb + 32 * t + 8 * gq + 4 * e;
-                const bool in = vb + 32 * t < V;
-                s4[t][e] = load4<F32>(rS, in ? 4 * (c * V + v) : kOffMasked);
-                d4[t][e] = load4<F32>(rS, in ? 4 * ((K + c) * V + v) : kOffMasked);
-            }
-    };
-    load_states(0);
-    for (int e = threadIdx.x; e < kGC * kGC / 4; e += K * 4) {
-        const int r = e / (kGC / 4), col = e % (kGC / 4) * 4;
-        if (col / 16 <= r / 16) as4(&Am[r * kMatRow + col]) = as4(ws.M() + r * kGC + col);
+    for (int e = 0; e < 1024 / (K * 4); ++e) {  // (its upper tiles are not read)
+        const int at = threadIdx.x + e * K * 4;
+        as4(&Am[at / 16 * kMatRow + at % 16 * 4]) = minv[e];
     }
     if (threadIdx.x < kGC) {
-        bs[threadIdx.x] = load1<F32>(grad_floats(ws.beta(), kGC), 4 * threadIdx.x);
+        bs[threadIdx.x] = my_beta;
         xdu[threadIdx.x] = 0.0f;
     }
     __syncthreads();
@@ -911,6 +929,7 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
             if (NW == 8) sum = lane_add<0x141>(sum);
             if (threadIdx.x % NW == 0) xdu[r] += sum;
         }
+        if (vb > 0) load_rows(s4, c, vb);
         // Y = M^T (B dU), its transpose in the accumulators: columns of four
         for (int n = w; n < nv / 16; n += NW) {
             f4 b[4];
@@ -941,6 +960,7 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                 grad_store4<E>(rdv, r * vstep + (uint32_t)(vb + col) * E::kBytes, acc);
             }
         }
+        load_rows(d4, K + c, vb);  // (not earlier: registers)
         __syncthreads();
         auto rows_of = [&](int base, int i, int t) {  // tile row i, columns 32 t ..
             const char *at = lds + base + (16 * i + x) * L::RS + 64 * t + 16 * gq;
@@ -968,57 +988,59 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
 #pragma unroll
         for (int t = 0; t < VB / 32; ++t) {
             if (32 * t >= nv) break;
-            // E, dP
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const bool isP = NW == 8 ? w >= 4 : j == 1;
-                if (isP) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i <= tr) ex[j][i] = dout_mul(tr, t, rows_of(L::X, i, t), ex[j][i]);
-                } else {
-                    const Operand a = rows_of(L::Y, tr, t);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i <= tr) {
-                            const Operand b = rows_of(L::X, i, t);
-#pragma unroll
-                            for (int m = 0; m < 6; ++m)
-                                ex[j][i] = mfma(a.p[part_a(m)], b.p[part_b(m)], ex[j][i]);
-                        }
-                }
-            }
             // the states' products
-            const Operand S = join(split4(s4[t][0]), split4(s4[t][1]));
-            const Operand D = join(split4(d4[t][0]), split4(d4[t][1]));
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) both = __builtin_fmaf(s4[t][e][s], d4[t][e][s], both);
             {
-                Operand a[4];
+                const Operand S = join(split4(s4[t][0]), split4(s4[t][1]));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = rows_of(L::Y, i, t);
+                for (int i = 0; i < 4; i += 2) {  // (four at a time lack registers)
+                    const Operand a[2] = {rows_of(L::Y, i, t), rows_of(L::Y, i + 1, t)};
 #pragma unroll
-                for (int m = 0; m < 6; ++m)
+                    for (int m = 0; m < 6; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dk[i] = mfma(a[i].p[part_a(m)], S.p[part_b(m)], dk[i]);
+                        for (int e = 0; e < 2; ++e)
+                            dk[i + e] = mfma(a[e].p[part_a(m)], S.p[part_b(m)], dk[i + e]);
+                    dq[i] = dout_mul(i, t, S, dq[i]);
+                    dq[i + 1] = dout_mul(i + 1, t, S, dq[i + 1]);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
             {
-                Operand a[4];
+                const Operand D = join(split4(d4[t][0]), split4(d4[t][1]));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = rows_of(L::X, i, t);
+                for (int i = 0; i < 4; i += 2) {
+                    const Operand a[2] = {rows_of(L::X, i, t), rows_of(L::X, i + 1, t)};
 #pragma unroll
-                for (int m = 0; m < 6; ++m)
+                    for (int m = 0; m < 6; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        ke[i] = mfma(a[i].p[part_a(m)], D.p[part_b(m)], ke[i]);
+                        for (int e = 0; e < 2; ++e)
+                            ke[i + e] = mfma(a[e].p[part_a(m)], D.p[part_b(m)], ke[i + e]);
+                    // E, dP, whose columns are the same rows of X
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const bool isP = NW == 8 ? w >= 4 : j == 1;
+                        if (i > tr) continue;
+                        if (isP) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                ex[j][i + e] = dout_mul(tr, t, a[e], ex[j][i + e]);
+                        } else {
+                            const Operand y = rows_of(L::Y, tr, t);
+#pragma unroll
+                            for (int m = 0; m < 6; ++m)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    ex[j][i + e] =
+                                        mfma(y.p[part_a(m)], a[e].p[part_b(m)], ex[j][i + e]);
+                        }
+                    }
+                }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dq[i] = dout_mul(i, t, S, dq[i]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (vb + VB < V) load_states(vb + VB);
     }
     both = add_rows32(add_rows16(both));
 #pragma unroll
@@ -1203,52 +1225,72 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
             asm volatile("" : "+v"(g[t]));  // its sums are not worth registers till here
             const f4 a = as4(&Am[(16 * t + x) * kMatRow + 16 * t + 4 * gq]);
             const f4 b = as4(&Pm[(16 * t + x) * kMatRow + 16 * t + 4 * gq]);
+            // levels 4 and 8
+            f4 f[2], e1[2], e2[2], z[2], kf[2], am[2], bm[2];
+            bool upper[2][4];
+            f[0] = exp2((gq & 1) ? in4(g[t]) : out4(g[t]));
+            f[1] = exp2(((gq & 2) ? in4(g[t]) : out4(g[t])) + next8[t]);
 #pragma unroll
-            for (int l = 0; l < 4; ++l) {
-                f4 am, bm, z, kf, f;
-                bool upper[4];
-                if (l == 0) f = f4{0.0f, g[t][1], 0.0f, g[t][3]};
-                if (l == 1) f = f4{g[t][1], 0.0f, g[t][2], g[t][2] + g[t][3]};
-                if (l == 2) f = (gq & 1) ? in4(g[t]) : out4(g[t]);
-                if (l == 3) f = ((gq & 2) ? in4(g[t]) : out4(g[t])) + next8[t];
-                f = exp2(f);
+            for (int l = 0; l < 2; ++l) {
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const int d = (4 * gq + s) ^ x;
-                    const bool here = d >= (1 << l) && d < (2 << l);
-                    am[s] = here ? a[s] : 0.0f;
-                    bm[s] = here ? b[s] : 0.0f;
-                    upper[s] = (4 * gq + s) & (1 << l);
-                    kf[s] = k[t][s] * f[s];
-                    z[s] = upper[s] ? q[t][s] * f[s] : kf[s];
+                    const bool here = d >= (4 << l) && d < (8 << l);
+                    am[l][s] = here ? a[s] : 0.0f;
+                    bm[l][s] = here ? b[s] : 0.0f;
+                    upper[l][s] = gq & (1 << l);
+                    kf[l][s] = k[t][s] * f[l][s];
+                    z[l][s] = upper[l][s] ? q[t][s] * f[l][s] : kf[l][s];
                 }
-                const f4 e2 = mm16(am, kf, zero4), e1 = mm16(bm, z, zero4);
-                const f4 r = level(t, f, upper, e1, e2);
-                if (l == 0) {
-                    dg[t][1] += r[1];
-                    dg[t][3] += r[3];
-                } else if (l == 1) {
-                    dg[t][1] += r[0];
-                    dg[t][2] += r[2] + r[3];
-                    dg[t][3] += r[3];
-                } else if (l == 2) {
-                    dg[t] += (gq & 1) ? from4(r) : before4(r);
-                } else {
-                    float o[4];
-                    groups((r[0] + r[1]) + (r[2] + r[3]), o);
-                    const float more = __builtin_fmaf(is2, o[3], is1 * o[0]);
-                    dg[t] += ((gq & 2) ? from4(r) : before4(r)) + more;
-                }
-                now(t);
+                e1[l] = e2[l] = zero4;
             }
-            // the diagonal of P
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int r = 16 * t + 4 * gq + s;
-                const float d = Pm[r * kMatRow + r];
-                dq[t][s] = __builtin_fmaf(d, k[t][s], dq[t][s]);
-                dk[t][s] = __builtin_fmaf(d, q[t][s], dk[t][s]);
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    e2[l] = __builtin_amdgcn_mfma_f32_16x16x4f32(am[l][s], kf[l][s], e2[l], 0, 0, 0);
+                    e1[l] = __builtin_amdgcn_mfma_f32_16x16x4f32(bm[l][s], z[l][s], e1[l], 0, 0, 0);
+                }
+            {  // levels 1 and 2, and the diagonal of P: pairs within a lane's four tokens
+                f4 A4[4], P4[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int at = (16 * t + 4 * gq + s) * kMatRow + 16 * t + 4 * gq;
+                    A4[s] = as4(&Am[at]);
+                    P4[s] = as4(&Pm[at]);
+                }
+                const float f1 = __builtin_amdgcn_exp2f(g[t][1]);
+                const float f2 = __builtin_amdgcn_exp2f(g[t][2]);
+                const float f3 = __builtin_amdgcn_exp2f(g[t][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dq[t][i] = __builtin_fmaf(P4[i][i], k[t][i], dq[t][i]);
+                    dk[t][i] = __builtin_fmaf(P4[i][i], q[t][i], dk[t][i]);
+                    float fall = 1.0f;
+#pragma unroll
+                    for (int j = i - 1; j >= 0; --j) {
+                        fall *= j == 2 ? f3 : j == 1 ? f2 : f1;
+                        const float kj = k[t][j] * fall;
+                        const float row = A4[i][j] * k[t][i] + P4[i][j] * q[t][i];
+                        dq[t][i] = __builtin_fmaf(P4[i][j], kj, dq[t][i]);
+                        dk[t][i] = __builtin_fmaf(A4[i][j], kj, dk[t][i]);
+                        dk[t][j] = __builtin_fmaf(fall, row, dk[t][j]);
+                        const float term = kj * row;
+#pragma unroll
+                        for (int m = j + 1; m <= i; ++m) dg[t][m] += term;
+                    }
+                }
             }
+            {
+                const f4 r4 = level(t, f[0], upper[0], e1[0], e2[0]);
+                dg[t] += (gq & 1) ? from4(r4) : before4(r4);
+                const f4 r8 = level(t, f[1], upper[1], e1[1], e2[1]);
+                float o[4];
+                groups((r8[0] + r8[1]) + (r8[2] + r8[3]), o);
+                const float more = __builtin_fmaf(is2, o[3], is1 * o[0]);
+                dg[t] += ((gq & 2) ? from4(r8) : before4(r8)) + more;
+            }
+            now(t);
             __builtin_amdgcn_sched_barrier(0);
         }
         auto tiles = [&](const float *m, int i, int j) {
