@@ -1007,7 +1007,6 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                     dq[i + 1] = dout_mul(i + 1, t, S, dq[i + 1]);
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);
             {
                 const Operand D = join(split4(d4[t][0]), split4(d4[t][1]));
 #pragma unroll
@@ -1039,7 +1038,6 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                     }
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
     both = add_rows32(add_rows16(both));
@@ -1205,7 +1203,6 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                 dg[t] += more;
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
         // pairs of tokens, level by level: z holds queries of the upper half
         // and keys of the lower, so one product serves rows and columns
         auto level = [&](int t, f4 f, const bool (&upper)[4], f4 e1, f4 e2) {
@@ -1291,7 +1288,6 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                 dg[t] += ((gq & 2) ? from4(r8) : before4(r8)) + more;
             }
             now(t);
-            __builtin_amdgcn_sched_barrier(0);
         }
         auto tiles = [&](const float *m, int i, int j) {
             return as4(m + (16 * i + x) * kMatRow + 16 * j + 4 * gq);
@@ -1318,7 +1314,6 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                 now(t);
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
         {  // level 32
             f4 kf[4], z[4];
             float sum[4];
