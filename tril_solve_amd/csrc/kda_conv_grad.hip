@@ -74,15 +74,24 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
             tap[w][e] = p.conv_w[((long)proj * W + w) * width + c + e];
             dtap[w][e] = 0.0f;
         }
-    auto row_in = [&](int t, float (&v)[8]) {
-        Raw8<EX> r;
-        r.load(xin + (long)t * xrow);
-        r.widen(v);
-        if constexpr (kCoded) {
-            const float s = p.qkv_scale[((long)t * 3 + proj) * p.H + c / D];
+    struct Row {  // an input and the gradient of its output, as loaded
+        Raw8<EX> x;
+        Raw8<E> d;
+        float scale;
+    };
+    auto load_x = [&](int t, Row &r) {
+        r.x.load(xin + (long)t * xrow);
+        r.scale = kCoded ? p.qkv_scale[((long)t * 3 + proj) * p.H + c / D] : 1.0f;
+    };
+    auto load_row = [&](int t, Row &r) {
+        load_x(t, r);
+        r.d.load(dout + (long)t * width);
+    };
+    auto widen_x = [&](const Row &r, float (&v)[8]) {
+        r.x.widen(v);
+        if constexpr (kCoded)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= s;
-        }
+            for (int e = 0; e < 8; ++e) v[e] *= r.scale;
     };
     auto window = [&](long slot, int w) {
         return ((slot * 3 + proj) * p.H + c / D) * (W - 1) * D + (long)w * D + c % D;
@@ -113,7 +122,9 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
         for (int w = 0; w < W - 1; ++w) {
             const int t = s - (W - 1) + w;
             if (t >= b) {
-                row_in(t, win[w]);
+                Row r;
+                load_x(t, r);
+                widen_x(r, win[w]);
             } else if (cont) {
                 const float *old = p.pool.base + window(slot, t - b + W - 1);
 #pragma unroll
@@ -139,23 +150,24 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
                 for (int e = 0; e < 8; ++e) d[e] = v[e];
             }
         };
-        const int stop = min(end, f + W - 1);
-        for (int t = s; t < stop; ++t) {
+        // Token t, whose window's oldest entry and unfinished row are at place R of
+        // the rings; in the segment itself also its share of dtaps.
+        auto token = [&]<int R, bool OWN>(int t, const Row &row) {
             float dn[8], y[8], a[8];
-            Raw8<E> rd;
-            rd.load(dout + (long)t * width);
-            row_in(t, win[W - 1]);
-            rd.widen(dn);
+            float(&xt)[8] = win[(R + W - 1) % W];
+            widen_x(row, xt);
+            row.d.widen(dn);
             float ss = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) sum = __builtin_fmaf(tap[w][e], win[w][e], sum);
-                const float em = __expf(-sum), sg = 1.0f / (1.0f + em);
+                for (int w = 0; w < W; ++w)
+                    sum = __builtin_fmaf(tap[w][e], win[(R + w) % W][e], sum);
+                const float em = __expf(-sum), sg = __builtin_amdgcn_rcpf(1.0f + em);
                 y[e] = sum * sg;
                 // the slope s (1 + a (1 - s)), with 1 - s = em s
-                a[e] = em < __builtin_inff() ? sg * (1.0f + sum * (em * sg)) : sum * 0.0f;
+                a[e] = em < __builtin_inff() ? sg * __builtin_fmaf(y[e], em, 1.0f) : sum * 0.0f;
                 ss = __builtin_fmaf(y[e], y[e], ss);
                 dot = __builtin_fmaf(y[e], dn[e], dot);
             }
@@ -164,7 +176,7 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
                 dot = D == 128 ? sum16(dot) : sum8(dot);
                 const float r = 1.0f / __builtin_sqrtf(ss + p.eps_l2), rr = r * r * dot;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dn[e] = r * (dn[e] - y[e] * rr);
+                for (int e = 0; e < 8; ++e) dn[e] = r * __builtin_fmaf(-y[e], rr, dn[e]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) a[e] *= dn[e];
@@ -172,19 +184,51 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
             for (int w = 0; w < W; ++w)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (t < f) dtap[w][e] = __builtin_fmaf(a[e], win[w][e], dtap[w][e]);
-                    acc[w][e] = __builtin_fmaf(tap[w][e], a[e], acc[w][e]);
+                    if constexpr (OWN)
+                        dtap[w][e] = __builtin_fmaf(a[e], win[(R + w) % W][e], dtap[w][e]);
+                    float &to = acc[(R + w) % W][e];
+                    to = w == W - 1 ? tap[w][e] * a[e] : __builtin_fmaf(tap[w][e], a[e], to);
                 }
-            leave(t - (W - 1), acc[0]);
+            leave(t - (W - 1), acc[R]);
+        };
+        // W tokens at a time, whose places in the rings are known; their successors
+        // are loaded meanwhile
+        int t = s;
+        if (t + W <= f) {
+            Row rows_[W];
 #pragma unroll
-            for (int w = 0; w < W - 1; ++w)
+            for (int i = 0; i < W; ++i) load_row(t + i, rows_[i]);
+            for (; t + W <= f; t += W) {
+                Row next[W];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int i = 0; i < W; ++i) load_row(min(t + W + i, end - 1), next[i]);
+                token.template operator()<0, true>(t, rows_[0]);
+                token.template operator()<1, true>(t + 1, rows_[1]);
+                if constexpr (W > 2) token.template operator()<2, true>(t + 2, rows_[2]);
+                if constexpr (W > 3) token.template operator()<3, true>(t + 3, rows_[3]);
+#pragma unroll
+                for (int i = 0; i < W; ++i) rows_[i] = next[i];
+            }
+        }
+        const int stop = min(end, f + W - 1);
+        for (; t < stop; ++t) {
+            Row row;
+            load_row(t, row);
+            if (t < f)
+                token.template operator()<0, true>(t, row);
+            else
+                token.template operator()<0, false>(t, row);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float w0 = win[0][e], a0 = acc[0][e];
+#pragma unroll
+                for (int w = 0; w < W - 1; ++w) {
                     win[w][e] = win[w + 1][e];
                     acc[w][e] = acc[w + 1][e];
                 }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[W - 1][e] = 0.0f;
+                win[W - 1][e] = w0;
+                acc[W - 1][e] = a0;
+            }
         }
         if (stop == end) {  // the last rows, which no later token adds to
 #pragma unroll
@@ -209,27 +253,33 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
     }
 }
 
-// dtaps: the sum of the workgroups' rows. Windows: what the first launch left,
-// or zeros where a request starts from zeros.
-__global__ __launch_bounds__(kCgThreads) void kda_conv_grad_sum_kernel(ConvGradProblem p,
-                                                                        long rows, long taps,
-                                                                        unsigned tap_blocks) {
+// dtaps: the sum of the workgroups' rows, four floats to a lane. Windows: what the
+// first launch left, or zeros where a request starts from zeros; a workgroup to
+// kCgPart floats.
+constexpr long kCgPart = 4 * kCgThreads;
+__global__ __launch_bounds__(kCgThreads) void kda_conv_grad_sum_kernel(ConvGradProblem p, int rows,
+                                                                        long taps,
+                                                                        unsigned tap_blocks,
+                                                                        unsigned parts) {
     if (blockIdx.x < tap_blocks) {
-        const long e = (long)blockIdx.x * kCgThreads + threadIdx.x;
+        const long e = ((long)blockIdx.x * kCgThreads + threadIdx.x) * 4;
         if (e >= taps) return;
-        float sum = 0.0f;
-        for (long r = 0; r < rows; ++r) sum += p.part[r * taps + e];
-        p.dconv_w[e] = sum;
+        f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) sum += *reinterpret_cast<const f4 *>(p.part + r * taps + e);
+        *reinterpret_cast<f4 *>(p.dconv_w + e) = sum;
         return;
     }
-    const int n = (int)(blockIdx.x - tap_blocks);
+    const int n = (int)((blockIdx.x - tap_blocks) / parts);
+    const long at = (blockIdx.x - tap_blocks) % parts * kCgPart + threadIdx.x * 4L;
+    const long size = 3L * p.H * (p.W - 1) * p.d;  // a multiple of 4
     const int slot = request_slot(p.grad, n);
-    if (slot < 0) return;
+    if (slot < 0 || at >= size) return;
     const bool cont = request_continues(p.grad, n);
-    const long size = 3L * p.H * (p.W - 1) * p.d;
     if (cont && request_rows(p.req, n).y == 0) return;  // handed on as it is
-    for (long e = threadIdx.x; e < size; e += kCgThreads)
-        p.grad.base[slot * size + e] = cont ? p.old[n * size + e] : 0.0f;
+    f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (cont) v = *reinterpret_cast<const f4 *>(p.old + n * size + at);
+    *reinterpret_cast<f4 *>(p.grad.base + slot * size + at) = v;
 }
 
 hipError_t launch_conv_grad(const ConvGradProblem &p, int dt, hipStream_t stream) {
@@ -254,10 +304,11 @@ hipError_t launch_conv_grad(const ConvGradProblem &p, int dt, hipStream_t stream
         });
         if (e != hipSuccess) return e;
     }
-    const unsigned tap_blocks = (unsigned)((taps + kCgThreads - 1) / kCgThreads);
+    const unsigned tap_blocks = (unsigned)((taps + kCgPart - 1) / kCgPart);
+    const unsigned parts = (unsigned)((taps / p.W * (p.W - 1) + kCgPart - 1) / kCgPart);
     const unsigned windows = p.grad.base != nullptr ? (unsigned)p.req.num_seqs : 0u;
-    hipLaunchKernelGGL(kda_conv_grad_sum_kernel, dim3(tap_blocks + windows), dim3(kCgThreads), 0,
-                       stream, p, rows, taps, tap_blocks);
+    hipLaunchKernelGGL(kda_conv_grad_sum_kernel, dim3(tap_blocks + windows * parts),
+                       dim3(kCgThreads), 0, stream, p, (int)rows, taps, tap_blocks, parts);
     return hipGetLastError();
 }
 

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kNgThreads) void kda_norm_grad_kernel(NormGradProbl
         float mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float e = __expf(-z[i]), s = 1.0f / (1.0f + e);
+            const float e = __expf(-z[i]), s = __builtin_amdgcn_rcpf(1.0f + e);
             const float n = o[i] * rn, ds = d[i] * s, dn = ds * w[i];
             dw[i] = __builtin_fmaf(ds, n, dw[i]);
             // 1 - s = e s, without its cancellation; 0 where e overflows (s = 0)
