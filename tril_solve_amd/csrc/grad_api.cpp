@@ -167,7 +167,7 @@ kda_status conv_sizes(int64_t tokens, int64_t num_seqs, int32_t H, int32_t d, in
     return KDA_OK;
 }
 size_t conv_part_bytes(int64_t tokens, int32_t H, int32_t d, int32_t W) {
-    return (size_t)conv_grad_rows(tokens, conv_grad_segment(tokens)) * 3 * W * H * d * 4;
+    return (size_t)conv_grad_rows(tokens, conv_grad_segment(tokens, H, d)) * 3 * W * H * d * 4;
 }
 size_t conv_bytes(int64_t tokens, int64_t num_seqs, int32_t H, int32_t d, int32_t W) {
     return conv_part_bytes(tokens, H, d, W) + (size_t)num_seqs * 3 * H * (W - 1) * d * 4;
@@ -235,7 +235,7 @@ kda_status conv_backward(const void *dq, const void *dk, const void *dv, kda_dty
     p.H = H;
     p.d = d;
     p.W = W;
-    p.seg = conv_grad_segment(tokens);
+    p.seg = conv_grad_segment(tokens, H, d);
     p.eps_l2 = eps_l2;
     return launch_conv_grad(p, (int)dtype, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }

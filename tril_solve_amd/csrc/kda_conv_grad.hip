@@ -8,8 +8,7 @@
 // behind hands its gradient to the last W - 1 inputs. Inputs are a tensor or an
 // 8-bit checkpoint.
 //
-// Bound by memory: two streams in, one out. A wavefront owns 512 adjacent
-// channels of one projection (lane: 8) and walks `seg` tokens forwards with the
+// A wavefront owns 256 adjacent channels of one projection (lane: 4) and walks `seg` tokens forwards with the
 // last W - 1 inputs and the unfinished dx of W - 1 rows in registers; it takes
 // W - 1 rows more on both sides, which its neighbours take, too. The four
 // wavefronts of a workgroup walk adjacent segments, join their dtaps in LDS and
@@ -24,6 +23,45 @@ namespace kda {
 
 constexpr int kCgThreads = 256;
 constexpr int kCgWaves = kCgThreads / kWave;
+constexpr int kCgChans = 4;  // channels of a lane
+
+// Four adjacent elements.
+template <class E>
+struct Quad {
+    w2 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const w2 *>(p); }
+    __device__ __forceinline__ void widen(float (&x)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = Elem<E>::widen(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+    }
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&x)[4]) {
+        const w2 o = {Elem<E>::pack(x[0], x[1]), Elem<E>::pack(x[2], x[3])};
+        __builtin_nontemporal_store(o, reinterpret_cast<w2 *>(p));
+    }
+};
+template <>
+struct Quad<F32> {
+    f4 w;
+    __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const f4 *>(p); }
+    __device__ __forceinline__ void widen(float (&x)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = w[i];
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[4]) {
+        __builtin_nontemporal_store(f4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f4 *>(p));
+    }
+};
+template <>
+struct Quad<I8> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const int8_t *p) {
+        w = *reinterpret_cast<const uint32_t *>(p);
+    }
+    __device__ __forceinline__ void widen(float (&x)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> 8 * i);
+    }
+};
 
 // Number of requests that end at or before row t (wave-uniform).
 __device__ __forceinline__ int requests_ended(const Requests &r, int t, int lane) {
@@ -43,55 +81,59 @@ __device__ __forceinline__ int requests_ended(const Requests &r, int t, int lane
 }
 
 template <class E, class EX, int D, int W>
-__global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProblem p) {
+__global__ __launch_bounds__(kCgThreads, 2) void kda_conv_grad_kernel(ConvGradProblem p) {
     typedef typename E::T T;
     constexpr bool kCoded = sizeof(typename EX::T) == 1;
-    __shared__ float joined[kCgWaves][8 * kWave];
+    __shared__ float joined[kCgWaves][kCgChans * kWave];
     const int lane = threadIdx.x & (kWave - 1);
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int width = p.H * D;
-    const int groups = (width + 8 * kWave - 1) / (8 * kWave);
+    const int groups = (width + kCgChans * kWave - 1) / (kCgChans * kWave);
     const int proj = (int)(blockIdx.x % 3);
     const int grp = (int)(blockIdx.x / 3 % groups);
     const long block = blockIdx.x / 3 / groups;
     const long t_first = (block * kCgWaves + wv) * p.seg;
     const int T_all = p.req.total_tokens;
     const int t0 = (int)min(t_first, (long)T_all), t1 = (int)min(t_first + p.seg, (long)T_all);
-    const int ch = grp * 8 * kWave + lane * 8;
+    const int ch = grp * kCgChans * kWave + lane * kCgChans;
     const bool live = ch < width;  // whole heads: width is a multiple of D
     const int c = live ? ch : 0;   // other lanes read valid channels and store nothing
     const bool unit = proj < 2;
 
-    const T *dout = static_cast<const T *>(p.dout[proj]) + c;
-    const typename EX::T *xin = static_cast<const typename EX::T *>(p.qkv) + (long)proj * width + c;
-    T *dx = static_cast<T *>(p.dqkv) + (long)proj * width + c;
+    // (rows are found in scalar registers, a lane adds its channel)
+    const uint32_t lc = c;
+    const T *dout = static_cast<const T *>(p.dout[proj]);
+    const typename EX::T *xin = static_cast<const typename EX::T *>(p.qkv) + (long)proj * width;
+    T *dx = static_cast<T *>(p.dqkv) + (long)proj * width;
+    const float *scales = p.qkv_scale + (kCoded ? (long)proj * p.H : 0);
+    const uint32_t head = lc / D;
     const long xrow = 3L * width;
-    float tap[W][8], dtap[W][8];
+    float tap[W][kCgChans], dtap[W][kCgChans];
 #pragma unroll
     for (int w = 0; w < W; ++w)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kCgChans; ++e) {
             tap[w][e] = p.conv_w[((long)proj * W + w) * width + c + e];
             dtap[w][e] = 0.0f;
         }
     struct Row {  // an input and the gradient of its output, as loaded
-        Raw8<EX> x;
-        Raw8<E> d;
+        Quad<EX> x;
+        Quad<E> d;
         float scale;
     };
     auto load_x = [&](int t, Row &r) {
-        r.x.load(xin + (long)t * xrow);
-        r.scale = kCoded ? p.qkv_scale[((long)t * 3 + proj) * p.H + c / D] : 1.0f;
+        r.x.load(xin + (long)t * xrow + lc);
+        r.scale = kCoded ? (scales + (long)t * 3 * p.H)[head] : 1.0f;
     };
     auto load_row = [&](int t, Row &r) {
         load_x(t, r);
-        r.d.load(dout + (long)t * width);
+        r.d.load(dout + (long)t * width + lc);
     };
-    auto widen_x = [&](const Row &r, float (&v)[8]) {
+    auto widen_x = [&](const Row &r, float (&v)[kCgChans]) {
         r.x.widen(v);
         if constexpr (kCoded)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= r.scale;
+            for (int e = 0; e < kCgChans; ++e) v[e] *= r.scale;
     };
     auto window = [&](long slot, int w) {
         return ((slot * 3 + proj) * p.H + c / D) * (W - 1) * D + (long)w * D + c % D;
@@ -99,7 +141,9 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
 
     for (int n = t0 < t1 ? requests_ended(p.req, t0, lane) : p.req.num_seqs; n < p.req.num_seqs;
          ++n) {
-        const int2 rows = request_rows(p.req, n);
+        int2 rows = request_rows(p.req, n);
+        rows.x = __builtin_amdgcn_readfirstlane(rows.x);
+        rows.y = __builtin_amdgcn_readfirstlane(rows.y);
         const int b = rows.x, end = rows.x + rows.y;
         if (b >= t1) break;
         const int s = max(b, t0), f = min(end, t1);
@@ -107,17 +151,17 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
         const int slot = p.grad.slot != nullptr || p.pool.base != nullptr || p.grad.base != nullptr
                              ? request_slot(p.grad, n) : 0;
         if (slot < 0) {  // padding
-            float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            float zero[kCgChans] = {0, 0, 0, 0};
             if (live)
-                for (int t = s; t < f; ++t) Raw8<E>::store(dx + (long)t * xrow, zero);
+                for (int t = s; t < f; ++t) Quad<E>::store(dx + (long)t * xrow + lc, zero);
             continue;
         }
         const bool cont = request_continues(p.pool, n);
-        float win[W][8], acc[W][8];  // inputs t - W + 1 .. t; dx of rows t - W + 1 .. t
+        float win[W][kCgChans], acc[W][kCgChans];  // inputs t - W + 1 .. t; dx of rows t - W + 1 .. t
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) win[w][e] = acc[w][e] = 0.0f;
+            for (int e = 0; e < kCgChans; ++e) win[w][e] = acc[w][e] = 0.0f;
 #pragma unroll
         for (int w = 0; w < W - 1; ++w) {
             const int t = s - (W - 1) + w;
@@ -128,11 +172,11 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
             } else if (cont) {
                 const float *old = p.pool.base + window(slot, t - b + W - 1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) win[w][e] = old[e];
+                for (int e = 0; e < kCgChans; ++e) win[w][e] = old[e];
             }
         }
         // row r is complete: to dx, or, in front of the request, to its window
-        auto leave = [&](int r, float (&v)[8]) {
+        auto leave = [&](int r, float (&v)[kCgChans]) {
             if (!live) return;
             const bool mine = r >= s && r < f, before = s == b && r < b;
             if (!mine && !before) return;
@@ -140,50 +184,49 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
             if (p.grad.base != nullptr && j >= 0) {
                 const float *d = p.grad.base + window(slot, j);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += d[e];
+                for (int e = 0; e < kCgChans; ++e) v[e] += d[e];
             }
             if (mine) {
-                Raw8<E>::store(dx + (long)r * xrow, v);
+                Quad<E>::store(dx + (long)r * xrow + lc, v);
             } else if (p.grad.base != nullptr) {
                 float *d = p.old + window(n, r - b + W - 1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = v[e];
+                for (int e = 0; e < kCgChans; ++e) d[e] = v[e];
             }
         };
         // Token t, whose window's oldest entry and unfinished row are at place R of
         // the rings; in the segment itself also its share of dtaps.
         auto token = [&]<int R, bool OWN>(int t, const Row &row) {
-            float dn[8], y[8], a[8];
-            float(&xt)[8] = win[(R + W - 1) % W];
+            float dn[kCgChans], y[kCgChans], a[kCgChans];
+            float(&xt)[kCgChans] = win[(R + W - 1) % W];
             widen_x(row, xt);
             row.d.widen(dn);
             float ss = 0.0f, dot = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kCgChans; ++e) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w)
                     sum = __builtin_fmaf(tap[w][e], win[(R + w) % W][e], sum);
                 const float em = __expf(-sum), sg = __builtin_amdgcn_rcpf(1.0f + em);
                 y[e] = sum * sg;
-                // the slope s (1 + a (1 - s)), with 1 - s = em s
-                a[e] = em < __builtin_inff() ? sg * __builtin_fmaf(y[e], em, 1.0f) : sum * 0.0f;
+                a[e] = sg + __builtin_fmaf(-y[e], sg, y[e]);  // the slope s + a s (1 - s)
                 ss = __builtin_fmaf(y[e], y[e], ss);
                 dot = __builtin_fmaf(y[e], dn[e], dot);
             }
             if (unit) {
-                ss = D == 128 ? sum16(ss) : sum8(ss);
-                dot = D == 128 ? sum16(dot) : sum8(dot);
-                const float r = 1.0f / __builtin_sqrtf(ss + p.eps_l2), rr = r * r * dot;
+                ss = D == 128 ? add_rows16(sum16(ss)) : sum16(ss);
+                dot = D == 128 ? add_rows16(sum16(dot)) : sum16(dot);
+                const float r = __builtin_amdgcn_rsqf(ss + p.eps_l2), rr = r * r * dot;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dn[e] = r * __builtin_fmaf(-y[e], rr, dn[e]);
+                for (int e = 0; e < kCgChans; ++e) dn[e] = r * __builtin_fmaf(-y[e], rr, dn[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] *= dn[e];
+            for (int e = 0; e < kCgChans; ++e) a[e] *= dn[e];
 #pragma unroll
             for (int w = 0; w < W; ++w)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < kCgChans; ++e) {
                     if constexpr (OWN)
                         dtap[w][e] = __builtin_fmaf(a[e], win[(R + w) % W][e], dtap[w][e]);
                     float &to = acc[(R + w) % W][e];
@@ -219,7 +262,7 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
             else
                 token.template operator()<0, false>(t, row);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kCgChans; ++e) {
                 const float w0 = win[0][e], a0 = acc[0][e];
 #pragma unroll
                 for (int w = 0; w < W - 1; ++w) {
@@ -241,10 +284,10 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_kernel(ConvGradProbl
     for (int w = 0; w < W; ++w) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) joined[wv][lane * 8 + e] = dtap[w][e];
+        for (int e = 0; e < kCgChans; ++e) joined[wv][lane * kCgChans + e] = dtap[w][e];
         __syncthreads();
-        for (int e = threadIdx.x; e < 8 * kWave; e += kCgThreads) {
-            const int at = grp * 8 * kWave + e;
+        for (int e = threadIdx.x; e < kCgChans * kWave; e += kCgThreads) {
+            const int at = grp * kCgChans * kWave + e;
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kCgWaves; ++i) sum += joined[i][e];
@@ -283,7 +326,7 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_sum_kernel(ConvGradP
 }
 
 hipError_t launch_conv_grad(const ConvGradProblem &p, int dt, hipStream_t stream) {
-    const long groups = ((long)p.H * p.d + 8 * kWave - 1) / (8 * kWave);
+    const long groups = ((long)p.H * p.d + kCgChans * kWave - 1) / (kCgChans * kWave);
     const long rows = conv_grad_rows(p.req.total_tokens, p.seg);
     const long taps = 3L * p.W * p.H * p.d;
     if (rows > 0) {

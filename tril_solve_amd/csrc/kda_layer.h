@@ -166,11 +166,17 @@ struct ConvGradProblem {
 inline int64_t conv_grad_rows(int64_t tokens, int32_t seg) {
     return (tokens + 4 * (int64_t)seg - 1) / (4 * (int64_t)seg);
 }
-// Tokens per wavefront: 32, fewer for short calls, more where the rows of
-// dconv_w would outgrow the tensors (from 16,384 tokens on 128 rows).
-inline int32_t conv_grad_segment(int64_t tokens) {
-    if (tokens > 16384) return (int32_t)((tokens + 511) / 512);
-    return tokens >= 2048 ? 32 : tokens >= 512 ? 16 : 4;
+// Tokens per wavefront: up to 64 (every segment takes W - 1 rows twice at both
+// ends: 8,192 tokens of 64 heads 363 us with 16, 325 with 32, 287 with 64), fewer
+// while a compute unit would have less than 12 wavefronts (6,000 tokens of 9 heads
+// of 64: 48 us with 64, 36 with 32), more where the rows of dconv_w would outgrow
+// the tensors (from 32,768 tokens on 128 rows).
+inline int32_t conv_grad_segment(int64_t tokens, int32_t H, int32_t d) {
+    if (tokens > 32768) return (int32_t)((tokens + 511) / 512);
+    const int64_t per_segment = ((int64_t)H * d + 255) / 256 * 3;
+    int32_t seg = 64;
+    while (seg > 4 && tokens / seg * per_segment < 12 * 256) seg /= 2;
+    return seg;
 }
 
 hipError_t launch_prefill(const DeltaProblem &p, int in_dt, hipStream_t stream);
