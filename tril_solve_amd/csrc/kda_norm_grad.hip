@@ -102,7 +102,7 @@ __global__ __launch_bounds__(1024) void kda_norm_grad_sum_kernel(NormGradProblem
 
 hipError_t launch_norm_grad(const NormGradProblem &p, int dt, hipStream_t stream) {
     const unsigned blocks = (unsigned)norm_grad_blocks(p.vecs, p.d);
-    const hipError_t e = dispatch_dtypes<F32, BF16, F16>(dt, 0, [&]<class E, class EO>() {
+    const hipError_t e = blocks == 0 ? hipSuccess : dispatch_dtypes<F32, BF16, F16>(dt, 0, [&]<class E, class EO>() {
         const bool coded = p.o_scale != nullptr;
         const auto fn = p.d == 64 ? (coded ? kda_norm_grad_kernel<E, I8, 64>
                                            : kda_norm_grad_kernel<E, E, 64>)
