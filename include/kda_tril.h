@@ -514,7 +514,7 @@ kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, cons
  * gate's gradient is 0).
  *
  * The states are computed again, one for every 64 tokens, and lie in the
- * workspace with what else passes between the launches: 394 KB for each chunk
+ * workspace with what else passes between the launches: 328 KB for each chunk
  * slot and head with K = V = 128.
  *
  * A value that is not finite reaches the gradients of its request and head (and

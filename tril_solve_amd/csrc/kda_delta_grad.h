@@ -56,17 +56,15 @@ struct GradWork {
     int V;
     // floats of one chunk and head
     static __device__ __forceinline__ long size(int V) {
-        return 2L * kGC * kGC + 5L * kGC * K + 2L * kGC * V + 2L * K * V + K + kGC + 4;
+        return 2L * kGC * kGC + 3L * kGC * K + 2L * kGC * V + 2L * K * V + K + kGC + 4;
     }
     __device__ __forceinline__ GradWork(float *work, int V, long item)
         : base(work + item * size(V)), V(V) {}
     __device__ __forceinline__ float *A() const { return base; }
     __device__ __forceinline__ float *M() const { return base + kGC * kGC; }       // (I + A B)^-1
     __device__ __forceinline__ float *W() const { return M() + kGC * kGC; }        // [C][K]
-    __device__ __forceinline__ float *Wt() const { return W() + kGC * K; }         // [K][C]
-    __device__ __forceinline__ float *Kb() const { return Wt() + kGC * K; }        // k e^{G - G_i}
-    __device__ __forceinline__ float *Kbt() const { return Kb() + kGC * K; }       // [K][C]
-    __device__ __forceinline__ float *Qt() const { return Kbt() + kGC * K; }       // q e^G, [K][C]
+    __device__ __forceinline__ float *Kb() const { return W() + kGC * K; }         // k e^{G - G_i}
+    __device__ __forceinline__ float *Qt() const { return Kb() + kGC * K; }        // q e^G, [K][C]
     __device__ __forceinline__ float *decay() const { return Qt() + kGC * K; }     // e^G, [K]
     __device__ __forceinline__ float *beta() const { return decay() + K; }         // [C]
     // the first row, the number of rows (0: no such chunk), whether it is padding
@@ -398,15 +396,12 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         if (w >= 2) image(imQ, w - 2, T) = q[T] * half;
         const f4 before = u1 * t[0] + u2 * t[1] + u3 * t[2];
         const f4 behind = d2 * t[3] + d1 * t[2] + d0 * t[1];
-        // operands of the walks: k e^{G - G_i} both ways, q e^G by channels
+        // operands of the walks: k e^{G - G_i} by tokens, q e^G by channels
         const f4 eg = exp2(pre[T] + before), kb = k[T] * exp2(suf[T] + behind), qg = q[T] * eg;
         kg[T] = k[T] * eg;
         as4(ws.Kb() + tok * K + 16 * T + 4 * gq) = kb;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            ws.Kbt()[(16 * T + 4 * gq + s) * kGC + tok] = kb[s];
-            ws.Qt()[(16 * T + 4 * gq + s) * kGC + tok] = qg[s];
-        }
+        for (int s = 0; s < 4; ++s) ws.Qt()[(16 * T + 4 * gq + s) * kGC + tok] = qg[s];
         if (w == 0 && x == 0) as4(ws.decay() + 16 * T + 4 * gq) = exp2(t[0] + t[1] + t[2] + t[3]);
     }
     __syncthreads();
@@ -501,7 +496,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     }
     __syncthreads();
 
-    // W = M (k e^G)
+    // W = M (k e^G); the transposed accumulators hold four adjacent channels of a row
     for (int n = w; n < NT; n += 4) {
         f4 b[4];
 #pragma unroll
@@ -512,11 +507,8 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         for (int i = 0; i < 4; ++i) {
             f4 acc = zero4;
 #pragma unroll
-            for (int t = 0; t <= i; ++t) acc = mm16(left(Mm, i, t), b[t], acc);
-            as4(ws.Wt() + (16 * n + x) * kGC + 16 * i + 4 * gq) = acc;
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                ws.W()[(16 * i + 4 * gq + s) * K + 16 * n + x] = acc[s];
+            for (int t = 0; t <= i; ++t) acc = mm16(b[t], left(Mm, i, t), acc);
+            as4(ws.W() + (16 * i + x) * K + 16 * n + 4 * gq) = acc;
         }
     }
     // X = M V, dU = P^T O', still without the states
@@ -537,21 +529,18 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         for (int i = 0; i < 4; ++i) {
             f4 acc = zero4, up = zero4;
 #pragma unroll
-            for (int t = 0; t <= i; ++t) acc = mm16(left(Mm, i, t), b[t], acc);
+            for (int t = 0; t <= i; ++t) acc = mm16(b[t], left(Mm, i, t), acc);
 #pragma unroll
             for (int t = i; t < 4; ++t) {  // column i of P's tiles, read across
                 f4 a;
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                     a[s] = Pm[(16 * t + 4 * gq + s) * kMatRow + 16 * i + x];
-                up = mm16(a, o[t], up);
+                up = mm16(o[t], a, up);
             }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int at = (16 * i + 4 * gq + s) * V + 16 * n + x;
-                ws.X()[at] = acc[s];
-                ws.U()[at] = up[s];
-            }
+            const int at = (16 * i + x) * V + 16 * n + 4 * gq;
+            as4(ws.X() + at) = acc;
+            as4(ws.U() + at) = up;
         }
     }
 }
@@ -655,12 +644,14 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
         }
     };
     auto load_last = [&](const GradWork<K> &ws) {
-        const Rsrc r = grad_floats(BACK ? ws.Wt() : ws.Kbt(), kGC * K);
+        const Rsrc r = grad_floats(BACK ? ws.W() : ws.Kb(), kGC * K);
 #pragma unroll
         for (int T = 0; T < NT; ++T)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                rhs[T][t] = load4<F32>(r, 4 * ((c0 + 16 * T + x) * kGC + 16 * t + 4 * gq));
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    rhs[T][t][s] = load1<F32>(r, 4 * ((16 * t + 4 * gq + s) * K + c0 + 16 * T + x));
     };
     auto chunk_of = [&](int j) { return BACK ? chunks - 1 - j : j; };
     if (chunks > 0) {

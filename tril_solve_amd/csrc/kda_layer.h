@@ -108,10 +108,10 @@ struct DeltaGradProblem {
 inline int64_t grad_slots(int64_t total_tokens, int64_t num_seqs) {
     return total_tokens / kGradChunk + num_seqs;
 }
-// A and its inverse, five operands of C x K, two of C x V, two states, decays,
+// A and its inverse, three operands of C x K, two of C x V, two states, decays,
 // beta, the chunk itself.
 inline int64_t grad_chunk_floats(int32_t K, int32_t V) {
-    return (int64_t)2 * kGradChunk * kGradChunk + 5 * kGradChunk * K + 2 * kGradChunk * V +
+    return (int64_t)2 * kGradChunk * kGradChunk + 3 * kGradChunk * K + 2 * kGradChunk * V +
            2 * K * V + K + kGradChunk + 4;
 }
 
