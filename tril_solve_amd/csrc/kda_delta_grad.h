@@ -566,6 +566,8 @@ template <int CT>
 struct GradWalkLds {
     float part[4][4 * CT][kWave * 4];  // [wavefront][tile row, column tile]
     float u[4 * CT][kWave * 4], o[4 * CT][kWave * 4];
+    // a wavefront's state by rows, on its way to memory in whole lines
+    float rows[4][32][16 * CT + 4];
 };
 template <class EO, int K, int CT, bool BACK>
 __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int h, int part,
@@ -697,8 +699,14 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
                 for (int c = 0; c < CT; ++c)
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        grad_store1<F32>(
-                            r, 4 * ((c0 + 16 * T + 4 * gq + s) * V + col + 16 * c), S[T][c][s]);
+                        lds.rows[w][16 * T + 4 * gq + s][16 * c + x] = S[T][c][s];
+            constexpr int kLanes = 4 * CT;  // to a row
+#pragma unroll
+            for (int e = 0; e < NT * CT; ++e) {
+                const int row = (e * kWave + lane) / kLanes, at = lane % kLanes * 4;
+                const f4 v = as4(&lds.rows[w][row][at]);
+                grad_store4<F32>(r, 4 * ((c0 + row) * V + part * 16 * CT + at), v);
+            }
         }
         grad_lds_barrier();
         {
