@@ -805,8 +805,9 @@ __device__ __forceinline__ Operand grad_operand(Rsrc r, uint32_t off) {
     return join(split4(a), split4(b));
 }
 
-// A wavefront to every 16 key channels.
-template <class E, class EO, int K>
+// A wavefront to every 16 key channels. ONE: all value columns at once (up to 128;
+// with a loop over them the sums take registers from what is loaded ahead).
+template <class E, class EO, int K, bool ONE>
 __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel(DeltaGradProblem p) {
     typedef GradLds<K> L;
     constexpr int NW = K / 16, VB = L::VB;
@@ -841,14 +842,40 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                 to[t][e] = load4<F32>(rS, vb + 32 * t < V ? 4 * (row * V + v) : kOffMasked);
             }
     };
+    // this thread's part of X and dU for LDS, and this wavefront's columns of dU
+    constexpr int NS = VB / (4 * NW);
+    f4 xs[NS], us[NS], ub[4];
+    auto load_columns = [&](int vb) {
+#pragma unroll
+        for (int e = 0; e < NS; ++e) {
+            const int col = vb + 4 * (threadIdx.x % NW) + 4 * NW * e;
+            const uint32_t at = col < V ? 4 * (threadIdx.x / NW * V + col) : kOffMasked;
+            xs[e] = load4<F32>(rX, at);
+            us[e] = load4<F32>(rU, at);
+        }
+    };
+    auto load_tile = [&](int vb, int n) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int col = vb + 16 * n + x;
+                ub[t][s] = load1<F32>(
+                    rU, col < V ? 4 * ((16 * t + 4 * gq + s) * V + col) : kOffMasked);
+            }
+    };
     const int4 where = *reinterpret_cast<const int4 *>(ws.chunk());
+    if constexpr (ONE) load_columns(0);
     f4 minv[1024 / (K * 4)];
 #pragma unroll
     for (int e = 0; e < 1024 / (K * 4); ++e)
         minv[e] = load4<F32>(rM, 16 * (threadIdx.x + e * K * 4));
     const float my_beta =
         threadIdx.x < kGC ? load1<F32>(grad_floats(ws.beta(), kGC), 4 * threadIdx.x) : 0.0f;
-    load_rows(s4, c, 0);
+    if constexpr (ONE) {
+        load_tile(0, w);
+        load_rows(s4, c, 0);
+    }
     const int len = __builtin_amdgcn_readfirstlane(where.y);
     if (len == 0) return;
     struct {
@@ -884,11 +911,7 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
         const int at = threadIdx.x + e * K * 4;
         as4(&Am[at / 16 * kMatRow + at % 16 * 4]) = minv[e];
     }
-    if (threadIdx.x < kGC) {
-        bs[threadIdx.x] = my_beta;
-        xdu[threadIdx.x] = 0.0f;
-    }
-    __syncthreads();
+    if (threadIdx.x < kGC) bs[threadIdx.x] = my_beta;
 
     // O' S^T, Y S^T, X dS^T, the rows of S * dS, and tile rows of Y X^T and O' X^T:
     // row w & 3 of one of them, or, with four wavefronts, row w of both
@@ -903,42 +926,48 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
     float both = 0.0f;
     const int tr = w & 3;
 #pragma unroll 1
-    for (int vb = 0; vb < V; vb += VB) {
+    for (int vb = 0; vb < (ONE ? 1 : V); vb += VB) {
         const int nv = min(VB, V - vb);
-        if (vb > 0) __syncthreads();
+        if constexpr (!ONE) {
+            if (vb > 0) __syncthreads();
+            load_columns(vb);
+            load_tile(vb, w);
+            load_rows(s4, c, vb);
+        }
         {  // X and dout to LDS; X.dU, NW lanes to a row
-            const int r = threadIdx.x / NW;
-            float sum = 0.0f;
-            for (int col = 4 * (threadIdx.x % NW); col < nv; col += 4 * NW) {
-                const f4 a = load4<F32>(rX, 4 * (r * V + vb + col));
-                const f4 b = load4<F32>(rU, 4 * (r * V + vb + col));
+            const int r = threadIdx.x / NW, c0 = 4 * (threadIdx.x % NW);
+            w2 os[NS];
+            if constexpr (kExact)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) sum = __builtin_fmaf(a[s], b[s], sum);
-                const Half parts = split4(a);
-                char *at = lds + L::X + r * L::RS + 2 * col;
+                for (int e = 0; e < NS; ++e)
+                    os[e] = __builtin_bit_cast(
+                        w2, __builtin_amdgcn_raw_buffer_load_b64(
+                                rdout, r * dstep + 2 * (vb + c0 + 4 * NW * e), 0, 0));
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < NS; ++e) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) sum = __builtin_fmaf(xs[e][s], us[e][s], sum);
+                const Half parts = split4(xs[e]);
+                char *at = lds + L::X + r * L::RS + 2 * (c0 + 4 * NW * e);
 #pragma unroll
                 for (int i = 0; i < kParts; ++i)
                     *reinterpret_cast<w2 *>(at + i * L::PART) = parts.p[i];
-                if constexpr (kExact)
-                    *reinterpret_cast<w2 *>(lds + L::O + r * L::RS + 2 * col) =
-                        __builtin_bit_cast(w2, __builtin_amdgcn_raw_buffer_load_b64(
-                                                   rdout, r * dstep + 2 * (vb + col), 0, 0));
             }
             sum = lane_add<0x4E>(lane_add<0xB1>(sum));
             if (NW == 8) sum = lane_add<0x141>(sum);
-            if (threadIdx.x % NW == 0) xdu[r] += sum;
+            if (threadIdx.x % NW == 0) xdu[r] = vb > 0 ? xdu[r] + sum : sum;
+            if constexpr (kExact)
+#pragma unroll
+                for (int e = 0; e < NS; ++e)
+                    *reinterpret_cast<w2 *>(lds + L::O + r * L::RS + 2 * (c0 + 4 * NW * e)) = os[e];
         }
-        if (vb > 0) load_rows(s4, c, vb);
+        if (vb == 0) __syncthreads();  // the inverse and beta
         // Y = M^T (B dU), its transpose in the accumulators: columns of four
-        for (int n = w; n < nv / 16; n += NW) {
+        auto gradients_of_v = [&](int n) {
             f4 b[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int r = 16 * t + 4 * gq + s;
-                    b[t][s] = bs[r] * load1<F32>(rU, 4 * (r * V + vb + 16 * n + x));
-                }
+            for (int t = 0; t < 4; ++t) b[t] = as4(&bs[16 * t + 4 * gq]) * ub[t];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f4 acc = zero4;
@@ -958,6 +987,11 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
                     *reinterpret_cast<w2 *>(at + j * L::PART) = parts.p[j];
                 grad_store4<E>(rdv, r * vstep + (uint32_t)(vb + col) * E::kBytes, acc);
             }
+        };
+        if (w < nv / 16) gradients_of_v(w);
+        if (NW == 4 && w + NW < nv / 16) {
+            load_tile(vb, w + NW);
+            gradients_of_v(w + NW);
         }
         load_rows(d4, K + c, vb);  // (not earlier: registers)
         __syncthreads();
@@ -1039,6 +1073,22 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
             }
         }
     }
+    const bool per_channel = p.gate_stride == K;
+    const Rsrc rk = grad_rows<E>(p.k, ch.row, hk, p.Hk, K, len);
+    const Rsrc rq = grad_rows<E>(p.q, ch.row, hk, p.Hk, K, len);
+    const Rsrc rg = grad_rows<F32>(p.g, ch.row, h, p.H, p.gate_stride, len);
+    const uint32_t kstep = (uint32_t)p.Hk * K, gstep = (uint32_t)p.H * p.gate_stride;
+    uint32_t kraw[4][4], qraw[4][4];
+    f4 g[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t r = 16 * t + 4 * gq + s, at = r * kstep + c;
+            kraw[t][s] = grad_raw1<E>(rk, at * E::kBytes);
+            qraw[t][s] = grad_raw1<E>(rq, at * E::kBytes);
+            g[t][s] = load1<F32>(rg, 4 * (r * gstep + (per_channel ? c : 0)));
+        }
     both = add_rows32(add_rows16(both));
 #pragma unroll
     for (int i = 0; i < 4; ++i) ke[i] *= as4(&bs[16 * i + 4 * gq]);
@@ -1093,21 +1143,15 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
     }
 
     // the rest by key channels, in registers
-    const bool per_channel = p.gate_stride == K;
-    const Rsrc rk = grad_rows<E>(p.k, ch.row, hk, p.Hk, K, len);
-    const Rsrc rq = grad_rows<E>(p.q, ch.row, hk, p.Hk, K, len);
-    const Rsrc rg = grad_rows<F32>(p.g, ch.row, h, p.H, p.gate_stride, len);
-    const uint32_t kstep = (uint32_t)p.Hk * K, gstep = (uint32_t)p.H * p.gate_stride;
     {
-        f4 k[4], q[4], g[4], pre[4], suf[4];
+        f4 k[4], q[4], pre[4], suf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const uint32_t r = 16 * t + 4 * gq + s, at = r * kstep + c;
-                k[t][s] = load1<E>(rk, at * E::kBytes);
-                q[t][s] = load1<E>(rq, at * E::kBytes);
-                g[t][s] = grad_gate(load1<F32>(rg, 4 * (r * gstep + (per_channel ? c : 0))));
+                k[t][s] = grad_widen<E>(kraw[t][s]);
+                q[t][s] = grad_widen<E>(qraw[t][s]);
+                g[t][s] = grad_gate(g[t][s]);
             }
         // In registers, tokens 4 g .. 4 g + 3 of a tile: sums through the token
         // (in) and behind it (out) over 4, 16 and more tokens.
@@ -1414,7 +1458,10 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     const long walks = (long)p.req.num_seqs * p.H, groups = (walks + 7) / 8;
-    if (walks * (p.V / 32) >= 1024 && !getenv("CT1")) {
+    // 32 columns to a workgroup halve what the operands cost in L2, 16 columns the
+    // work of a step: one sequence of 4,096 tokens takes 207 us in 16 and 303 in
+    // 32 with 8 heads (128 and 64 workgroups), 440 and 352 with 32 heads.
+    if (2 * walks * (p.V / 16) > device_cus()) {
         const int parts = p.V / 32;
         hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 2>), dim3((unsigned)(groups * 8 * parts), 2),
                            dim3(256), 0, stream, p, parts);
@@ -1425,8 +1472,9 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (p.req.total_tokens > 0) {
-        hipLaunchKernelGGL((kda_grad_chunk_kernel<E, EO, K>), dim3(items), dim3(K * 4), 0, stream,
-                           p);
+        const auto fn = p.V <= GradLds<K>::VB ? kda_grad_chunk_kernel<E, EO, K, true>
+                                              : kda_grad_chunk_kernel<E, EO, K, false>;
+        hipLaunchKernelGGL(fn, dim3(items), dim3(K * 4), 0, stream, p);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (p.Hk != p.H)
             hipLaunchKernelGGL((kda_grad_shared_kernel<E, K>), dim3((unsigned)(p.slots * p.Hk)),
