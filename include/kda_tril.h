@@ -508,8 +508,9 @@ kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, cons
  *   dq, dk      [T, Hk, K], dv [T, H, V] of in_dtype (of shared key heads: the
  *               sum over the heads that read them).
  *   dg          FP32, g's shape; dbeta FP32 [T, H].
- * The same limits on K, V, Hk and gate_dim; at most 2^24 - 1 chunk slots x heads,
- * chunk slots = total_tokens / 64 + num_seqs, else KDA_ERR_UNSUPPORTED. All
+ * The same limits on K, V, Hk and gate_dim; with chunk slots = total_tokens / 64 +
+ * num_seqs, chunk slots x H < 2^23 and num_seqs x H x V / 32 < 2^24 - 64, else
+ * KDA_ERR_UNSUPPORTED. All
  * arithmetic is FP32. Any decay is taken exactly, from e^0 to e^-inf (whose
  * gate's gradient is 0).
  *

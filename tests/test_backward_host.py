@@ -56,7 +56,8 @@ def test_delta_refusals(kt):
             if at != own:
                 assert _delta(kt, **kw) == E, kw
     for kw in [dict(K=96, gate=96), dict(V=48), dict(V=288), dict(H=8192), dict(T=2 ** 31),
-               dict(n=2 ** 31), dict(n=2 ** 21, H=8), dict(T=2 ** 30), dict(slots=2 ** 31)]:
+               dict(n=2 ** 31), dict(n=2 ** 21, H=8), dict(T=2 ** 30), dict(slots=2 ** 31),
+               dict(n=2 ** 20, H=4, V=256, slots=2 ** 21), dict(T=2 ** 27, H=4)]:
         assert _delta(kt, **kw) == U, kw
     need = kt.kda_prefill_backward_workspace_size(64, 2, 4, 2, 128, 128)
     assert 0 < need < G

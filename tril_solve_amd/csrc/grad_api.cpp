@@ -12,7 +12,8 @@ using namespace kda;
 
 namespace {
 
-constexpr int64_t kMaxItems = ((int64_t)1 << 24) - 1;  // 256 threads each, below 2^32 in all
+constexpr int64_t kMaxItems = ((int64_t)1 << 24) - 1;   // 256 threads each, below 2^32 in all
+constexpr int64_t kMaxChunks = ((int64_t)1 << 23) - 1;  // 512 threads each
 constexpr int64_t kMaxVectors = (int64_t)1 << 28;      // 16 lanes each, below 2^32 in all
 
 // Writable arguments overlap neither each other nor anything that is read.
@@ -51,7 +52,8 @@ kda_status delta_sizes(int64_t tokens, int64_t num_seqs, int32_t H, int32_t Hk, 
         return KDA_ERR_INVALID_ARG;
     if (tokens > kMaxTokens || num_seqs > kMaxTokens || H > kMaxHeads || (K != 64 && K != 128) ||
         V % 32 != 0 || V > 256 || num_seqs > kMaxPairs / H ||
-        grad_slots(tokens, num_seqs) > kMaxItems / H)
+        grad_slots(tokens, num_seqs) > kMaxChunks / H ||
+        num_seqs * H + 8 > kMaxItems / (V / 32))  // walks of 32 columns, in groups of 8
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
