@@ -6,6 +6,7 @@ their outputs and the workspace.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -37,9 +38,12 @@ for _n, _a in _ARGS.items():
     getattr(_lib, _n).argtypes = _a
 
 
-def _size(fn, *args) -> int:
+# (the queries depend on the sizes alone; asked once for each of them, a call spends 2 us
+# less on them)
+@lru_cache(maxsize=256)
+def _size(name, *args) -> int:
     b = _sz(0)
-    _check(fn(*args, ctypes.byref(b)))
+    _check(getattr(_lib, name)(*args, ctypes.byref(b)))
     return int(b.value)
 
 
@@ -95,7 +99,7 @@ def _codes(name, t, shape):
 def kda_prefill_backward_workspace_size(total_tokens: int, num_seqs: int, H: int, Hk: int, K: int,
                                         V: int) -> int:
     """Workspace bytes of kda_prefill_backward. Host only."""
-    return _size(_lib.kda_prefill_backward_workspace_size, total_tokens, num_seqs, H, Hk, K, V)
+    return _size("kda_prefill_backward_workspace_size", total_tokens, num_seqs, H, Hk, K, V)
 
 
 def kda_prefill_backward(dout, q, k, v, g, beta, dq, dk, dv, dg, dbeta, workspace,
@@ -147,7 +151,7 @@ def prefill_backward(dout, q, k, v, g, beta, cu_seqlens=None, state=None, dstate
 def kda_conv_backward_workspace_size(total_tokens: int, num_seqs: int, H: int, head_dim: int,
                                      conv_width: int) -> int:
     """Workspace bytes of kda_conv_backward. Host only."""
-    return _size(_lib.kda_conv_backward_workspace_size, total_tokens, num_seqs, H, head_dim,
+    return _size("kda_conv_backward_workspace_size", total_tokens, num_seqs, H, head_dim,
                  conv_width)
 
 
@@ -209,7 +213,7 @@ def conv_prefill_backward(dq, dk, dv, qkv, conv_w, cu_seqlens=None, conv_state=N
 
 def kda_gated_norm_backward_workspace_size(rows: int, H: int, head_dim: int) -> int:
     """Workspace bytes of kda_gated_norm_backward. Host only."""
-    return _size(_lib.kda_gated_norm_backward_workspace_size, rows, H, head_dim)
+    return _size("kda_gated_norm_backward_workspace_size", rows, H, head_dim)
 
 
 def kda_gated_norm_backward(dout, o, z, norm_w, do, dz, dnorm_w, workspace, eps_norm=1e-6,
