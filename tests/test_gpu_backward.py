@@ -348,8 +348,8 @@ def test_delta_many_requests(kt):
 
 @pytest.mark.parametrize("V", [32, 128])
 def test_delta_many_walks(kt, V):
-    """The walks of 32 columns to a workgroup (1,024 of them and more) give what
-    single requests do."""
+    """The walks of 32 columns to a workgroup (many requests and heads) give what
+    those of 16 columns (single requests) do."""
     n, H = 70, 16
     lens = [65 if i % 7 else 1 for i in range(n)]
     if V == 32:

@@ -16,13 +16,15 @@
 //   dg_t = what crosses the border in front of token t: the terms of q dq and
 //          k dk of every pair i >= t > j, and those of both states.
 //
-// Three launches. Chunks are prepared side by side (A, its inverse, W =
-// (I + A B)^-1 (k e^G), X and dU without the states). Then the states walk
-// forwards, X -= W S, and their gradients backwards, both at once, each
-// wavefront on its own value columns:
-//   S <- e^G S + (k e^{G - G_i})^T U,  dS <- e^G dS + (q e^G)^T O' - W^T B dU.
-// Last, the chunks' gradients side by side, each wavefront on its own key
-// channels. States and their gradients lie in the workspace between launches.
+// Three launches. Chunks are prepared side by side: A, its inverse, W =
+// (I + A B)^-1 (k e^G), and X and dU without the states. Then the states walk
+// forwards and their gradients backwards, both at once, each workgroup on its
+// own value columns:
+//   X -= W S,                    S <- e^G S + (k e^{G - G_i})^T B X
+//   dU += (k e^{G - G_i}) dS,    dS <- e^G dS + (q e^G)^T O' - W^T B dU.
+// Last, the chunks' gradients side by side, each wavefront on its own 16 key
+// channels. States and their gradients lie in the workspace between launches, one
+// for every 64 tokens: chunks of 32 would double that.
 //
 // Decays within a chunk never leave [0, 1]: a pair i > j meets at the level
 // b = msb(i ^ j) (1, 2, ..., 32) with m the middle of the 2b tokens around both,
@@ -31,8 +33,17 @@
 // any decay down to e^-inf goes through it exactly. dg is summed the same
 // way, level by level, without differences.
 //
-// All products run on the FP32 matrix instructions: gradients are sums of long
-// chains, and FP32 outputs (dg, dbeta, states) are wanted to FP32.
+// Products run on the FP32 matrix instructions, but for those of the chunks' last
+// kernel over value columns, which take six bfloat16 products of three parts (see
+// bf16_parts.h). FP32 outputs are 1e-7 to 4e-7 of their norm from 64 bits.
+//
+// What bounds it (16 x 512 tokens of 64 heads, K = V = 128, bf16: 3.15 ms, 0.77 +
+// 1.25 + 1.28 in the three kernels; one sequence of 16,384 tokens and 32 heads
+// 3.33 ms, 0.77 + 1.45 + 1.24): the traffic of the workspace (10 GB a call, 3.2, 3.2
+// and 2.8 TB/s of a copy's 5.1) and the chains between barriers, which the
+// few wavefronts that their registers and LDS leave room for do not cover (two to a
+// SIMD). The matrix pipes are busy for 38, 49 and 26% of the cycles, the vector
+// units for 29, 10 and 35%.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -119,25 +130,6 @@ __device__ __forceinline__ f4 mm16(f4 a, f4 b, f4 c) {
     return c;
 }
 
-template <class E>
-__device__ __forceinline__ f4 grad_load4(const typename E::T *p);
-template <>
-__device__ __forceinline__ f4 grad_load4<F32>(const float *p) {
-    return *reinterpret_cast<const f4 *>(p);
-}
-template <>
-__device__ __forceinline__ f4 grad_load4<BF16>(const uint16_t *p) {
-    const w2 w = *reinterpret_cast<const w2 *>(p);
-    return f4{bf16_to_f32(w[0] & 0xFFFFu), bf16_to_f32(w[0] >> 16), bf16_to_f32(w[1] & 0xFFFFu),
-              bf16_to_f32(w[1] >> 16)};
-}
-template <>
-__device__ __forceinline__ f4 grad_load4<F16>(const uint16_t *p) {
-    const w2 w = *reinterpret_cast<const w2 *>(p);
-    return f4{Elem<F16>::widen(w[0] & 0xFFFFu), Elem<F16>::widen(w[0] >> 16),
-              Elem<F16>::widen(w[1] & 0xFFFFu), Elem<F16>::widen(w[1] >> 16)};
-}
-__device__ __forceinline__ void grad_store(float *p, float x) { *p = x; }
 template <class E>
 __device__ __forceinline__ void grad_put(typename E::T *p, float x);
 template <>
@@ -229,6 +221,12 @@ __device__ __forceinline__ void grad_join(float &pre, float &suf, float &tot, bo
 
 // ---------------------------------------------------------------- preparation
 
+// A workgroup to a chunk and head. The levels are products of 64-token images in
+// LDS (16 lanes: 16 tokens, their sums by DPP); the inverse is substitution within
+// 16 x 16 and products above; all that the other kernels read is stored as they
+// load it, rows of four floats to a lane. Bound by what it stores and by the
+// latency between its parts (16 x 512 tokens of 64 heads: 0.77 ms for 0.8 GB read
+// and 1.6 written; without X and dU 0.55, without the decayed rows 0.58).
 template <class E, class EO, int K>
 __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProblem p) {
     constexpr int NT = K / 16, KR = K + 4;
@@ -561,7 +559,12 @@ __device__ __forceinline__ void grad_lds_barrier() {
 // makes X (or dU) of it, and every wavefront updates its channels with the whole
 // U. So one step of the chain is a quarter of the products, two exchanges in LDS
 // and another quarter, and the operands of the next chunk are on their way
-// meanwhile.
+// meanwhile. (One wavefront with all channels: a call of 16,384 tokens and 32 heads
+// took 15.4 ms, 5.3 so, and now 3.3. Six bfloat16 products, 0.75 of the matrix time
+// of FP32's, lose: the splits are vector instructions in the chain, 1.92 ms instead
+// of 1.48, and on 16 x 512 tokens of 64 heads 1.43 instead of 1.26.)
+// Bound by the chain with one sequence (256 steps of 5.7 us), by the states' traffic
+// with many (16 x 512 tokens: 4 GB in 1.25 ms; the products alone take 0.76).
 template <int CT>
 struct GradWalkLds {
     float part[4][4 * CT][kWave * 4];  // [wavefront][tile row, column tile]
@@ -798,15 +801,21 @@ struct GradLds {
     static constexpr int kBytes = DG + K / 16 * kGC * 4;
     static_assert(kBytes <= 160 * 1024);
 };
-// Eight adjacent elements of dout as an operand: one part if they are bfloat16.
+// Eight adjacent elements of dout as an operand (bfloat16: all in its first part).
 template <class EO>
 __device__ __forceinline__ Operand grad_operand(Rsrc r, uint32_t off) {
     const f4 a = load4<EO>(r, off), b = load4<EO>(r, off + 4 * EO::kBytes);
     return join(split4(a), split4(b));
 }
 
-// A wavefront to every 16 key channels. ONE: all value columns at once (up to 128;
-// with a loop over them the sums take registers from what is loaded ahead).
+// A wavefront to every 16 key channels, one workgroup to a compute unit (160 KB of
+// LDS): Y, X and dout are there for all of them, and S and dS are read once. FP32
+// products over the value columns instead of six bfloat16 ones made a call of 16 x
+// 512 tokens of 64 heads 3.6 ms instead of 3.3. Levels 1 and 2, pairs within a
+// lane's four tokens, are vector instructions (1.39 -> 1.31 ms for this kernel with
+// the operands of E taken as they lie); from 4 on a level is one product of
+// masked tiles. ONE: all value columns at once (up to 128; with a loop over them the
+// sums take registers from what is loaded ahead).
 template <class E, class EO, int K, bool ONE>
 __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel(DeltaGradProblem p) {
     typedef GradLds<K> L;
@@ -1427,7 +1436,9 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
     }
 }
 
-// Gradients of shared key heads: the sum over the value heads that read them.
+// Gradients of shared key heads: the sum over the value heads that read them, in
+// order, so its bits are the same every time. Bound by memory: it reads FP32 rows
+// of every value head (18 us on 8,161 tokens, 8 heads over 4 of 64).
 template <class E, int K>
 __global__ __launch_bounds__(256) void kda_grad_shared_kernel(DeltaGradProblem p) {
     const int lane = threadIdx.x & (kWave - 1);

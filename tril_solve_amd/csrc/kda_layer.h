@@ -168,7 +168,7 @@ inline int64_t conv_grad_rows(int64_t tokens, int32_t seg) {
 }
 // Tokens per wavefront: up to 64 (every segment takes W - 1 rows twice at both
 // ends: 8,192 tokens of 64 heads 363 us with 16, 325 with 32, 287 with 64), fewer
-// while a compute unit would have less than 12 wavefronts (6,000 tokens of 9 heads
+// while a compute unit would have less than 12 wavefronts (7,000 tokens of 9 heads
 // of 64: 48 us with 64, 36 with 32), more where the rows of dconv_w would outgrow
 // the tensors (from 32,768 tokens on 128 rows).
 inline int32_t conv_grad_segment(int64_t tokens, int32_t H, int32_t d) {
