@@ -511,7 +511,7 @@ kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, cons
  * The same limits on K, V, Hk and gate_dim; with chunk slots = total_tokens / 64 +
  * num_seqs, chunk slots x H < 2^23 and num_seqs x H x V / 32 < 2^24 - 64, else
  * KDA_ERR_UNSUPPORTED. All
- * arithmetic is FP32. Any decay is taken exactly, from e^0 to e^-inf (whose
+ * sums are FP32, products of FP32 factors exact to 2^-24 or so. Any decay is taken exactly, from e^0 to e^-inf (whose
  * gate's gradient is 0).
  *
  * The states are computed again, one for every 64 tokens, and lie in the

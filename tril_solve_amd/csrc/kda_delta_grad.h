@@ -211,12 +211,24 @@ __device__ __forceinline__ float grad_gate(float g) {
 // b tokens are joined to 2b. pre: through the token from the half's start;
 // suf: behind the token to the half's end; tot: of the half.
 template <int CTRL>
+__device__ __forceinline__ float grad_dpp(float v) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
 __device__ __forceinline__ void grad_join(float &pre, float &suf, float &tot, bool upper) {
-    const float o = __builtin_bit_cast(
-        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, tot), CTRL, 0xF, 0xF, true));
+    const float o = grad_dpp<CTRL>(tot);
     pre += upper ? o : 0.0f;
     suf += upper ? 0.0f : o;
     tot += o;
+}
+
+// Barrier of the workgroup that orders LDS alone: loads and stores of memory stay
+// in flight.
+__device__ __forceinline__ void grad_lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // ---------------------------------------------------------------- preparation
@@ -224,9 +236,11 @@ __device__ __forceinline__ void grad_join(float &pre, float &suf, float &tot, bo
 // A workgroup to a chunk and head. The levels are products of 64-token images in
 // LDS (16 lanes: 16 tokens, their sums by DPP); the inverse is substitution within
 // 16 x 16 and products above; all that the other kernels read is stored as they
-// load it, rows of four floats to a lane. Bound by what it stores and by the
-// latency between its parts (16 x 512 tokens of 64 heads: 0.77 ms for 0.8 GB read
-// and 1.6 written; without X and dU 0.55, without the decayed rows 0.58).
+// load it, rows of four floats to a lane. Pairs within four tokens are vector
+// instructions (as masked products with the others 0.73 instead of 0.69 ms), the values
+// are on their way while the inverse is made (0.77 ms without). Bound by what it
+// stores and by the latency between its parts: 16 x 512 tokens of 64 heads take 0.69
+// ms for 0.8 GB read and 1.6 written.
 template <class E, class EO, int K>
 __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProblem p) {
     constexpr int NT = K / 16, KR = K + 4;
@@ -279,7 +293,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         }
     }
 
-    // diagonal tiles: the levels below 16 within the wavefront
+    // diagonal tiles: the levels below 16, within the wavefront
     f4 dA = {0.0f, 0.0f, 0.0f, 0.0f}, dP = dA;
     float pd = 0.0f;
 #pragma unroll
@@ -308,7 +322,39 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
             }
         }
     };
-    diagonal(1);
+    // pairs within four tokens: y holds the key of 1, 2, 3 tokens before, decayed to
+    // this one; lanes whose pair crosses the four do not count
+    {
+        float sA[3] = {0.0f, 0.0f, 0.0f}, sP[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int T = 0; T < NT; ++T) {
+            const f4 e = exp2(tot[T]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float y = k[T][s];
+#pragma unroll
+                for (int d = 0; d < 3; ++d) {
+                    y = e[s] * grad_dpp<0x111>(y);  // row_shr:1
+                    sA[d] = __builtin_fmaf(k[T][s], y, sA[d]);
+                    sP[d] = __builtin_fmaf(q[T][s], y, sP[d]);
+                }
+            }
+        }
+        auto put4 = [&](f4 &to, const float (&sum)[3]) {
+            float v[3];
+#pragma unroll
+            for (int d = 0; d < 3; ++d) v[d] = add_rows32(add_rows16(sum[d]));
+            const float a1 = grad_dpp<0x55>(v[0]), a2 = grad_dpp<0xAA>(v[0]),
+                        b2 = grad_dpp<0xAA>(v[1]), a3 = grad_dpp<0xFF>(v[0]),
+                        b3 = grad_dpp<0xFF>(v[1]), c3 = grad_dpp<0xFF>(v[2]);
+            const int at = gq == x >> 2 ? x & 3 : 4;
+            to[1] = at == 0 ? a1 : to[1];
+            to[2] = at == 1 ? a2 : at == 0 ? b2 : to[2];
+            to[3] = at == 2 ? a3 : at == 1 ? b3 : at == 0 ? c3 : to[3];
+        };
+        put4(dA, sA);
+        put4(dP, sP);
+    }
 #pragma unroll
     for (int T = 0; T < NT; ++T)
 #pragma unroll
@@ -317,7 +363,6 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
             grad_join<0xB1>(a, c, t, x & 1);
             pre[T][s] = a, suf[T][s] = c, tot[T][s] = t;
         }
-    diagonal(2);
 #pragma unroll
     for (int T = 0; T < NT; ++T)
 #pragma unroll
@@ -368,7 +413,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         image(imK, w, T) = k[T] * f;
         if (w & 1) image(imQ, w >> 1, T) = q[T] * f;
     }
-    __syncthreads();
+    grad_lds_barrier();
     f4 o16 = {0.0f, 0.0f, 0.0f, 0.0f}, oA = o16, oP = o16;
     {  // wavefronts 0, 1: A and P of tile (1, 0); 2, 3: of tile (3, 2)
         const int pair = w >> 1;
@@ -378,7 +423,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
             o16 = mm16(a, image(imK, 2 * pair, T), o16);
         }
     }
-    __syncthreads();
+    grad_lds_barrier();
     // 1 for wavefronts from 1, 2, 3 on and up to 0, 1, 2 (branches on them would cut
     // the code into pieces)
     const float u1 = w >= 1, u2 = w >= 2, u3 = w >= 3, d0 = w < 1, d1 = w < 2, d2 = w < 3;
@@ -402,7 +447,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         for (int s = 0; s < 4; ++s) ws.Qt()[(16 * T + 4 * gq + s) * kGC + tok] = qg[s];
         if (w == 0 && x == 0) as4(ws.decay() + 16 * T + 4 * gq) = exp2(t[0] + t[1] + t[2] + t[3]);
     }
-    __syncthreads();
+    grad_lds_barrier();
     const int ti = 2 + (w >> 1), tj = w & 1;  // this wavefront's tile of level 32
 #pragma unroll
     for (int T = 0; T < NT; ++T) {
@@ -411,7 +456,25 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         oP = mm16(image(imQ, ti - 2, T), b, oP);
     }
 
-    __syncthreads();  // the images are read
+    grad_lds_barrier();  // the images are read
+
+    // the values' first columns, on their way until the inverse is there
+    const Rsrc rv = grad_rows<E>(p.v, ch.row, h, p.H, V, ch.len);
+    const Rsrc ro = grad_rows<EO>(p.dout, ch.row, h, p.H, V, ch.len);
+    const uint32_t vstep = (uint32_t)p.H * V;
+    uint32_t vraw[4][4], oraw[4][4];
+    auto load_values = [&](int n) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t at =
+                    n < V / 16 ? (16 * t + 4 * gq + s) * vstep + 16 * n + x : kOffMasked / 4;
+                vraw[t][s] = grad_raw1<E>(rv, at * E::kBytes);
+                oraw[t][s] = grad_raw1<EO>(ro, at * EO::kBytes);
+            }
+    };
+    load_values(w);
 
     // the matrices: A to memory, L = A B and P to LDS
     float *Mm = lds, *Pm = lds + kMat, *Lm = lds + 2 * kMat;
@@ -433,7 +496,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
     put(2 * (w >> 1) + 1, 2 * (w >> 1), o16, !(w & 1), w & 1);
     put(ti, tj, oA, true, false);
     put(ti, tj, oP, false, true);
-    __syncthreads();
+    grad_lds_barrier();
 
     // M = (I + L)^-1: diagonal blocks by substitution, then merged twice
     {
@@ -451,7 +514,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
 #pragma unroll
             for (int r = 0; r < 16; ++r) Mm[(16 * w + r) * kMatRow + 16 * w + x] = m[r];
     }
-    __syncthreads();
+    grad_lds_barrier();
     auto left = [&](const float *mat, int bi, int bj) {  // operand a: rows of a tile
         return as4(mat + (16 * bi + x) * kMatRow + 16 * bj + 4 * gq);
     };
@@ -471,7 +534,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         const f4 t = mm16(left(Lm, a, b), right(Mm, b, b), zero4);
         keep(a, b, -mm16(left(Mm, a, a), t, zero4));
     }
-    __syncthreads();
+    grad_lds_barrier();
     if (w < 2) {
         f4 t2 = zero4, t3 = zero4;
         for (int c = w; c < 2; ++c) {
@@ -482,7 +545,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         keep(2, w, -mm16(left(Mm, 2, 2), t2, zero4));
         keep(3, w, -mm16(left(Mm, 3, 3), t3, mm16(left(Mm, 3, 2), t2, zero4)));
     }
-    __syncthreads();
+    grad_lds_barrier();
 
     // k e^G by tokens, in L's place; M to memory
     float *Kg = Lm;
@@ -492,7 +555,7 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         const int r = e / (kGC / 4), c = e % (kGC / 4) * 4;
         if (c / 16 <= r / 16) as4(ws.M() + r * kGC + c) = as4(&Mm[r * kMatRow + c]);
     }
-    __syncthreads();
+    grad_lds_barrier();
 
     // W = M (k e^G); the transposed accumulators hold four adjacent channels of a row
     for (int n = w; n < NT; n += 4) {
@@ -510,19 +573,16 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         }
     }
     // X = M V, dU = P^T O', still without the states
-    const Rsrc rv = grad_rows<E>(p.v, ch.row, h, p.H, V, ch.len);
-    const Rsrc ro = grad_rows<EO>(p.dout, ch.row, h, p.H, V, ch.len);
-    const uint32_t vstep = (uint32_t)p.H * V;
     for (int n = w; n < V / 16; n += 4) {
         f4 b[4], o[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const uint32_t at = (16 * t + 4 * gq + s) * vstep + 16 * n + x;
-                b[t][s] = load1<E>(rv, at * E::kBytes);
-                o[t][s] = load1<EO>(ro, at * EO::kBytes) * p.scale;
+                b[t][s] = grad_widen<E>(vraw[t][s]);
+                o[t][s] = grad_widen<EO>(oraw[t][s]) * p.scale;
             }
+        load_values(n + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             f4 acc = zero4, up = zero4;
@@ -544,14 +604,6 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
 }
 
 // -------------------------------------------------------------------- the walks
-
-// Barrier of the workgroup that orders LDS alone: loads and stores of memory stay
-// in flight.
-__device__ __forceinline__ void grad_lds_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 // A workgroup's columns of a request and head: CT tiles of 16. Each of its four
 // wavefronts owns a quarter of the state's channels and adds its part of W S (or
