@@ -75,7 +75,7 @@ struct GradWork {
     __device__ __forceinline__ float *M() const { return base + kGC * kGC; }       // (I + A B)^-1
     __device__ __forceinline__ float *W() const { return M() + kGC * kGC; }        // [C][K]
     __device__ __forceinline__ float *Kb() const { return W() + kGC * K; }         // k e^{G - G_i}
-    __device__ __forceinline__ float *Qt() const { return Kb() + kGC * K; }        // q e^G, [K][C]
+    __device__ __forceinline__ float *Qt() const { return Kb() + kGC * K; }        // q e^G
     __device__ __forceinline__ float *decay() const { return Qt() + kGC * K; }     // e^G, [K]
     __device__ __forceinline__ float *beta() const { return decay() + K; }         // [C]
     // the first row, the number of rows (0: no such chunk), whether it is padding
@@ -439,12 +439,11 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
         if (w >= 2) image(imQ, w - 2, T) = q[T] * half;
         const f4 before = u1 * t[0] + u2 * t[1] + u3 * t[2];
         const f4 behind = d2 * t[3] + d1 * t[2] + d0 * t[1];
-        // operands of the walks: k e^{G - G_i} by tokens, q e^G by channels
+        // operands of the walks, by tokens: k e^{G - G_i}, q e^G
         const f4 eg = exp2(pre[T] + before), kb = k[T] * exp2(suf[T] + behind), qg = q[T] * eg;
         kg[T] = k[T] * eg;
         as4(ws.Kb() + tok * K + 16 * T + 4 * gq) = kb;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) ws.Qt()[(16 * T + 4 * gq + s) * kGC + tok] = qg[s];
+        as4(ws.Qt() + tok * K + 16 * T + 4 * gq) = qg;
         if (w == 0 && x == 0) as4(ws.decay() + 16 * T + 4 * gq) = exp2(t[0] + t[1] + t[2] + t[3]);
     }
     grad_lds_barrier();
@@ -659,13 +658,13 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
 
     f4 lhs[4][NT], rhs[NT][4], qt[NT][4], x0[CT], beta, decay[NT];
     uint32_t o[CT][4];
-    auto load_first = [&](const GradWork<K> &ws) {  // for W S or (k e^{G - G_i}) dS
+    // Operands are loaded tile row by tile row, each right behind the products that
+    // read its predecessor: 32 loads at once would hold the wavefront up.
+    auto load_first = [&](const GradWork<K> &ws, int i) {  // for W S or (k e^{G - G_i}) dS
         const Rsrc r = grad_floats(BACK ? ws.Kb() : ws.W(), kGC * K);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int T = 0; T < NT; ++T)
-                lhs[i][T] = load4<F32>(r, 4 * ((16 * i + x) * K + c0 + 16 * T + 4 * gq));
+        for (int T = 0; T < NT; ++T)
+            lhs[i][T] = load4<F32>(r, 4 * ((16 * i + x) * K + c0 + 16 * T + 4 * gq));
     };
     auto load_join = [&](const GradWork<K> &ws) {
         const Rsrc r = grad_floats(BACK ? ws.U() : ws.X(), kGC * V);
@@ -688,36 +687,37 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
                                                  16 * c) * EO::kBytes);
         }
     };
-    auto load_middle = [&](const GradWork<K> &ws) {
-        const Rsrc rq = grad_floats(ws.Qt(), kGC * K), rd = grad_floats(ws.decay(), K);
+    auto load_decay = [&](const GradWork<K> &ws) {
+        const Rsrc rd = grad_floats(ws.decay(), K);
 #pragma unroll
-        for (int T = 0; T < NT; ++T) {
-            decay[T] = load4<F32>(rd, 4 * (c0 + 16 * T + 4 * gq));
-            if constexpr (BACK)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    qt[T][t] =
-                        load4<F32>(rq, 4 * ((c0 + 16 * T + x) * kGC + 16 * t + 4 * gq));
-        }
+        for (int T = 0; T < NT; ++T) decay[T] = load4<F32>(rd, 4 * (c0 + 16 * T + 4 * gq));
     };
-    auto load_last = [&](const GradWork<K> &ws) {
-        const Rsrc r = grad_floats(BACK ? ws.W() : ws.Kb(), kGC * K);
+    auto load_rows = [&](float *rows, f4 (&to)[NT][4], int t) {  // as a left operand, across
+        const Rsrc r = grad_floats(rows, kGC * K);
 #pragma unroll
-        for (int T = 0; T < NT; ++T)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    rhs[T][t][s] = load1<F32>(r, 4 * ((16 * t + 4 * gq + s) * K + c0 + 16 * T + x));
+            for (int T = 0; T < NT; ++T)
+                to[T][t][s] = load1<F32>(r, 4 * ((16 * t + 4 * gq + s) * K + c0 + 16 * T + x));
+    };
+    auto load_middle = [&](const GradWork<K> &ws, int t) {
+        if constexpr (BACK) load_rows(ws.Qt(), qt, t);
+    };
+    auto load_last = [&](const GradWork<K> &ws, int t) {
+        load_rows(BACK ? ws.W() : ws.Kb(), rhs, t);
     };
     auto chunk_of = [&](int j) { return BACK ? chunks - 1 - j : j; };
     if (chunks > 0) {
         const GradWork<K> ws(work, V, (long)(slot0 + chunk_of(0)) * H + h);
         load_dout(chunk_of(0));
-        load_first(ws);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_first(ws, i);
         load_join(ws);
-        load_middle(ws);
-        load_last(ws);
+        load_decay(ws);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) load_middle(ws, t);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) load_last(ws, t);
     }
     for (int j = 0; j < chunks; ++j) {
         const GradWork<K> ws(work, V, (long)(slot0 + chunk_of(j)) * H + h);
@@ -734,14 +734,16 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
         load_dout(jn);
         f4 acc[4][CT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 acc[i][c] = zero4;
 #pragma unroll
                 for (int T = 0; T < NT; ++T) acc[i][c] = mm16(lhs[i][T], S[T][c], acc[i][c]);
             }
-        load_first(next);
+            load_first(next, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -781,32 +783,34 @@ __device__ __forceinline__ void grad_walk(const DeltaGradProblem &p, int n, int 
         }
         load_join(next);
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            f4 og[4];
-            if constexpr (BACK)
+        for (int T = 0; T < NT; ++T)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) og[t] = as4(&lds.o[t * CT + c][lane * 4]);
+            for (int c = 0; c < CT; ++c) S[T][c] *= decay[T];
+        load_decay(next);
+        // S += tile column t of the operand, times tile row t of u
+        auto add = [&](const f4 (&to)[NT][4], const float (*u)[kWave * 4], int t) {
+            f4 b[CT];
 #pragma unroll
-            for (int T = 0; T < NT; ++T) {
-                S[T][c] *= decay[T];
-                if constexpr (BACK)
+            for (int c = 0; c < CT; ++c) b[c] = as4(&u[t * CT + c][lane * 4]);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) S[T][c] = mm16(qt[T][t], og[t], S[T][c]);
+            for (int T = 0; T < NT; ++T)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) S[T][c] = mm16(to[T][t], b[c], S[T][c]);
+        };
+        if constexpr (BACK)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                add(qt, lds.o, t);
+                load_middle(next, t);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
-        load_middle(next);
         grad_lds_barrier();
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            f4 u[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) u[t] = as4(&lds.u[t * CT + c][lane * 4]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int T = 0; T < NT; ++T) S[T][c] = mm16(rhs[T][t], u[t], S[T][c]);
+        for (int t = 0; t < 4; ++t) {
+            add(rhs, lds.u, t);
+            load_last(next, t);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        load_last(next);
     }
     if (BACK && pool.base != nullptr) {
         const bool cont = request_continues(pool, n);
