@@ -844,18 +844,18 @@ __global__ __launch_bounds__(256, 2) void kda_grad_walk_kernel(DeltaGradProblem 
 
 // ------------------------------------------------------------ gradients of a chunk
 
-// LDS of the last kernel (bytes): parts of Y and X of up to 128 value columns
-// (rows 16 bytes apart in their banks), dout if it is bfloat16 (one part), the two
-// matrices (first the inverse in dA's place), and per token beta, X.dU, the column
-// sums of A * E by tile rows and, with one gate per head, dg by wavefronts.
-template <int K>
+// LDS of the last kernel (bytes): parts of Y and X of up to VB value columns (rows
+// 16 bytes apart in their banks), dout if it is kept (bfloat16, one part), the
+// inverse and then dA in its place, dP in X's place, and per token beta, X.dU, the
+// column sums of A * E by tile rows and, with one gate per head, dg by wavefronts.
+template <int K, int VB, bool DOUT>
 struct GradLds {
-    static constexpr int VB = 128, RS = 2 * VB + 16, PART = kGC * RS, kMat = kGC * kMatRow * 4;
-    static constexpr int Y = 0, X = Y + kParts * PART, O = X + kParts * PART, A = O + PART;
-    static constexpr int P = A + kMat, BETA = P + kMat, XDU = BETA + kGC * 4;
-    static constexpr int COLS = XDU + kGC * 4, DG = COLS + 4 * kGC * 4;
+    static constexpr int RS = 2 * VB + 16, PART = kGC * RS, kMat = kGC * kMatRow * 4;
+    static constexpr int Y = 0, X = Y + kParts * PART, O = X + kParts * PART;
+    static constexpr int A = O + (DOUT ? PART : 0), P = X, BETA = A + kMat;
+    static constexpr int XDU = BETA + kGC * 4, COLS = XDU + kGC * 4, DG = COLS + 4 * kGC * 4;
     static constexpr int kBytes = DG + K / 16 * kGC * 4;
-    static_assert(kBytes <= 160 * 1024);
+    static_assert(kMat <= kParts * PART && kBytes <= (VB == 64 ? 80 : 160) * 1024);
 };
 // Eight adjacent elements of dout as an operand (bfloat16: all in its first part).
 template <class EO>
@@ -871,12 +871,15 @@ __device__ __forceinline__ Operand grad_operand(Rsrc r, uint32_t off) {
 // lane's four tokens, are vector instructions (1.39 -> 1.31 ms for this kernel with
 // the operands of E taken as they lie); from 4 on a level is one product of
 // masked tiles. ONE: all value columns at once (up to 128; with a loop over them the
-// sums take registers from what is loaded ahead).
-template <class E, class EO, int K, bool ONE>
-__global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel(DeltaGradProblem p) {
-    typedef GradLds<K> L;
-    constexpr int NW = K / 16, VB = L::VB;
-    constexpr bool kExact = EO::kBytes == 2 && !__is_same(EO, F16);  // dout is one bfloat16 part
+// sums take registers from what is loaded ahead). With K = 64 and up to 64 columns
+// two workgroups of four wavefronts share a unit (8,161 tokens of 8 heads, f32: 124 -> 88 us).
+template <class E, class EO, int K, int VB, bool ONE>
+__global__ __launch_bounds__(K * 4, K == 128 || VB == 64 ? 2 : 1) void kda_grad_chunk_kernel(
+    DeltaGradProblem p) {
+    constexpr int NW = K / 16;
+    // dout is one bfloat16 part (which two workgroups' LDS does not hold)
+    constexpr bool kExact = VB == 128 && EO::kBytes == 2 && !__is_same(EO, F16);
+    typedef GradLds<K, VB, kExact> L;
     __shared__ __align__(16) char lds[L::kBytes];
     const int lane = threadIdx.x & (kWave - 1);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -1492,6 +1495,14 @@ __global__ __launch_bounds__(K * 4, K == 128 ? 2 : 1) void kda_grad_chunk_kernel
     }
 }
 
+template <class E>
+__device__ __forceinline__ void grad_put4(typename E::T *p, f4 v) {
+    if constexpr (E::kBytes == 4)
+        *reinterpret_cast<f4 *>(p) = v;
+    else
+        *reinterpret_cast<w2 *>(p) = w2{Elem<E>::pack(v[0], v[1]), Elem<E>::pack(v[2], v[3])};
+}
+
 // Gradients of shared key heads: the sum over the value heads that read them, in
 // order, so its bits are the same every time. Bound by memory: it reads FP32 rows
 // of every value head (18 us on 8,161 tokens, 8 heads over 4 of 64).
@@ -1501,18 +1512,18 @@ __global__ __launch_bounds__(256) void kda_grad_shared_kernel(DeltaGradProblem p
     const int hk = (int)(blockIdx.x % p.Hk), slot = (int)(blockIdx.x / p.Hk);
     const GradChunk ch = grad_chunk(p.req, slot, lane);
     const int group = p.H / p.Hk;
-    for (int e = threadIdx.x; e < ch.len * K; e += 256) {
-        const long row = ch.row + e / K;
-        const int c = e % K;
+    for (int e = threadIdx.x; e < ch.len * (K / 4); e += 256) {  // four channels to a lane
+        const long row = ch.row + e / (K / 4);
+        const int c = e % (K / 4) * 4;
         const long from = (row * p.H + (long)hk * group) * K + c;
-        float a = 0.0f, b = 0.0f;
+        f4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
         for (int i = 0; i < group; ++i) {
-            a += p.dq_head[from + (long)i * K];
-            b += p.dk_head[from + (long)i * K];
+            a += as4(p.dq_head + from + (long)i * K);
+            b += as4(p.dk_head + from + (long)i * K);
         }
         const long to = (row * p.Hk + hk) * K + c;
-        grad_put<E>(static_cast<typename E::T *>(p.dq) + to, a);
-        grad_put<E>(static_cast<typename E::T *>(p.dk) + to, b);
+        grad_put4<E>(static_cast<typename E::T *>(p.dq) + to, a);
+        grad_put4<E>(static_cast<typename E::T *>(p.dk) + to, b);
     }
 }
 
@@ -1539,8 +1550,10 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (p.req.total_tokens > 0) {
-        const auto fn = p.V <= GradLds<K>::VB ? kda_grad_chunk_kernel<E, EO, K, true>
-                                              : kda_grad_chunk_kernel<E, EO, K, false>;
+        auto fn = p.V <= 128 ? kda_grad_chunk_kernel<E, EO, K, 128, true>
+                             : kda_grad_chunk_kernel<E, EO, K, 128, false>;
+        if constexpr (K == 64)
+            if (p.V <= 64) fn = kda_grad_chunk_kernel<E, EO, K, 64, true>;
         hipLaunchKernelGGL(fn, dim3(items), dim3(K * 4), 0, stream, p);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         if (p.Hk != p.H)
