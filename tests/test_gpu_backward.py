@@ -129,6 +129,8 @@ CASES = [
     ([70, 2, 64], 2, 2, 128, 32, "f32", "f32", "channel", "steep", 3),
     ([100, 31], 3, 1, 64, 128, "f32", "f32", "head", "steep", 2),
     ([500], 1, 1, 128, 128, "f32", "f32", "channel", "mixed", 1),
+    ([100, 64], 4, 2, 64, 64, "bf16", "bf16", "channel", "mixed", 3),
+    ([70, 9], 2, 1, 64, 64, "f32", "f32", "channel", "steep", 2),
 ]
 
 
@@ -365,6 +367,20 @@ def test_delta_many_walks(kt, V):
         alone = _run_delta(kt, one)
         for x in got:
             assert torch.equal(got[x][a:b], alone[x]), (i, x)
+
+
+def test_delta_long_workspace(kt):
+    """Requests whose part of the workspace lies past 2^33 bytes give what they do
+    alone."""
+    n, H = 600, 64
+    d, _ = _delta([1] * n, H, H, 128, 128, "bf16", "bf16", seed=16)
+    assert kt.kda_prefill_backward_workspace_size(n, n, H, H, 128, 128) > 2 ** 33
+    got = _run_delta(kt, d)
+    for i in (0, 399, 405, n - 1):
+        one = {x: d[x][i:i + 1] for x in ("q", "k", "v", "g", "beta", "dout")}
+        alone = _run_delta(kt, {**one, "cu": _cu([1])})
+        for x in got:
+            assert torch.equal(got[x][i:i + 1], alone[x]), (i, x)
 
 
 # ----------------------------------------------------------------- convolution

@@ -37,13 +37,13 @@
 // kernel over value columns, which take six bfloat16 products of three parts (see
 // bf16_parts.h). FP32 outputs are 1e-7 to 4e-7 of their norm from 64 bits.
 //
-// What bounds it (16 x 512 tokens of 64 heads, K = V = 128, bf16: 3.15 ms, 0.77 +
-// 1.25 + 1.28 in the three kernels; one sequence of 16,384 tokens and 32 heads
-// 3.33 ms, 0.77 + 1.45 + 1.24): the traffic of the workspace (10 GB a call, 3.2, 3.2
-// and 2.8 TB/s of a copy's 5.1) and the chains between barriers, which the
+// What bounds it (16 x 512 tokens of 64 heads, K = V = 128, bf16: 3.02 ms, 0.69 +
+// 1.18 + 1.28 in the three kernels under a trace; one sequence of 16,384 tokens and
+// 32 heads 3.00 ms, 0.69 + 1.18 + 1.26): the traffic of the workspace (9.9 GB a call,
+// 3.5, 3.3 and 2.8 TB/s of a copy's 5.1) and the chains between barriers, which the
 // few wavefronts that their registers and LDS leave room for do not cover (two to a
-// SIMD). The matrix pipes are busy for 38, 49 and 26% of the cycles, the vector
-// units for 29, 10 and 35%.
+// SIMD). The matrix pipes are busy for 34, 52 and 26% of the cycles, the vector
+// units for 34, 10 and 35%.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -610,12 +610,15 @@ __global__ __launch_bounds__(256, 2) void kda_grad_prepare_kernel(DeltaGradProbl
 // makes X (or dU) of it, and every wavefront updates its channels with the whole
 // U. So one step of the chain is a quarter of the products, two exchanges in LDS
 // and another quarter, and the operands of the next chunk are on their way
-// meanwhile. (One wavefront with all channels: a call of 16,384 tokens and 32 heads
-// took 15.4 ms, 5.3 so, and now 3.3. Six bfloat16 products, 0.75 of the matrix time
-// of FP32's, lose: the splits are vector instructions in the chain, 1.92 ms instead
-// of 1.48, and on 16 x 512 tokens of 64 heads 1.43 instead of 1.26.)
-// Bound by the chain with one sequence (256 steps of 5.7 us), by the states' traffic
-// with many (16 x 512 tokens: 4 GB in 1.25 ms; the products alone take 0.76).
+// meanwhile, a tile row behind the products that read it: all of them at once hold the
+// wavefront up (one sequence of 16,384 tokens and 32 heads 1.45 ms, 1.18 so; loads
+// spread evenly between the products, or the states' stores among them, 1.18 to
+// 1.28). One wavefront with all channels made that call 15.4 ms instead of 5.3. Six
+// bfloat16 products, 0.75 of the matrix time of FP32's, lost: the splits are vector
+// instructions in the chain (1.92 ms then, for 1.48).
+// Bound by the chain with one sequence (256 steps of 4.6 us, 2.9 of them products of the
+// longer way), by the states' traffic with many (16 x 512 tokens: 3.9 GB in 1.18 ms;
+// the products alone take 0.76).
 template <int CT>
 struct GradWalkLds {
     float part[4][4 * CT][kWave * 4];  // [wavefront][tile row, column tile]
@@ -1537,8 +1540,8 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
     }
     const long walks = (long)p.req.num_seqs * p.H, groups = (walks + 7) / 8;
     // 32 columns to a workgroup halve what the operands cost in L2, 16 columns the
-    // work of a step: one sequence of 4,096 tokens takes 207 us in 16 and 303 in
-    // 32 with 8 heads (128 and 64 workgroups), 440 and 352 with 32 heads.
+    // work of a step: one sequence of 4,096 tokens takes 170 us in 16 and 243 in
+    // 32 with 8 heads (128 and 64 workgroups), 411 and 294 with 32 heads.
     if (2 * walks * (p.V / 16) > device_cus()) {
         const int parts = p.V / 32;
         hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 2>), dim3((unsigned)(groups * 8 * parts), 2),
