@@ -683,3 +683,50 @@ def test_layer(kt, coded):
                              (dbeta, want["dbeta"], "dbeta"), (dx, wx, "dqkv"),
                              (dcw, wcw, "dconv_w")):
         _check(got, right, "f32", name, norm=6e-6, each=2.4e-4)
+
+
+def test_step_in_a_graph(kt):
+    """Checkpoints and all gradients of a step, captured, on pools that the step
+    changes: the eager step's bits on every replay, whatever ran between."""
+    lens, H, d, W, slots = [70, 3, 0, 130], 2, 128, 4, 6
+    T = sum(lens)
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    new = lambda *s, dt=torch.bfloat16: torch.randn(s, generator=gen, device=DEV).to(dt)  # noqa: E731
+    f32 = torch.float32
+    qkv, z, dout, do = new(T, 3, H, d), new(T, H, d), new(T, H, d), new(T, H, d)
+    o, cw, w = new(T, H, d), new(3, W, H, d, dt=f32) * 0.5, 1 + 0.1 * new(d, dt=f32)
+    g, beta = -torch.rand(T, H, d, device=DEV) * 0.3, torch.rand(T, H, device=DEV)
+    q, k, v = (torch.nn.functional.normalize(new(T, H, d).float(), dim=-1).bfloat16()
+               for _ in range(3))
+    state, conv_state = new(slots, H, d, d, dt=f32), new(slots, 3, H, W - 1, d, dt=f32)
+    pools0 = (new(slots, H, d, d, dt=f32), new(slots, 3, H, W - 1, d, dt=f32))
+    slot = torch.tensor([4, 0, 2, -1], dtype=torch.int32, device=DEV)
+    init = torch.tensor([1, 0, 1, 1], dtype=torch.int32, device=DEV)
+    cu = _cu(lens)
+
+    def step(dstate, dconv_state):
+        x8, xs = kt.checkpoint(qkv)
+        out, o8, os, z8, zs = kt.gated_norm_checkpoint(o, z, w)
+        dn, dz, dw = kt.gated_norm_backward(dout, o8, z8, w, o_scale=os, z_scale=zs)
+        dq, dk, dv, dg, dbeta = kt.prefill_backward(dn, q, k, v, g, beta, cu, state, dstate, slot,
+                                                    init)
+        dx, dcw = kt.conv_prefill_backward(dq, dk, dv, x8, cw, cu, conv_state, dconv_state, slot,
+                                           init, qkv_scale=xs)
+        back = kt.checkpoint_load(x8, xs)
+        return [x8, xs, out, o8, os, z8, zs, dn, dz, dw, dq, dk, dv, dg, dbeta, dx, dcw, back]
+
+    pools = [p.clone() for p in pools0]
+    want = step(*pools) + [p.clone() for p in pools]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*pools)
+    for i in range(3):
+        for p, p0 in zip(pools, pools0):
+            p.copy_(p0)
+        for x in got:
+            x.zero_()
+        graph.replay()
+        for n, (a, b) in enumerate(zip(got + pools, want)):
+            assert torch.equal(a, b), (i, n)
+        step(*[p.clone() for p in pools0])
+        torch.cuda.synchronize()
