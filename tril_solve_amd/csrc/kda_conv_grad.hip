@@ -19,7 +19,7 @@
 //
 // Bound by the vector units: the silu, its derivative, 2 W products and the
 // normalisation are 34 instructions to an element, and 84% of the cycles issue
-// one. 16 x 512 tokens of 64 heads of 128, bf16 from 8-bit codes: 242 us (4.2 TB/s;
+// one. 16 x 512 tokens of 64 heads of 128, bf16 from 8-bit codes: 242 to 252 us (4.1 TB/s;
 // one channel to a lane 431). 7,000 tokens of 9 heads of 64, f32: 50 us (2.9 TB/s).
 #include <hip/hip_runtime.h>
 
