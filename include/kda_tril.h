@@ -543,7 +543,9 @@ kda_status kda_prefill_backward_dense(
  * Gradients of kda_conv_prefill_*: dq, dk, dv [T, H, d] (of its outputs) and
  * dqkv [T, 3, H, d] of dtype, dconv_w [3, W, H, d] FP32 (zeros for a call of no
  * tokens). qkv is [T, 3, H, d] of dtype, or, where qkv_scale [T, 3, H] is given,
- * the int8 codes of a checkpoint of it.
+ * the int8 codes of a checkpoint of it. num_seqs < 2^24, and with dconv_state
+ * num_seqs x ceil(3 (W - 1) H d / 1024) + ceil(3 W H d / 1024) < 2^24, else
+ * KDA_ERR_UNSUPPORTED (the workspace query knows of the first limit alone).
  */
 kda_status kda_conv_backward_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H,
                                             int32_t head_dim, int32_t conv_width, size_t *bytes);

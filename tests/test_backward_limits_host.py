@@ -1,0 +1,39 @@
+"""The largest sizes that the backward pass and the checkpoints take (CPU only:
+every call here returns before any launch; one that passes the limits ends at its
+missing workspace or pointers)."""
+import pytest
+
+from tests.test_backward_host import G, P, _conv, kt  # noqa: F401
+
+
+def _window_blocks(H, d, W):
+    return -(-3 * (W - 1) * H * d // 1024)
+
+
+def _tap_blocks(H, d, W):
+    return -(-3 * W * H * d // 1024)
+
+
+@pytest.mark.parametrize("H", [1, 3639, 3640, 4096])
+@pytest.mark.parametrize("d,W", [(64, 2), (128, 4)])
+def test_conv_takes_all_heads(kt, H, d, W):
+    """One request passes with and without the windows' gradients."""
+    for dS in (10 * G, None):
+        assert _conv(kt, n=1, T=1, H=H, hd=d, W=W, dS=dS, wsb=0) == kt.KDA_ERR_WORKSPACE
+    assert kt.kda_conv_backward_workspace_size(1, 1, H, d, W) > 0
+
+
+@pytest.mark.parametrize("H,d,W", [(1, 64, 2), (64, 128, 4), (3639, 128, 4), (4096, 128, 4),
+                                   (5, 64, 3)])
+def test_conv_requests_up_to_the_launch(kt, H, d, W):
+    """The sum kernel's workgroups of 256 threads stay below 2^32 threads in all: the
+    last number of requests that does so passes, the next one does not."""
+    most = (2 ** 24 - 1 - _tap_blocks(H, d, W)) // _window_blocks(H, d, W)
+    slots = dict(slot=1 << 50, init=1 << 51, slots=1, S=None, cu=1 << 52, dS=1 << 53)
+    assert _conv(kt, n=most, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_WORKSPACE
+    assert _conv(kt, n=most + 1, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_UNSUPPORTED
+    # without the windows' gradients that launch has the taps alone
+    slots["dS"] = None
+    assert _conv(kt, n=most + 1, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_WORKSPACE
+    assert _conv(kt, n=2 ** 24 - 1, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_WORKSPACE
+    assert _conv(kt, n=2 ** 24, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_UNSUPPORTED

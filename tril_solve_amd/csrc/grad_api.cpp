@@ -191,9 +191,8 @@ kda_status conv_backward(const void *dq, const void *dk, const void *dv, kda_dty
     if (st != KDA_OK) return st;
     st = check_pools(p.pool, p.grad, conv_state, dconv_state, slot, init, num_slots, num_seqs);
     if (st != KDA_OK) return st;
-    // (workgroups that put the windows' gradients into the pool)
     if (dconv_state != nullptr &&
-        num_seqs > (kMaxItems >> 12) / ((int64_t)3 * H * (W - 1) * d / 1024 + 1) * 4096)
+        num_seqs > (kMaxItems - conv_grad_tap_blocks(H, d, W)) / conv_grad_window_blocks(H, d, W))
         return KDA_ERR_UNSUPPORTED;
     if (!conv_w || !dconv_w || !aligned(conv_w, 16) || !aligned(dconv_w, 16))
         return KDA_ERR_INVALID_ARG;

@@ -305,8 +305,8 @@ __global__ __launch_bounds__(kCgThreads, 2) void kda_conv_grad_kernel(ConvGradPr
 
 // dtaps: the sum of the workgroups' rows, four floats to a lane. Windows: what the
 // first launch left, or zeros where a request starts from zeros; a workgroup to
-// kCgPart floats.
-constexpr long kCgPart = 4 * kCgThreads;
+// kConvGradPart floats.
+static_assert(kConvGradPart == 4 * kCgThreads);
 __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_sum_kernel(ConvGradProblem p, int rows,
                                                                         long taps,
                                                                         unsigned tap_blocks,
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(kCgThreads) void kda_conv_grad_sum_kernel(ConvGradP
         return;
     }
     const int n = (int)((blockIdx.x - tap_blocks) / parts);
-    const long at = (blockIdx.x - tap_blocks) % parts * kCgPart + threadIdx.x * 4L;
+    const long at = (blockIdx.x - tap_blocks) % parts * kConvGradPart + threadIdx.x * 4L;
     const long size = 3L * p.H * (p.W - 1) * p.d;  // a multiple of 4
     const int slot = request_slot(p.grad, n);
     if (slot < 0 || at >= size) return;
@@ -354,8 +354,8 @@ hipError_t launch_conv_grad(const ConvGradProblem &p, int dt, hipStream_t stream
         });
         if (e != hipSuccess) return e;
     }
-    const unsigned tap_blocks = (unsigned)((taps + kCgPart - 1) / kCgPart);
-    const unsigned parts = (unsigned)((taps / p.W * (p.W - 1) + kCgPart - 1) / kCgPart);
+    const unsigned tap_blocks = (unsigned)conv_grad_tap_blocks(p.H, p.d, p.W);
+    const unsigned parts = (unsigned)conv_grad_window_blocks(p.H, p.d, p.W);
     const unsigned windows = p.grad.base != nullptr ? (unsigned)p.req.num_seqs : 0u;
     hipLaunchKernelGGL(kda_conv_grad_sum_kernel, dim3(tap_blocks + windows * parts),
                        dim3(kCgThreads), 0, stream, p, (int)rows, taps, tap_blocks, parts);

@@ -162,6 +162,15 @@ struct ConvGradProblem {
     int32_t seg;          // tokens per wavefront
     float eps_l2;
 };
+// Workgroups of the launch that sums dconv_w and puts the gradients of `windows`
+// requests' windows into the pool: kConvGradPart floats each, the taps' first.
+constexpr int64_t kConvGradPart = 1024;
+inline int64_t conv_grad_tap_blocks(int32_t H, int32_t d, int32_t W) {
+    return ((int64_t)3 * W * H * d + kConvGradPart - 1) / kConvGradPart;
+}
+inline int64_t conv_grad_window_blocks(int32_t H, int32_t d, int32_t W) {  // of one request
+    return ((int64_t)3 * (W - 1) * H * d + kConvGradPart - 1) / kConvGradPart;
+}
 // Rows of dconv_w that the workgroups (four segments each) leave.
 inline int64_t conv_grad_rows(int64_t tokens, int32_t seg) {
     return (tokens + 4 * (int64_t)seg - 1) / (4 * (int64_t)seg);
