@@ -587,7 +587,8 @@ kda_status kda_gated_norm_backward(const void *dout, const void *o, const void *
  * Activation checkpoints in 8 bits. Every vector of d channels is kept as int8
  * codes and one FP32 scale:
  *   scale = max |x| / 127,   code = x / scale to the nearest integer, halves to even
- * (each value off by at most half a step, max |x| / 254). Vectors whose largest
+ * (each value off by at most half a step, max |x| / 254; of the largest float the
+ * scale is the float below, so that 127 steps stay finite). Vectors whose largest
  * magnitude is below 2^-110 are kept as zeros; one that holds a value that is not
  * finite gets a scale of NaN and reads back as NaN.
  *   x       [rows, H, d] of dtype (of kda_conv_prefill's qkv: rows x 3, H).

@@ -47,6 +47,9 @@ __device__ __forceinline__ float lanes_max(float v) {
 // Largest magnitudes below this are stored as zeros: their steps would leave
 // FP32's normal range.
 constexpr float kLeast8 = 0x1p-110f;
+// The largest step of which 127 are finite in FP32: the quotient of the largest
+// float (and of no other) rounds to the one above and would read back as infinity.
+constexpr float kMost8 = 0x1.020406p+121f;
 
 // Codes of x and the vector's scale: the integer nearest x / scale, halves to
 // even, found exactly. x / scale is first taken by 127 / max, off by less
@@ -63,7 +66,7 @@ __device__ __forceinline__ float encode8(const float (&x)[8], int (&c)[8]) {
     for (int i = 0; i < 8; ++i) top = __builtin_elementwise_maximum(top, __builtin_fabsf(x[i]));
     top = lanes_max<L>(top);
     const bool fine = top < __builtin_inff(), some = top >= kLeast8;
-    const float scale = top / 127.0f, half = 0.5f * scale;
+    const float scale = __builtin_fminf(top / 127.0f, kMost8), half = 0.5f * scale;
     const float inv = fine && some ? 127.0f / top : 0.0f;
     float n[8], worst = 0.0f;
 #pragma unroll
