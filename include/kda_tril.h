@@ -572,7 +572,7 @@ kda_status kda_conv_backward_dense(const void *dq, const void *dk, const void *d
  * Gradients of kda_gated_norm: dout (of its output), d_o and dz [rows, H, d] of
  * dtype, dnorm_w [d] FP32 (zeros for a call of no rows). o and z are of dtype, or,
  * where o_scale and z_scale [rows, H] are given (both or neither), the int8 codes
- * of checkpoints of them.
+ * of checkpoints of them. rows x H < 2^28, else KDA_ERR_UNSUPPORTED.
  */
 kda_status kda_gated_norm_backward_workspace_size(int64_t rows, int32_t H, int32_t head_dim,
                                                   size_t *bytes);
@@ -596,7 +596,8 @@ kda_status kda_gated_norm_backward(const void *dout, const void *o, const void *
  * kda_checkpoint writes codes and scale, kda_checkpoint_load writes
  * out = code x scale. kda_gated_norm_checkpoint is kda_gated_norm (the same bits)
  * that also writes the checkpoints of o and z.
- * head_dim 64 or 128, else KDA_ERR_UNSUPPORTED; rows x H < 2^28.
+ * head_dim 64 or 128, rows x H < 2^28 (with 128 channels at most 2^28 - 16), else
+ * KDA_ERR_UNSUPPORTED.
  */
 kda_status kda_checkpoint(const void *x, kda_dtype dtype, int8_t *codes, float *scale,
                           int64_t rows, int32_t H, int32_t head_dim, hipStream_t stream);

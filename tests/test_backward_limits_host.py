@@ -37,3 +37,34 @@ def test_conv_requests_up_to_the_launch(kt, H, d, W):
     assert _conv(kt, n=most + 1, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_WORKSPACE
     assert _conv(kt, n=2 ** 24 - 1, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_WORKSPACE
     assert _conv(kt, n=2 ** 24, H=H, hd=d, W=W, wsb=0, **slots) == kt.KDA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 5, 16, 4096])
+@pytest.mark.parametrize("d", [64, 128])
+def test_vectors_up_to_the_launch(kt, H, d):
+    """rows x H < 2^28, and no launch of 2^32 threads: workgroups of 256, d / 8 lanes
+    to a vector."""
+    L, far = kt._lib, [P(i << 50) for i in range(1, 9)]
+
+    def norm(rows):
+        return L.kda_gated_norm_backward(*far[:3], 0, None, None, *far[3:7], rows, H, d, 1e-6,
+                                         None, 0, None)
+
+    def save(rows):
+        return L.kda_checkpoint(None, 0, *far[:2], rows, H, d, None)
+
+    def load(rows):
+        return L.kda_checkpoint_load(None, *far[:2], 0, rows, H, d, None)
+
+    def both(rows):
+        return L.kda_gated_norm_checkpoint(None, *far[:1], 0, *far[1:3], 0, *far[3:7], rows, H, d,
+                                           1e-6, None)
+
+    most = (2 ** 28 - 1) // H
+    assert norm(most) == kt.KDA_ERR_WORKSPACE and norm(most + 1) == kt.KDA_ERR_UNSUPPORTED
+    if d == 128:
+        most = (2 ** 28 - 16) // H
+    assert -(-most * H * (d // 8) // 256) * 256 < 2 ** 32
+    for call in (save, load, both):
+        assert call(most) == kt.KDA_ERR_INVALID_ARG  # past the sizes, at the null pointer
+        assert call(most + 1) == kt.KDA_ERR_UNSUPPORTED
