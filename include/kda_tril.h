@@ -470,7 +470,8 @@ kda_status kda_recurrent_dense(const void *q, const void *k, const void *v, kda_
  * Gated RMSNorm of `rows` x H vectors, the decode step's last stage:
  *   out = o / sqrt(mean(o^2) + eps_norm) * norm_w * sigmoid(z)
  * o, z [rows, H, d] of in_dtype, out of out_dtype, norm_w [d]. head_dim 64 or
- * 128, else KDA_ERR_UNSUPPORTED. out may be o itself when the types are equal.
+ * 128, rows x H < 2^28 (with 128 channels at most 2^28 - 16), else
+ * KDA_ERR_UNSUPPORTED. out may be o itself when the types are equal.
  */
 kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, const float *norm_w,
                           void *out, kda_dtype out_dtype, int64_t rows, int32_t H,

@@ -1,6 +1,6 @@
-"""The largest sizes that the backward pass and the checkpoints take (CPU only:
-every call here returns before any launch; one that passes the limits ends at its
-missing workspace or pointers)."""
+"""The largest sizes that the backward pass, the checkpoints and the gated norm take
+(CPU only: every call here returns before any launch; one that passes the limits ends
+at its missing workspace or pointers)."""
 import pytest
 
 from tests.test_backward_host import G, P, _conv, kt  # noqa: F401
@@ -60,11 +60,14 @@ def test_vectors_up_to_the_launch(kt, H, d):
         return L.kda_gated_norm_checkpoint(None, *far[:1], 0, *far[1:3], 0, *far[3:7], rows, H, d,
                                            1e-6, None)
 
+    def forward(rows):
+        return L.kda_gated_norm(None, *far[:1], 0, *far[1:3], 0, rows, H, d, 1e-6, None)
+
     most = (2 ** 28 - 1) // H
     assert norm(most) == kt.KDA_ERR_WORKSPACE and norm(most + 1) == kt.KDA_ERR_UNSUPPORTED
     if d == 128:
         most = (2 ** 28 - 16) // H
     assert -(-most * H * (d // 8) // 256) * 256 < 2 ** 32
-    for call in (save, load, both):
+    for call in (save, load, both, forward):
         assert call(most) == kt.KDA_ERR_INVALID_ARG  # past the sizes, at the null pointer
         assert call(most + 1) == kt.KDA_ERR_UNSUPPORTED

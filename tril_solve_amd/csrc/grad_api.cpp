@@ -12,9 +12,7 @@ using namespace kda;
 
 namespace {
 
-constexpr int64_t kMaxItems = ((int64_t)1 << 24) - 1;   // 256 threads each, below 2^32 in all
 constexpr int64_t kMaxChunks = ((int64_t)1 << 23) - 1;  // 512 threads each
-constexpr int64_t kMaxVectors = ((int64_t)1 << 28) - 1;
 
 // Writable arguments overlap neither each other nor anything that is read.
 template <size_t N, size_t M>
@@ -248,18 +246,6 @@ kda_status dense_tokens(int64_t B, int64_t T) {
 
 // --------------------------------------------------------- norm and checkpoints
 
-kda_status vector_sizes(int64_t rows, int32_t H, int32_t d) {
-    if (rows < 0 || H <= 0 || d <= 0) return KDA_ERR_INVALID_ARG;
-    if (rows > kMaxTokens || H > kMaxHeads || (d != 64 && d != 128) || rows > kMaxVectors / H)
-        return KDA_ERR_UNSUPPORTED;
-    return KDA_OK;
-}
-// Likewise for the checkpoints, which take d / 8 lanes to a vector in workgroups of
-// 256: below 2^32 threads in all, the last workgroup's idle ones counted.
-kda_status code_sizes(int64_t rows, int32_t H, int32_t d) {
-    const kda_status st = vector_sizes(rows, H, d);
-    return st == KDA_OK && rows * H * (d / 8) > kMaxItems * 256 ? KDA_ERR_UNSUPPORTED : st;
-}
 size_t norm_bytes(int64_t rows, int32_t H, int32_t d) {
     return (size_t)norm_grad_blocks(rows * H, d) * d * 4;
 }
@@ -400,7 +386,7 @@ kda_status kda_gated_norm_backward(const void *dout, const void *o, const void *
 kda_status kda_checkpoint(const void *x, kda_dtype dtype, int8_t *codes, float *scale,
                           int64_t rows, int32_t H, int32_t head_dim, hipStream_t stream) {
     if (!valid_dtype(dtype)) return KDA_ERR_INVALID_ARG;
-    const kda_status st = code_sizes(rows, H, head_dim);
+    const kda_status st = vector_launch_sizes(rows, H, head_dim);
     if (st != KDA_OK || rows == 0) return st;
     if (!x || !codes || !scale || !aligned(x, 16) || !aligned(codes, 8) || !aligned(scale, 4))
         return KDA_ERR_INVALID_ARG;
@@ -422,7 +408,7 @@ kda_status kda_checkpoint_load(const int8_t *codes, const float *scale, void *ou
                                kda_dtype out_dtype, int64_t rows, int32_t H, int32_t head_dim,
                                hipStream_t stream) {
     if (!valid_dtype(out_dtype)) return KDA_ERR_INVALID_ARG;
-    const kda_status st = code_sizes(rows, H, head_dim);
+    const kda_status st = vector_launch_sizes(rows, H, head_dim);
     if (st != KDA_OK || rows == 0) return st;
     if (!codes || !scale || !out || !aligned(codes, 8) || !aligned(scale, 4) || !aligned(out, 16))
         return KDA_ERR_INVALID_ARG;
@@ -447,7 +433,7 @@ kda_status kda_gated_norm_checkpoint(const void *o, const void *z, kda_dtype in_
                                      float eps_norm, hipStream_t stream) {
     if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || bad_eps(eps_norm))
         return KDA_ERR_INVALID_ARG;
-    const kda_status st = code_sizes(rows, H, head_dim);
+    const kda_status st = vector_launch_sizes(rows, H, head_dim);
     if (st != KDA_OK || rows == 0) return st;
     if (!o || !z || !norm_w || !out || !o_codes || !o_scale || !z_codes || !z_scale ||
         !aligned(o, 16) || !aligned(z, 16) || !aligned(out, 16) || !aligned(norm_w, 4) ||

@@ -297,14 +297,10 @@ kda_status kda_recurrent_dense(const void *q, const void *k, const void *v, kda_
 kda_status kda_gated_norm(const void *o, const void *z, kda_dtype in_dtype, const float *norm_w,
                           void *out, kda_dtype out_dtype, int64_t rows, int32_t H,
                           int32_t head_dim, float eps_norm, hipStream_t stream) {
-    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || rows < 0 || H <= 0 ||
-        head_dim <= 0 || bad_eps(eps_norm))
+    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype) || bad_eps(eps_norm))
         return KDA_ERR_INVALID_ARG;
-    // 16 lanes per vector at most, fewer than 2^32 threads
-    if (rows > kMaxTokens || H > kMaxHeads || (head_dim != 64 && head_dim != 128) ||
-        rows > ((int64_t)1 << 28) / H - 1)
-        return KDA_ERR_UNSUPPORTED;
-    if (rows == 0) return KDA_OK;
+    const kda_status st = vector_launch_sizes(rows, H, head_dim);
+    if (st != KDA_OK || rows == 0) return st;
     if (!o || !z || !norm_w || !out) return KDA_ERR_INVALID_ARG;
     if (!aligned(o, 16) || !aligned(z, 16) || !aligned(out, 16) || !aligned(norm_w, 4))
         return KDA_ERR_INVALID_ARG;

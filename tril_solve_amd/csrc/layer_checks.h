@@ -15,6 +15,8 @@ constexpr int32_t kMaxHeads = 4096;
 // (request, head) pairs of one launch: at most 512 threads each, fewer than
 // 2^32 threads in all
 constexpr int64_t kMaxPairs = ((int64_t)1 << 23) - 1;
+constexpr int64_t kMaxItems = ((int64_t)1 << 24) - 1;  // 256 threads each, likewise
+constexpr int64_t kMaxVectors = ((int64_t)1 << 28) - 1;
 
 inline bool valid_dtype(kda_dtype d) { return d == KDA_F32 || d == KDA_BF16 || d == KDA_F16; }
 inline size_t dtype_bytes(kda_dtype d) { return d == KDA_F32 ? 4 : 2; }
@@ -72,6 +74,20 @@ inline kda_status check_pool(Pool &p, float *base, const int32_t *slot, const in
     p.init = init;
     p.num_slots = (int32_t)num_slots;
     return KDA_OK;
+}
+
+// rows x H vectors of d channels.
+inline kda_status vector_sizes(int64_t rows, int32_t H, int32_t d) {
+    if (rows < 0 || H <= 0 || d <= 0) return KDA_ERR_INVALID_ARG;
+    if (rows > kMaxTokens || H > kMaxHeads || (d != 64 && d != 128) || rows > kMaxVectors / H)
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+// Likewise for a launch that takes d / 8 lanes to a vector in workgroups of 256: below
+// 2^32 threads in all, the last workgroup's idle ones counted.
+inline kda_status vector_launch_sizes(int64_t rows, int32_t H, int32_t d) {
+    const kda_status st = vector_sizes(rows, H, d);
+    return st == KDA_OK && rows * H * (d / 8) > kMaxItems * 256 ? KDA_ERR_UNSUPPORTED : st;
 }
 
 }  // namespace kda
