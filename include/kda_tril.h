@@ -547,6 +547,9 @@ kda_status kda_prefill_backward_dense(
  * the int8 codes of a checkpoint of it. num_seqs < 2^24, and with dconv_state
  * num_seqs x ceil(3 (W - 1) H d / 1024) + ceil(3 W H d / 1024) < 2^24, else
  * KDA_ERR_UNSUPPORTED (the workspace query knows of the first limit alone).
+ *
+ * A value that is not finite reaches dqkv, dconv_w and the window's gradient of its
+ * projection and head, dqkv within conv_width - 1 tokens of its own request.
  */
 kda_status kda_conv_backward_workspace_size(int64_t total_tokens, int64_t num_seqs, int32_t H,
                                             int32_t head_dim, int32_t conv_width, size_t *bytes);
@@ -573,7 +576,8 @@ kda_status kda_conv_backward_dense(const void *dq, const void *dk, const void *d
  * Gradients of kda_gated_norm: dout (of its output), d_o and dz [rows, H, d] of
  * dtype, dnorm_w [d] FP32 (zeros for a call of no rows). o and z are of dtype, or,
  * where o_scale and z_scale [rows, H] are given (both or neither), the int8 codes
- * of checkpoints of them. rows x H < 2^28, else KDA_ERR_UNSUPPORTED.
+ * of checkpoints of them. rows x H < 2^28, else KDA_ERR_UNSUPPORTED. A value that is
+ * not finite reaches d_o and dz of its vector, and dnorm_w.
  */
 kda_status kda_gated_norm_backward_workspace_size(int64_t rows, int32_t H, int32_t head_dim,
                                                   size_t *bytes);
@@ -596,7 +600,7 @@ kda_status kda_gated_norm_backward(const void *dout, const void *o, const void *
  *   codes   [rows, H, d] int8;  scale [rows, H] FP32.
  * kda_checkpoint writes codes and scale, kda_checkpoint_load writes
  * out = code x scale. kda_gated_norm_checkpoint is kda_gated_norm (the same bits)
- * that also writes the checkpoints of o and z.
+ * that also writes the checkpoints of o and z; its out must not be o.
  * head_dim 64 or 128, rows x H < 2^28 (with 128 channels at most 2^28 - 16), else
  * KDA_ERR_UNSUPPORTED.
  */

@@ -302,7 +302,7 @@ def checkpoint_load(codes, scale, dtype=torch.bfloat16, stream=None):
 
 def kda_gated_norm_checkpoint(o, z, norm_w, out, o_codes, o_scale, z_codes, z_scale,
                               eps_norm=1e-6, stream=None) -> None:
-    """kda_gated_norm that also writes the checkpoints of o and z."""
+    """kda_gated_norm that also writes the checkpoints of o and z (out must not be o)."""
     s = _place(stream, (o, z, norm_w, out, o_codes, o_scale, z_codes, z_scale))
     rows, H, d = _vectors(o)
     shape = o.shape
