@@ -239,11 +239,6 @@ kda_status conv_backward(const void *dq, const void *dk, const void *dv, kda_dty
     return launch_conv_grad(p, (int)dtype, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
-kda_status dense_tokens(int64_t B, int64_t T) {
-    if (B < 0 || T < 0) return KDA_ERR_INVALID_ARG;
-    return B > 0 && T > kMaxTokens / B ? KDA_ERR_UNSUPPORTED : KDA_OK;
-}
-
 // --------------------------------------------------------- norm and checkpoints
 
 size_t norm_bytes(int64_t rows, int32_t H, int32_t d) {
@@ -281,7 +276,7 @@ kda_status kda_prefill_backward_dense(
     float *dbeta, int64_t B, int64_t T, int32_t H, int32_t Hk, int32_t K, int32_t V,
     int32_t gate_dim, const float *state, float *dstate, const int32_t *slot, const int32_t *init,
     int64_t num_slots, float scale, void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    const kda_status st = dense_tokens(B, T);
+    const kda_status st = check_dense(B, T);
     if (st != KDA_OK) return st;
     const DeltaGradArgs a = {dout, out_dtype, q, k, v, in_dtype, g, beta, dq, dk, dv, dg, dbeta,
                              H, Hk, K, V, gate_dim, state, dstate, slot, init, num_slots, scale,
@@ -319,7 +314,7 @@ kda_status kda_conv_backward_dense(const void *dq, const void *dk, const void *d
                                    float *dconv_state, const int32_t *slot, const int32_t *init,
                                    int64_t num_slots, float eps_l2, void *workspace,
                                    size_t workspace_bytes, hipStream_t stream) {
-    const kda_status st = dense_tokens(B, T);
+    const kda_status st = check_dense(B, T);
     if (st != KDA_OK) return st;
     return conv_backward(dq, dk, dv, dtype, qkv, qkv_scale, conv_w, dqkv, dconv_w, nullptr, B,
                          B * T, T, H, head_dim, conv_width, conv_state, dconv_state, slot, init,

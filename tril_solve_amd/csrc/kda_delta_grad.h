@@ -57,7 +57,6 @@ namespace kda {
 constexpr int kGC = kGradChunk;
 constexpr int kMatRow = kGC + 4;  // floats between rows of a 64 x 64 matrix in LDS
 constexpr float kGradLog2E = 1.4426950408889634f;
-constexpr float kGradLn2 = 0.6931471805599453f;
 constexpr float kLeastGate = -1024.0f;  // in powers of two; e^-inf and this are 0 alike
 
 // Parts of one chunk-head's workspace.
