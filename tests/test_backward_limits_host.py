@@ -71,3 +71,22 @@ def test_vectors_up_to_the_launch(kt, H, d):
     for call in (save, load, both, forward):
         assert call(most) == kt.KDA_ERR_INVALID_ARG  # past the sizes, at the null pointer
         assert call(most + 1) == kt.KDA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("H", [1, 3, 64, 4096])
+@pytest.mark.parametrize("K,V", [(64, 32), (128, 256)])
+def test_delta_up_to_the_launch(kt, H, K, V):
+    """(total_tokens / 64 + num_seqs) x H < 2^23, and num_seqs x H x V / 32 < 2^24 - 64
+    (the query's sizes are the call's)."""
+    def takes(tokens, n):
+        try:
+            return kt.kda_prefill_backward_workspace_size(tokens, n, H, H, K, V) > 0
+        except kt.KdaError as e:
+            assert e.status == kt.KDA_ERR_UNSUPPORTED
+            return False
+
+    slots = (2 ** 23 - 1) // H
+    assert takes(64 * (slots - 1) + 63, 1) and not takes(64 * slots, 1)
+    walks = min((2 ** 24 - 65) // (H * (V // 32)), slots)
+    assert takes(63, walks)
+    assert not takes(63, 2 ** 21 // H + 1 if V == 256 else slots + 1)
