@@ -40,7 +40,7 @@
 // What bounds it (16 x 512 tokens of 64 heads, K = V = 128, bf16: 3.02 ms, 0.69 +
 // 1.18 + 1.28 in the three kernels under a trace; one sequence of 16,384 tokens and
 // 32 heads 3.00 ms, 0.69 + 1.18 + 1.26): the traffic of the workspace (9.9 GB a call,
-// 3.5, 3.3 and 2.8 TB/s of a copy's 5.1) and the chains between barriers, which the
+// 3.5, 3.3 and 2.8 TB/s of a tuned copy's 6.4) and the chains between barriers, which the
 // few wavefronts that their registers and LDS leave room for do not cover (two to a
 // SIMD). The matrix pipes are busy for 34, 52 and 26% of the cycles, the vector
 // units for 34, 10 and 35%.
@@ -874,7 +874,10 @@ __device__ __forceinline__ Operand grad_operand(Rsrc r, uint32_t off) {
 // the operands of E taken as they lie); from 4 on a level is one product of
 // masked tiles. ONE: all value columns at once (up to 128; with a loop over them the
 // sums take registers from what is loaded ahead). With K = 64 and up to 64 columns
-// two workgroups of four wavefronts share a unit (8,161 tokens of 8 heads, f32: 124 -> 88 us).
+// two workgroups of four wavefronts share a unit (8,161 tokens of 8 heads, f32: 124 -> 88
+// us). Two wavefronts to a SIMD leave 256 registers, which are not quite enough: 24 bytes
+// a lane go through scratch with K = 128, 76 to 92 with a loop over the columns, 8 with
+// K = 64 and up to 64 columns; K = 64 with more has one wavefront to a SIMD, and none.
 template <class E, class EO, int K, int VB, bool ONE>
 __global__ __launch_bounds__(K * 4, K == 128 || VB == 64 ? 2 : 1) void kda_grad_chunk_kernel(
     DeltaGradProblem p) {
@@ -1540,7 +1543,12 @@ hipError_t launch_delta_grad_with(const DeltaGradProblem &p, hipStream_t stream)
     const long walks = (long)p.req.num_seqs * p.H, groups = (walks + 7) / 8;
     // 32 columns to a workgroup halve what the operands cost in L2, 16 columns the
     // work of a step: one sequence of 4,096 tokens takes 170 us in 16 and 243 in
-    // 32 with 8 heads (128 and 64 workgroups), 411 and 294 with 32 heads.
+    // 32 with 8 heads (128 and 64 workgroups), 411 and 294 with 32 heads. With K = 64
+    // the rule holds, too (the whole call, 4,096 tokens, V = 64: 8 heads 150 and 209, 32
+    // heads 348 and 390, 64 heads 685 and 642; V = 128: 16 heads 273 and 327, 32 heads
+    // 578 and 535), but not for every set of requests (8,161 tokens in 20, 8 heads, f32
+    // 218 and the 232 of this rule: there four workgroups of 16 columns share a unit, two
+    // of 32).
     if (2 * walks * (p.V / 16) > device_cus()) {
         const int parts = p.V / 32;
         hipLaunchKernelGGL((kda_grad_walk_kernel<EO, K, 2>), dim3((unsigned)(groups * 8 * parts), 2),

@@ -176,10 +176,16 @@ inline int64_t conv_grad_rows(int64_t tokens, int32_t seg) {
     return (tokens + 4 * (int64_t)seg - 1) / (4 * (int64_t)seg);
 }
 // Tokens per wavefront: up to 64 (every segment takes W - 1 rows twice at both
-// ends: 8,192 tokens of 64 heads 363 us with 16, 325 with 32, 287 with 64), fewer
-// while a compute unit would have less than 12 wavefronts (7,000 tokens of 9 heads
-// of 64: 48 us with 64, 36 with 32), more where the rows of dconv_w would outgrow
-// the tensors (from 32,768 tokens on 128 rows).
+// ends: 8,192 tokens of 64 heads, bf16 308 us with 16, 263 with 32, 248 with 64, 249
+// with 128, 256 with 256; from 8-bit codes 311, 261, 242, 239, 236), fewer while a
+// compute unit would have less than 12 wavefronts (2,048 tokens of 16 heads 24 us with
+// the 16 of this rule, 27 with 32, 35 with 64; 512 tokens of 64 heads 23, 28 with 32).
+// With rows of two and a half wavefronts a part of their lanes idles, and it divides
+// too far: 7,000 tokens of 9 heads of 64, f32, 49 us with its 16, 42 with 32, 43 with
+// 64. Past 32,768 tokens always 512 segments, so that the workspace stays as it is
+// however long the call: 131,072 tokens of 4 heads 283 us with its 256 or with 64,
+// 65,536 of 16 heads 536 with 128, 511 with 64, 65,536 of one head of 64 channels 79
+// and 85, 40,000 of two 57 with 79, 50 with 64.
 inline int32_t conv_grad_segment(int64_t tokens, int32_t H, int32_t d) {
     if (tokens > 32768) return (int32_t)((tokens + 511) / 512);
     const int64_t per_segment = ((int64_t)H * d + 255) / 256 * 3;
